@@ -53,7 +53,8 @@ typedef enum {
 
 typedef enum { FM_MEL_HTK = 0, FM_MEL_SLANEY = 1 } fm_mel_scale;
 typedef enum { FM_NORM_NONE = 0, FM_NORM_SLANEY = 1 } fm_norm;
-typedef enum { FM_F32 = 0, FM_I16 = 1, FM_F16 = 2 } fm_dtype;
+/* FM_BF16: the operators of fm_ops.h only */
+typedef enum { FM_F32 = 0, FM_I16 = 1, FM_F16 = 2, FM_BF16 = 3 } fm_dtype;
 /* torch's pad modes for the centre padding: mirror without repeating the
  * edge sample, zeros, repeat the edge sample, wrap around the signal */
 typedef enum { FM_PAD_REFLECT = 0, FM_PAD_CONSTANT = 1, FM_PAD_REPLICATE = 2, FM_PAD_CIRCULAR = 3 } fm_pad_mode;

@@ -28,3 +28,15 @@ from ._binding import (  # noqa: F401
     status_string,
 )
 from .transform import MelSpectrogram  # noqa: F401
+
+
+def __getattr__(name):
+    # the frame-encoder operators need torch; the mel binding above does not
+    if name in ("attention", "bucket_map", "layer_norm", "ops", "relative_bias"):
+        import importlib
+
+        ops = importlib.import_module(".ops", __name__)
+        globals().update(ops=ops, attention=ops.attention, bucket_map=ops.bucket_map, layer_norm=ops.layer_norm,
+                         relative_bias=ops.relative_bias)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -19,7 +19,7 @@ CHECK_LIB_PATH = os.path.join(_HERE, "libfm_mel_check.so")
 FM_OK, FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_CUDA, FM_ERR_OOM, FM_ERR_KERNEL_TIMEOUT, FM_ERR_BOUNDS = range(7)
 FM_MEL_HTK, FM_MEL_SLANEY = 0, 1
 FM_NORM_NONE, FM_NORM_SLANEY = 0, 1
-FM_F32, FM_I16, FM_F16 = 0, 1, 2
+FM_F32, FM_I16, FM_F16, FM_BF16 = 0, 1, 2, 3  # FM_BF16: ops.py only
 FM_PAD_REFLECT, FM_PAD_CONSTANT, FM_PAD_REPLICATE, FM_PAD_CIRCULAR = 0, 1, 2, 3
 FM_NORMALIZED_NONE, FM_NORMALIZED_WINDOW, FM_NORMALIZED_FRAME_LENGTH = 0, 1, 2
 

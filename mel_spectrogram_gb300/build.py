@@ -36,8 +36,11 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libfm_mel.so")
 
 
-def _sources() -> list[str]:
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+def _sources(build_dir: str = BUILD) -> list[str]:
+    found = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+    if build_dir == BUILD_CHECK:  # the frame-encoder operators have no index-checked build
+        found = [f for f in found if not os.path.basename(f).startswith("fm_ops_")]
+    return found
 
 
 def _headers() -> list[str]:
@@ -82,7 +85,7 @@ def build_many(checks: list[bool], verbose: bool = False, extra: list[str] | Non
     todo = []
     for bdir, _, flags in targets:
         os.makedirs(bdir, exist_ok=True)
-        todo += [(s, flags, bdir) for s in _sources() if extra or _stale(_obj(s, bdir), [s, *hdrs, __file__])]
+        todo += [(s, flags, bdir) for s in _sources(bdir) if extra or _stale(_obj(s, bdir), [s, *hdrs, __file__])]
     if todo:
         n = jobs or min(len(todo), max(1, os.cpu_count() or 1))
         with cf.ThreadPoolExecutor(n) as ex:
@@ -90,7 +93,7 @@ def build_many(checks: list[bool], verbose: bool = False, extra: list[str] | Non
                 if verbose and log.strip():
                     print(f"[{os.path.basename(src)}]\n{log}", file=sys.stderr)
     for bdir, lib, _ in targets:
-        objs = [_obj(s, bdir) for s in _sources()]
+        objs = [_obj(s, bdir) for s in _sources(bdir)]
         if any(t[2] == bdir for t in todo) or _stale(lib, objs):
             tmp = lib + ".tmp"
             cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]

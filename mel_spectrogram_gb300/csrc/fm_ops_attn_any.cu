@@ -1,0 +1,427 @@
+// Attention on the FP32 pipes, for what the tensor cores cannot take: 32-bit
+// inputs (their products are exact to 32 bits here), head sizes and strides
+// that do not fit 16-byte tiles. Forward: a running maximum and sum over key
+// tiles of 64. Backward: one kernel per owner (a tile of keys sums dk and dv
+// over the queries and the heads that share it, a tile of queries sums dq and
+// the bias), each recomputing the scores, so that every sum has one owner and
+// one order. Bound by the FP32 pipes' shared-memory operands: 4 x 4 products
+// per thread and step.
+#include "fm_ops_attn.cuh"
+
+#include <cmath>
+
+namespace fm {
+namespace {
+
+constexpr int kRows = kAnyTile;  // rows a block owns
+constexpr int kThreads = 256;
+
+// Floats between rows of a staged tile: padded to whole float4, an odd number
+// of them, so that float4 reads down a column of rows hit distinct banks.
+__host__ __device__ inline int pitch_of(int dim) {
+  const int d4 = (dim + 3) / 4;
+  return 4 * (d4 | 1);
+}
+
+template <typename T>
+__device__ __forceinline__ void stage(float* to, const T* from, long long stride, int n, int rows, int dim, int pitch,
+                                      const int32_t* docs) {
+  // rows at or past n, and padding frames, arrive as zeros whatever memory holds
+  for (int e = threadIdx.x; e < rows * pitch; e += kThreads) {
+    const int r = e / pitch, d = e - r * pitch;
+    float v = 0.f;
+    if (r < n && d < dim && (docs == nullptr || docs[r] >= 0)) v = to_f(from[r * stride + d]);
+    to[e] = v;
+  }
+}
+
+struct Score {
+  float z;      // the biased score, or -inf where unseen
+  float slope;  // d(capped)/d(scaled): 1 - tanh^2
+  bool seen;
+};
+
+template <typename T>
+struct ScoreOf {
+  const AttnParams& p;
+  RowInfo r;
+  int h;
+  float slope_h;
+  const int32_t *qd, *kd;
+  __device__ ScoreOf(const AttnParams& p_, int b, int h_) : p(p_), r(row_info(p_, b)), h(h_) {
+    slope_h = p.slopes ? p.slopes[h] : 0.f;
+    qd = p.q_docs ? p.q_docs + (long long)b * p.q_len : nullptr;
+    kd = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
+  }
+  __device__ __forceinline__ Score operator()(float dot, int i, int j) const {
+    Score s;
+    s.seen = i < p.q_len && j < r.len;
+    s.slope = 1.f;
+    s.z = dot * p.scale;
+    if (!s.seen) {
+      s.z = -INFINITY;
+      return s;
+    }
+    if (p.cap > 0.f) {
+      const float t = tanhf(s.z / p.cap);
+      s.slope = 1.f - t * t;
+      s.z = p.cap * t;
+    }
+    const int o = j - (r.start + i);
+    if (p.map) {
+      const int D = p.max_distance, c = o < -D ? -D : o > D ? D : o;
+      const long long at = (long long)p.map[c + D] * p.heads + h;
+      s.z += p.table_f32 ? ((const float*)p.table)[at] : to_f(((const T*)p.table)[at]);
+    }
+    if (p.slopes) s.z -= slope_h * fabsf((float)o);
+    if (p.causal && o > 0 && j >= r.prefix) s.seen = false;
+    if (qd) {
+      const int d = qd[i];
+      if (d < 0 || d != kd[j]) s.seen = false;
+    }
+    if (!s.seen) s.z = -INFINITY;
+    return s;
+  }
+};
+
+__device__ __forceinline__ float half_max(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float half_sum(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// s[r][c] = A row (ty*4 + r) . B row (tx + 16 c)
+template <int C>
+__device__ __forceinline__ void products(const float* A, const float* B, int dim, int pitch, int tx, int ty,
+                                         float (&s)[4][C]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[r][c] = 0.f;
+  const int d4 = (dim + 3) / 4;
+  for (int d = 0; d < d4; ++d) {
+    float4 a[4], b[C];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) a[r] = *(const float4*)(A + (ty * 4 + r) * pitch + 4 * d);
+#pragma unroll
+    for (int c = 0; c < C; ++c) b[c] = *(const float4*)(B + (tx + 16 * c) * pitch + 4 * d);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        s[r][c] = fmaf(a[r].x, b[c].x, s[r][c]);
+        s[r][c] = fmaf(a[r].y, b[c].y, s[r][c]);
+        s[r][c] = fmaf(a[r].z, b[c].z, s[r][c]);
+        s[r][c] = fmaf(a[r].w, b[c].w, s[r][c]);
+      }
+  }
+}
+
+// acc[r][g] += sum_j W[(ty*4 + r)][j] * V[j][4 tx + 64 g ..]
+template <int G>
+__device__ __forceinline__ void accumulate(float4 (&acc)[4][G], const float* W, int wpitch, const float* V, int n,
+                                           int dim, int pitch, int tx, int ty) {
+  for (int j = 0; j < n; ++j) {
+    float w[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) w[r] = W[(ty * 4 + r) * wpitch + j];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int d = 4 * tx + 64 * g;
+      if (d >= dim) continue;
+      const float4 v = *(const float4*)(V + j * pitch + d);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[r][g].x = fmaf(w[r], v.x, acc[r][g].x);
+        acc[r][g].y = fmaf(w[r], v.y, acc[r][g].y);
+        acc[r][g].z = fmaf(w[r], v.z, acc[r][g].z);
+        acc[r][g].w = fmaf(w[r], v.w, acc[r][g].w);
+      }
+    }
+  }
+}
+template <int G>
+__device__ __forceinline__ void clear(float4 (&acc)[4][G]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int g = 0; g < G; ++g) acc[r][g] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+template <typename T, int G>
+__device__ __forceinline__ void put(T* to, long long stride, int n, int dim, const float4 (&acc)[4][G],
+                                    const float (&f)[4], int tx, int ty) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = ty * 4 + r;
+    if (row >= n) continue;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int d = 4 * tx + 64 * g;
+      const float v[4] = {acc[r][g].x, acc[r][g].y, acc[r][g].z, acc[r][g].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (d + k < dim) to[row * stride + d + k] = from_f<T>(v[k] * f[r]);
+    }
+  }
+}
+
+constexpr int kFwdKeys = 64;
+
+template <typename T, int G>
+__global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
+  extern __shared__ float sm[];
+  const int pitch = pitch_of(p.dim);
+  float *Q = sm, *K = Q + kRows * pitch, *V = K + kFwdKeys * pitch, *P = V + kFwdKeys * pitch;
+  constexpr int wp = kFwdKeys + 4;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int i0 = blockIdx.x * kRows, h = blockIdx.y, b = blockIdx.z, hk = h / p.group;
+  const ScoreOf<T> score(p, b, h);
+  const T* q = (const T*)p.q + b * p.qs.b + i0 * p.qs.t + h * p.qs.h;
+  const T* k = (const T*)p.k + b * p.ks.b + hk * p.ks.h;
+  const T* v = (const T*)p.v + b * p.vs.b + hk * p.vs.h;
+  const int nq = min(kRows, p.q_len - i0);
+  stage(Q, q, p.qs.t, nq, kRows, p.dim, pitch, score.qd ? score.qd + i0 : nullptr);
+  float4 acc[4][G];
+  clear(acc);
+  float m[4], l[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.f;
+  int end = score.r.len;
+  if (p.causal) end = min(end, max(score.r.start + i0 + nq, score.r.prefix));
+  for (int j0 = 0; j0 < end; j0 += kFwdKeys) {
+    const int n = min(kFwdKeys, score.r.len - j0);
+    __syncthreads();
+    stage(K, k + j0 * p.ks.t, p.ks.t, n, kFwdKeys, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
+    stage(V, v + j0 * p.vs.t, p.vs.t, n, kFwdKeys, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
+    __syncthreads();
+    float s[4][4];
+    products<4>(Q, K, p.dim, pitch, tx, ty, s);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float top = m[r];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        s[r][c] = score(s[r][c], i0 + ty * 4 + r, j0 + tx + 16 * c).z;
+        top = fmaxf(top, s[r][c]);
+      }
+      top = half_max(top);
+      const float base = top == -INFINITY ? 0.f : top;  // nothing seen yet: exp(-inf - 0) = 0
+      const float f = expf(m[r] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float e = expf(s[r][c] - base);
+        sum += e;
+        P[(ty * 4 + r) * wp + tx + 16 * c] = e;
+      }
+      l[r] = l[r] * f + half_sum(sum);
+      m[r] = top;
+#pragma unroll
+      for (int g = 0; g < G; ++g) acc[r][g].x *= f, acc[r][g].y *= f, acc[r][g].z *= f, acc[r][g].w *= f;
+    }
+    __syncwarp();  // a row's weights come from the 16 lanes of its half warp
+    accumulate<G>(acc, P, wp, V, n, p.dim, pitch, tx, ty);
+  }
+  float f[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f[r] = l[r] == 0.f ? 0.f : 1.f / l[r];
+    const int i = i0 + ty * 4 + r;
+    if (p.lse && tx == 0 && i < p.q_len)
+      p.lse[((long long)b * p.heads + h) * p.q_len + i] = l[r] == 0.f ? -INFINITY : m[r] + logf(l[r]);
+  }
+  put((T*)p.out + b * p.os.b + i0 * p.os.t + h * p.os.h, p.os.t, nq, p.dim, acc, f, tx, ty);
+}
+
+constexpr int kBwdCols = 32;  // rows of the streamed tile
+
+// OF_KEYS: the block owns keys and streams queries (dk, dv); otherwise it
+// owns queries and streams keys (dq and the bias).
+template <typename T, int G, bool OF_KEYS>
+__global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
+  extern __shared__ float sm[];
+  const int pitch = pitch_of(p.dim);
+  float *R1 = sm, *R2 = R1 + kRows * pitch;              // owned: (K, V) or (Q, dout)
+  float *C1 = R2 + kRows * pitch, *C2 = C1 + kBwdCols * pitch;  // streamed: (Q, dout) or (K, V)
+  float *W1 = C2 + kBwdCols * pitch, *W2 = W1 + kRows * (kBwdCols + 4);
+  constexpr int wp = kBwdCols + 4;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int r0 = blockIdx.x * kRows, b = blockIdx.z;
+  const int hk = OF_KEYS ? blockIdx.y : blockIdx.y / p.group;
+  const int h0 = OF_KEYS ? hk * p.group : blockIdx.y, h1 = OF_KEYS ? h0 + p.group : h0 + 1;
+  const T* k = (const T*)p.k + b * p.ks.b + hk * p.ks.h;
+  const T* v = (const T*)p.v + b * p.vs.b + hk * p.vs.h;
+  const RowInfo info = row_info(p, b);
+  const int32_t* kd = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
+  const int32_t* qd = p.q_docs ? p.q_docs + (long long)b * p.q_len : nullptr;
+  const int owned = min(kRows, (OF_KEYS ? p.k_len : p.q_len) - r0);
+  if (OF_KEYS) {
+    const int n = min(owned, info.len - r0);
+    stage(R1, k + r0 * p.ks.t, p.ks.t, n, kRows, p.dim, pitch, kd ? kd + r0 : nullptr);
+    stage(R2, v + r0 * p.vs.t, p.vs.t, n, kRows, p.dim, pitch, kd ? kd + r0 : nullptr);
+  }
+  float4 a1[4][G], a2[4][G];
+  clear(a1);
+  clear(a2);
+  float* part = nullptr;
+  const int D = p.max_distance;
+  if (!OF_KEYS && p.part) {
+    part = p.part + (((long long)b * p.q_tiles + blockIdx.x) * p.heads + h0) * (2 * D + 1);
+    for (int i = threadIdx.x; i <= 2 * D; i += kThreads) part[i] = 0.f;
+  }
+  for (int h = h0; h < h1; ++h) {
+    const ScoreOf<T> score(p, b, h);
+    const T* q = (const T*)p.q + b * p.qs.b + h * p.qs.h;
+    const T* g = (const T*)p.dout + b * p.dos.b + h * p.dos.h;
+    const float* lse = p.lse + ((long long)b * p.heads + h) * p.q_len;
+    const float* delta = p.delta + ((long long)b * p.heads + h) * p.q_len;
+    if (!OF_KEYS) {
+      stage(R1, q + r0 * p.qs.t, p.qs.t, owned, kRows, p.dim, pitch, qd ? qd + r0 : nullptr);
+      stage(R2, g + r0 * p.dos.t, p.dos.t, owned, kRows, p.dim, pitch, qd ? qd + r0 : nullptr);
+    }
+    int begin = 0, end = OF_KEYS ? p.q_len : info.len;
+    if (p.causal && !OF_KEYS) end = min(end, max(info.start + r0 + owned, info.prefix));
+    if (OF_KEYS && r0 >= info.len) end = 0;
+    for (int c0 = begin; c0 < end; c0 += kBwdCols) {
+      const int n = min(kBwdCols, end - c0);
+      __syncthreads();
+      if (OF_KEYS) {
+        stage(C1, q + c0 * p.qs.t, p.qs.t, n, kBwdCols, p.dim, pitch, qd ? qd + c0 : nullptr);
+        stage(C2, g + c0 * p.dos.t, p.dos.t, n, kBwdCols, p.dim, pitch, qd ? qd + c0 : nullptr);
+      } else {
+        stage(C1, k + c0 * p.ks.t, p.ks.t, n, kBwdCols, p.dim, pitch, kd ? kd + c0 : nullptr);
+        stage(C2, v + c0 * p.vs.t, p.vs.t, n, kBwdCols, p.dim, pitch, kd ? kd + c0 : nullptr);
+      }
+      __syncthreads();
+      float s[4][2], dp[4][2];
+      products<2>(R1, C1, p.dim, pitch, tx, ty, s);
+      products<2>(R2, C2, p.dim, pitch, tx, ty, dp);
+      float bias_grad[4][2];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = r0 + ty * 4 + r, col = c0 + tx + 16 * c;
+          const int i = OF_KEYS ? col : row, j = OF_KEYS ? row : col;
+          const Score z = score(s[r][c], i, j);
+          float w = 0.f, d = 0.f;
+          if (z.seen) {
+            w = expf(z.z - lse[i]);
+            d = w * (dp[r][c] - delta[i]);
+          }
+          bias_grad[r][c] = d;
+          W1[(ty * 4 + r) * wp + tx + 16 * c] = w;
+          W2[(ty * 4 + r) * wp + tx + 16 * c] = d * z.slope;
+        }
+      __syncwarp();
+      if (OF_KEYS) accumulate<G>(a1, W1, wp, C2, n, p.dim, pitch, tx, ty);  // dv
+      accumulate<G>(a2, W2, wp, C1, n, p.dim, pitch, tx, ty);               // dk or dq
+      if (part) {
+        // the tile's diagonals, one thread each; the clamped ends one each
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) W1[(ty * 4 + r) * wp + tx + 16 * c] = bias_grad[r][c];
+        __syncthreads();
+        constexpr int kDiag = kRows + kBwdCols - 1;
+        const int base = c0 - (info.start + r0) - (kRows - 1);  // offset of diagonal 0
+        const int t = threadIdx.x;
+        float sum = 0.f;
+        if (t < kDiag) {
+          for (int i = 0; i < kRows; ++i) {
+            const int j = t - (kRows - 1) + i;
+            if (j >= 0 && j < kBwdCols) sum += W1[i * wp + j];
+          }
+        }
+        __syncthreads();
+        if (t < kDiag) W2[t] = sum;
+        __syncthreads();
+        if (t < kDiag && base + t > -D && base + t < D) {
+          part[base + t + D] += sum;
+        } else if (t == kDiag || t == kDiag + 1) {
+          float far = 0.f;
+          for (int e = 0; e < kDiag; ++e)
+            if (t == kDiag ? base + e <= -D : base + e >= D) far += W2[e];
+          part[t == kDiag ? 0 : 2 * D] += far;
+        }
+      }
+    }
+  }
+  const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {p.scale, p.scale, p.scale, p.scale};
+  if (OF_KEYS) {
+    put((T*)p.dv + b * p.dvs.b + r0 * p.dvs.t + hk * p.dvs.h, p.dvs.t, owned, p.dim, a1, one, tx, ty);
+    put((T*)p.dk + b * p.dks.b + r0 * p.dks.t + hk * p.dks.h, p.dks.t, owned, p.dim, a2, sc, tx, ty);
+  } else {
+    put((T*)p.dq + b * p.dqs.b + r0 * p.dqs.t + h0 * p.dqs.h, p.dqs.t, owned, p.dim, a2, sc, tx, ty);
+  }
+}
+
+// delta[b][h][i] = dout . out, a warp per row; 0 for padding frames, whose
+// dout may hold anything
+template <typename T>
+__global__ void __launch_bounds__(256) any_delta(const AttnParams p) {
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long rows = (long long)p.batch * p.heads * p.q_len;
+  if (row >= rows) return;
+  const int i = (int)(row % p.q_len), h = (int)(row / p.q_len % p.heads), b = (int)(row / p.q_len / p.heads);
+  const T* g = (const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h;
+  const T* o = (const T*)p.out_in + b * p.os.b + i * p.os.t + h * p.os.h;
+  float s = 0.f;
+  if (p.q_docs == nullptr || p.q_docs[(long long)b * p.q_len + i] >= 0)
+    for (int d = threadIdx.x & 31; d < p.dim; d += 32) s = fmaf(to_f(g[d]), to_f(o[d]), s);
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) p.delta[row] = s;
+}
+
+size_t fwd_smem(int dim) {
+  return sizeof(float) * ((size_t)(kRows + 2 * kFwdKeys) * pitch_of(dim) + kRows * (kFwdKeys + 4));
+}
+size_t bwd_smem(int dim) {
+  return sizeof(float) * ((size_t)(2 * kRows + 2 * kBwdCols) * pitch_of(dim) + 2 * kRows * (kBwdCols + 4));
+}
+
+template <typename T, int G>
+fm_status fwd(const AttnParams& p, cudaStream_t st) {
+  const dim3 grid((p.q_len + kRows - 1) / kRows, p.heads, p.batch);
+  const size_t smem = fwd_smem(p.dim);
+  if (!allow_smem(any_fwd<T, G>, smem)) return FM_ERR_CUDA;
+  any_fwd<T, G><<<grid, kThreads, smem, st>>>(p);
+  return launch_status();
+}
+template <typename T, int G>
+fm_status bwd(const AttnParams& p, cudaStream_t st) {
+  const size_t smem = bwd_smem(p.dim);
+  if (!allow_smem(any_bwd<T, G, true>, smem) || !allow_smem(any_bwd<T, G, false>, smem)) return FM_ERR_CUDA;
+  if (p.q_len > 0) {
+    const long long rows = (long long)p.batch * p.heads * p.q_len;
+    any_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
+    any_bwd<T, G, false><<<dim3((p.q_len + kRows - 1) / kRows, p.heads, p.batch), kThreads, smem, st>>>(p);
+  }
+  if (p.k_len > 0)
+    any_bwd<T, G, true><<<dim3((p.k_len + kRows - 1) / kRows, p.kv_heads, p.batch), kThreads, smem, st>>>(p);
+  return launch_status();
+}
+template <typename T>
+fm_status fwd_g(const AttnParams& p, cudaStream_t st) {
+  return p.dim <= 64 ? fwd<T, 1>(p, st) : p.dim <= 128 ? fwd<T, 2>(p, st) : fwd<T, 4>(p, st);
+}
+template <typename T>
+fm_status bwd_g(const AttnParams& p, cudaStream_t st) {
+  return p.dim <= 64 ? bwd<T, 1>(p, st) : p.dim <= 128 ? bwd<T, 2>(p, st) : bwd<T, 4>(p, st);
+}
+}  // namespace
+
+fm_status attn_any_forward(const AttnParams& p, int64_t dtype, cudaStream_t st) {
+  return dtype == FM_F32 ? fwd_g<float>(p, st)
+                         : dtype == FM_F16 ? fwd_g<__half>(p, st) : fwd_g<__nv_bfloat16>(p, st);
+}
+fm_status attn_any_backward(const AttnParams& p, int64_t dtype, cudaStream_t st) {
+  return dtype == FM_F32 ? bwd_g<float>(p, st)
+                         : dtype == FM_F16 ? bwd_g<__half>(p, st) : bwd_g<__nv_bfloat16>(p, st);
+}
+}  // namespace fm

@@ -1,0 +1,356 @@
+// Distance buckets, the dense position bias and its gradient (fm_ops.h).
+#include "fm_ops.cuh"
+
+#include <cmath>
+#include <new>
+#include <vector>
+
+namespace fm {
+
+int num_sms() {
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  if (known[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    known[dev] = n;
+  }
+  return known[dev];
+}
+
+namespace {
+
+// Whole numbers as base-2^32 digits, for the one comparison below.
+using Digits = std::vector<uint32_t>;
+void times(Digits& d, uint32_t f) {
+  uint64_t carry = 0;
+  for (uint32_t& x : d) {
+    carry += (uint64_t)x * f;
+    x = (uint32_t)carry;
+    carry >>= 32;
+  }
+  if (carry) d.push_back((uint32_t)carry);
+}
+int compare(const Digits& a, const Digits& b) {
+  if (a.size() != b.size()) return a.size() < b.size() ? -1 : 1;
+  for (size_t i = a.size(); i-- > 0;)
+    if (a[i] != b[i]) return a[i] < b[i] ? -1 : 1;
+  return 0;
+}
+
+// n^L >= e^(L-m) M^m. Logarithms settle all but the near ties, which are
+// multiplied out.
+bool reaches(int n, int L, int e, int M, int m) {
+  const double left = L * std::log((double)n), right = (L - m) * std::log((double)e) + m * std::log((double)M);
+  if (std::fabs(left - right) > 1e-9 * (1.0 + std::fabs(right))) return left > right;
+  Digits a{1}, b{1};
+  for (int i = 0; i < L; ++i) times(a, (uint32_t)n);
+  for (int i = 0; i < L - m; ++i) times(b, (uint32_t)e);
+  for (int i = 0; i < m; ++i) times(b, (uint32_t)M);
+  return compare(a, b) >= 0;
+}
+
+struct BiasParams {
+  int heads, q_len, k_len, q_start, max_distance;
+  const int32_t* map;
+  const void* table;
+  void* out;
+  const void* dout;
+  float* part;  // [chunks][heads][q_len + k_len - 1]
+  int rows_per_chunk;
+};
+
+constexpr int kFillThreads = 256;
+constexpr int kFillPacks = 8;  // packs of 16 bytes a thread writes
+
+// Write bound. A block writes a flat run of one head's matrix with 16-byte
+// stores; the head's values by offset sit in shared memory, so an element
+// costs one index and one shared read.
+template <typename T>
+__global__ void __launch_bounds__(kFillThreads) bias_fill(const BiasParams p) {
+  extern __shared__ unsigned char raw[];
+  T* val = (T*)raw;  // by clamped offset
+  constexpr int V = 16 / sizeof(T);
+  const int h = blockIdx.y, D = p.max_distance;
+  for (int i = threadIdx.x; i <= 2 * D; i += kFillThreads)
+    val[i] = ((const T*)p.table)[(long long)p.map[i] * p.heads + h];
+  __syncthreads();
+  const long long n = (long long)p.q_len * p.k_len;
+  T* out = (T*)p.out + h * n;
+  // elements before the first 16-byte boundary, at most V - 1, go to block 0
+  const int head = (int)((16 - ((uintptr_t)out & 15)) & 15) / (int)sizeof(T);
+  auto value = [&](int i, int j) {
+    int o = j - i - p.q_start;
+    o = o < -D ? -D : o > D ? D : o;
+    return val[o + D];
+  };
+  const long long run = (long long)kFillThreads * kFillPacks * V;
+  const long long begin = head + blockIdx.x * run;
+  if (blockIdx.x == 0 && threadIdx.x < head && threadIdx.x < n) {
+    const int i = threadIdx.x / p.k_len;
+    out[threadIdx.x] = value(i, threadIdx.x - i * p.k_len);
+  }
+  if (begin >= n) return;
+  const int i0 = (int)(begin / p.k_len), j0 = (int)(begin - (long long)i0 * p.k_len);
+#pragma unroll
+  for (int s = 0; s < kFillPacks; ++s) {
+    const int local = (s * kFillThreads + threadIdx.x) * V;
+    const long long at = begin + local;
+    if (at >= n) continue;
+    const unsigned u = (unsigned)j0 + (unsigned)local;
+    const unsigned r = u / (unsigned)p.k_len;
+    int i = i0 + (int)r, j = (int)(u - r * (unsigned)p.k_len);
+    Pack<T, V> q;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      q.v[k] = value(i, j);
+      if (++j == p.k_len) j = 0, ++i;
+    }
+    if (at + V <= n) {
+      *(Pack<T, V>*)(out + at) = q;
+    } else {
+      for (int k = 0; at + k < n; ++k) out[at + k] = q.v[k];
+    }
+  }
+}
+
+// Read bound. A thread owns an offset and walks down its diagonal over the
+// rows of a chunk, so neighbouring threads read neighbouring elements and a
+// sum stays in one register: no atomics, one fixed order.
+template <typename T>
+__global__ void __launch_bounds__(256) bias_diagonals(const BiasParams p) {
+  const int W = p.q_len + p.k_len - 1;
+  const int o = blockIdx.x * 256 + threadIdx.x;
+  if (o >= W) return;
+  const int h = blockIdx.z, c = o - (p.q_len - 1);  // j - i
+  const int r0 = blockIdx.y * p.rows_per_chunk;
+  int lo = max(r0, -c), hi = min(min(r0 + p.rows_per_chunk, p.q_len), p.k_len - c);
+  const T* x = (const T*)p.dout + (long long)h * p.q_len * p.k_len;
+  float s = 0.f;
+  const long long step = (long long)p.k_len + 1;
+  const T* at = x + (long long)lo * step + c;
+  int i = lo;
+  for (; i + 8 <= hi; i += 8) {
+    T v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = at[k * step];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += to_f(v[k]);
+    at += 8 * step;
+  }
+  for (; i < hi; ++i, at += step) s += to_f(*at);
+  p.part[((long long)blockIdx.y * p.heads + h) * W + o] = s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) bucket_sums(const int32_t* ranges, int max_distance, const float* part,
+                                                   long long rows, long long row_stride, long long head_stride,
+                                                   int first, int count, int heads, T* dtable) {
+  __shared__ float red[8];
+  const int c = blockIdx.x, h = blockIdx.y;
+  int lo = ranges[2 * c], hi = ranges[2 * c + 1];
+  float s = 0.f;
+  if (lo <= hi) {
+    if (lo == -max_distance || lo < first) lo = first;
+    if (hi == max_distance || hi > first + count - 1) hi = first + count - 1;
+    const int n = hi - lo + 1;
+    if (n > 0) {
+      const float* base = part + h * head_stride + (lo - first);
+      const long long total = rows * n;
+#pragma unroll 8
+      for (long long t = threadIdx.x; t < total; t += 256) {
+        const unsigned r = (unsigned)t / (unsigned)n;
+        s += base[r * row_stride + ((unsigned)t - r * (unsigned)n)];
+      }
+    }
+  }
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i];
+    dtable[(long long)c * heads + h] = from_f<T>(s);
+  }
+}
+
+constexpr int kMaxLen = (1 << 29) - 1;
+
+fm_status check(const fm_relative_bias_args* a) {
+  if (a == nullptr || a->buckets == nullptr) return FM_ERR_INVALID_ARG;
+  if (a->heads < 1 || a->heads > 65535 || a->q_len < 0 || a->q_len > kMaxLen || a->k_len < 0 || a->k_len > kMaxLen)
+    return FM_ERR_INVALID_ARG;
+  if (!is_float_type(a->dtype)) return FM_ERR_INVALID_ARG;
+  return FM_OK;
+}
+// Rows of a chunk of bias_diagonals: chunks of 256 rows keep the partial sums
+// below a hundredth of the matrix; few rows get shorter ones for more blocks.
+int chunk_rows(const fm_relative_bias_args* a) { return a->q_len >= 2048 ? 256 : a->q_len >= 256 ? 64 : 16; }
+int chunks_of(const fm_relative_bias_args* a) {
+  const int r = chunk_rows(a);
+  return (int)((a->q_len + r - 1) / r);
+}
+BiasParams params(const fm_relative_bias_args* a) {
+  BiasParams p{};
+  p.heads = (int)a->heads;
+  p.q_len = (int)a->q_len;
+  p.k_len = (int)a->k_len;
+  // beyond 2^30 every offset is past max_distance: the same bias
+  const int64_t far = 1 << 30;
+  p.q_start = (int)(a->q_start > far ? far : a->q_start < -far ? -far : a->q_start);
+  p.max_distance = a->buckets->max_distance;
+  p.map = a->buckets->map;
+  return p;
+}
+bool same_device(const fm_buckets* b) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == b->device;
+}
+}  // namespace
+
+fm_status bucket_sums_launch(const fm_buckets* b, const float* part, long long rows, long long row_stride,
+                             long long head_stride, int first, int count, int heads, void* dtable, int64_t dtype,
+                             cudaStream_t st) {
+  const dim3 grid(b->num_buckets, heads);
+  if (dtype == FM_F32)
+    bucket_sums<float><<<grid, 256, 0, st>>>(b->ranges, b->max_distance, part, rows, row_stride, head_stride, first,
+                                             count, heads, (float*)dtable);
+  else if (dtype == FM_F16)
+    bucket_sums<__half><<<grid, 256, 0, st>>>(b->ranges, b->max_distance, part, rows, row_stride, head_stride, first,
+                                              count, heads, (__half*)dtable);
+  else
+    bucket_sums<__nv_bfloat16><<<grid, 256, 0, st>>>(b->ranges, b->max_distance, part, rows, row_stride, head_stride,
+                                                     first, count, heads, (__nv_bfloat16*)dtable);
+  return launch_status();
+}
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" fm_status fm_buckets_create(fm_buckets** out, int num_buckets, int max_distance, int bidirectional) {
+  if (out == nullptr) return FM_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (num_buckets > 4096 || num_buckets < (bidirectional ? 4 : 2) || (bidirectional && num_buckets % 2))
+    return FM_ERR_INVALID_ARG;
+  const int side = bidirectional ? num_buckets / 2 : num_buckets, e = side / 2, L = side - e;
+  if (max_distance <= e || max_distance > 2048) return FM_ERR_INVALID_ARG;
+  fm_buckets* b = new (std::nothrow) fm_buckets{};
+  const int n_map = 2 * max_distance + 1, n_all = n_map + 2 * num_buckets;
+  int32_t* host = new (std::nothrow) int32_t[n_all];
+  if (b == nullptr || host == nullptr) {
+    delete b;
+    delete[] host;
+    return FM_ERR_OOM;
+  }
+  b->num_buckets = num_buckets;
+  b->max_distance = max_distance;
+  b->bidirectional = bidirectional ? 1 : 0;
+  b->host = host;
+  try {  // the digits' vectors may throw
+    int m = 0;
+    for (int n = 0; n <= max_distance; ++n) {
+      if (n >= e)
+        while (m < L - 1 && reaches(n, L, e, max_distance, m + 1)) ++m;
+      const int c = n < e ? n : e + m;
+      host[max_distance - n] = c;
+      host[max_distance + n] = b->bidirectional ? c + (n > 0 ? side : 0) : 0;
+    }
+  } catch (...) {
+    delete[] host;
+    delete b;
+    return FM_ERR_OOM;
+  }
+  for (int c = 0; c < num_buckets; ++c) host[n_map + 2 * c] = 1, host[n_map + 2 * c + 1] = 0;
+  for (int i = 0; i < n_map; ++i) {
+    int32_t* r = host + n_map + 2 * host[i];
+    if (r[0] > r[1]) r[0] = i - max_distance;
+    r[1] = i - max_distance;
+  }
+  fm_status st = FM_ERR_CUDA;
+  if (cudaGetDevice(&b->device) == cudaSuccess) {
+    const cudaError_t err = cudaMalloc(&b->map, sizeof(int32_t) * n_all);
+    if (err == cudaErrorMemoryAllocation) st = FM_ERR_OOM;
+    if (err == cudaSuccess) {
+      if (cudaMemcpy(b->map, host, sizeof(int32_t) * n_all, cudaMemcpyHostToDevice) == cudaSuccess) st = FM_OK;
+      else cudaFree(b->map);
+    }
+  }
+  if (st != FM_OK) {
+    cudaGetLastError();  // an allocation failure stays out of later calls' status
+    delete[] host;
+    delete b;
+    return st;
+  }
+  b->ranges = b->map + n_map;
+  *out = b;
+  return FM_OK;
+}
+
+extern "C" fm_status fm_buckets_map(const fm_buckets* b, int32_t* map) {
+  if (b == nullptr || map == nullptr) return FM_ERR_INVALID_ARG;
+  for (int i = 0; i <= 2 * b->max_distance; ++i) map[i] = b->host[i];
+  return FM_OK;
+}
+
+extern "C" fm_status fm_buckets_destroy(fm_buckets* b) {
+  if (b == nullptr) return FM_OK;
+  const bool ok = cudaFree(b->map) == cudaSuccess;
+  delete[] b->host;
+  delete b;
+  return ok ? FM_OK : FM_ERR_CUDA;
+}
+
+extern "C" fm_status fm_relative_bias_forward(const fm_relative_bias_args* a, fm_stream_t stream) {
+  if (fm_status s = check(a)) return s;
+  if (a->q_len == 0 || a->k_len == 0) return FM_OK;
+  if (a->table == nullptr || a->out == nullptr || ((uintptr_t)a->out % item_size(a->dtype)) ||
+      !same_device(a->buckets))
+    return FM_ERR_INVALID_ARG;
+  BiasParams p = params(a);
+  p.table = a->table;
+  p.out = a->out;
+  const int64_t item = item_size(a->dtype);
+  const long long run = (long long)kFillThreads * kFillPacks * (16 / item);
+  const long long blocks = ((long long)a->q_len * a->k_len + run - 1) / run;
+  if (blocks > 0x7fffffffLL) return FM_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (unsigned)a->heads);
+  const size_t smem = item * (2 * (size_t)p.max_distance + 1);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (a->dtype == FM_F32) bias_fill<float><<<grid, kFillThreads, smem, st>>>(p);
+  else if (a->dtype == FM_F16) bias_fill<__half><<<grid, kFillThreads, smem, st>>>(p);
+  else bias_fill<__nv_bfloat16><<<grid, kFillThreads, smem, st>>>(p);
+  return launch_status();
+}
+
+extern "C" int64_t fm_relative_bias_workspace(const fm_relative_bias_args* a) {
+  if (check(a) != FM_OK) return -1;
+  return (int64_t)chunks_of(a) * a->heads * (a->q_len + a->k_len) * (int64_t)sizeof(float) + 16;
+}
+
+extern "C" fm_status fm_relative_bias_backward(const fm_relative_bias_args* a, fm_stream_t stream) {
+  if (fm_status s = check(a)) return s;
+  if (a->dtable == nullptr || !same_device(a->buckets)) return FM_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (a->q_len == 0 || a->k_len == 0) {
+    const size_t n = (size_t)a->buckets->num_buckets * a->heads * item_size(a->dtype);
+    return cudaMemsetAsync(a->dtable, 0, n, st) == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+  }
+  if (a->dout == nullptr || a->workspace == nullptr || a->workspace_bytes < fm_relative_bias_workspace(a) ||
+      ((uintptr_t)a->workspace & 15))
+    return FM_ERR_INVALID_ARG;
+  BiasParams p = params(a);
+  p.dout = a->dout;
+  p.part = (float*)a->workspace;
+  p.rows_per_chunk = chunk_rows(a);
+  const int W = p.q_len + p.k_len - 1, chunks = chunks_of(a);
+  if (chunks > 65535) return FM_ERR_UNSUPPORTED;
+  const dim3 grid((W + 255) / 256, chunks, p.heads);
+  if (a->dtype == FM_F32) bias_diagonals<float><<<grid, 256, 0, st>>>(p);
+  else if (a->dtype == FM_F16) bias_diagonals<__half><<<grid, 256, 0, st>>>(p);
+  else bias_diagonals<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
+  if (fm_status s = launch_status()) return s;
+  return bucket_sums_launch(a->buckets, p.part, chunks, (long long)p.heads * W, W, -(p.q_len - 1) - p.q_start, W,
+                            p.heads, a->dtable, a->dtype, st);
+}
