@@ -178,6 +178,12 @@ fm_status fm_attention_backward(const fm_attention_args* args, fm_stream_t strea
  * slopes, dtable). */
 int64_t fm_attention_workspace(const fm_attention_args* args, int backward);
 
+/* Takes and clears the current device's error word of these operators, after
+ * waiting for the work queued on it: FM_ERR_KERNEL_TIMEOUT if a bounded wait
+ * inside an attention kernel gave up (its results are then not valid), FM_OK
+ * otherwise. Not allowed while a graph is being recorded. */
+fm_status fm_ops_poll_error(void);
+
 #ifdef __cplusplus
 }
 #endif

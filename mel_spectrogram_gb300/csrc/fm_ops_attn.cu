@@ -1,6 +1,6 @@
 // C entry points of attention (fm_ops.h): argument checks, workspaces and the
 // choice of kernels.
-#include "fm_ops_attn.cuh"
+#include "fm_ops_attn_tc.cuh"
 
 namespace fm {
 namespace {
@@ -57,20 +57,32 @@ AttnParams params(const fm_attention_args* a) {
   return p;
 }
 
+// Layout of the backward workspace for the kernels of any type; the
+// tensor-core kernels' own (tc_plan) is followed by partial bias gradients too.
 struct Workspace {
   int64_t delta, part, total;
   int q_tiles;
 };
-Workspace backward_layout(const fm_attention_args* a) {
+int64_t part_bytes(const fm_attention_args* a, int q_tiles) {
+  if (a->buckets == nullptr || a->dtable == nullptr) return 0;
+  return align256(sizeof(float) * a->batch * q_tiles * a->heads * (2 * (int64_t)a->buckets->max_distance + 1));
+}
+Workspace any_layout(const fm_attention_args* a) {
   Workspace w{};
   w.q_tiles = (int)((a->q_len + kAnyTile - 1) / kAnyTile);
-  w.delta = 0;
   w.part = align256(sizeof(float) * a->batch * a->heads * a->q_len);
-  w.total = w.part;
-  if (a->buckets && a->dtable)
-    w.total += align256(sizeof(float) * a->batch * w.q_tiles * a->heads * (2 * (int64_t)a->buckets->max_distance + 1));
-  w.total += 256;
+  w.total = w.part + part_bytes(a, w.q_tiles) + 256;
   return w;
+}
+int64_t backward_bytes(const fm_attention_args* a) {
+  int64_t n = any_layout(a).total;
+  if (a->dtype != FM_F32 && a->dim <= 128 && a->dim % 8 == 0) {
+    // whichever kernels the pointers' alignment lets run
+    const TcPlan w = tc_plan(params(a), true);
+    const int64_t tc = w.total + part_bytes(a, w.q_tiles);
+    if (tc > n) n = tc;
+  }
+  return n;
 }
 bool same_device(const fm_buckets* b) {
   int dev = -1;
@@ -83,8 +95,9 @@ using namespace fm;
 
 extern "C" int64_t fm_attention_workspace(const fm_attention_args* a, int backward) {
   if (check(a) != FM_OK) return -1;
-  if (!backward) return 0;
-  return backward_layout(a).total;
+  if (a->batch == 0 || a->q_len == 0) return backward ? backward_bytes(a) : 0;
+  if (!backward) return a->dtype == FM_F32 || a->dim > 128 || a->dim % 8 ? 0 : tc_plan(params(a), false).total;
+  return backward_bytes(a);
 }
 
 extern "C" fm_status fm_attention_forward(const fm_attention_args* a, fm_stream_t stream) {
@@ -95,6 +108,12 @@ extern "C" fm_status fm_attention_forward(const fm_attention_args* a, fm_stream_
   if ((a->buckets && a->table == nullptr) || !same_device(a->buckets)) return FM_ERR_INVALID_ARG;
   AttnParams p = params(a);
   p.out = a->out;
+  if (tc_layout_ok(p, a->dtype, false)) {
+    const TcPlan w = tc_plan(p, false);
+    if (w.total > 0 && (a->workspace == nullptr || a->workspace_bytes < w.total || ((uintptr_t)a->workspace & 15)))
+      return FM_ERR_INVALID_ARG;
+    return attn_tc_forward(p, a->dtype, (char*)a->workspace, (cudaStream_t)stream);
+  }
   return attn_any_forward(p, a->dtype, (cudaStream_t)stream);
 }
 
@@ -113,8 +132,7 @@ extern "C" fm_status fm_attention_backward(const fm_attention_args* a, fm_stream
   if (a->k_len > 0 && (a->k == nullptr || a->v == nullptr || a->dk == nullptr || a->dv == nullptr))
     return FM_ERR_INVALID_ARG;
   if ((a->buckets && a->table == nullptr) || !same_device(a->buckets)) return FM_ERR_INVALID_ARG;
-  const Workspace w = backward_layout(a);
-  if (a->workspace == nullptr || a->workspace_bytes < w.total || ((uintptr_t)a->workspace & 15))
+  if (a->workspace == nullptr || a->workspace_bytes < backward_bytes(a) || ((uintptr_t)a->workspace & 15))
     return FM_ERR_INVALID_ARG;
   AttnParams p = params(a);
   p.out_in = a->out;
@@ -122,11 +140,18 @@ extern "C" fm_status fm_attention_backward(const fm_attention_args* a, fm_stream
   p.dos = strides(a->dout_s);
   p.dq = a->dq, p.dk = a->dk, p.dv = a->dv;
   p.dqs = strides(a->dq_s), p.dks = strides(a->dk_s), p.dvs = strides(a->dv_s);
-  p.delta = (float*)((char*)a->workspace + w.delta);
-  p.q_tiles = w.q_tiles;
   const bool grad = a->buckets && a->dtable;
-  if (grad) p.part = (float*)((char*)a->workspace + w.part);
-  if (fm_status s = attn_any_backward(p, a->dtype, (cudaStream_t)stream)) return s;
+  char* ws = (char*)a->workspace;
+  if (tc_layout_ok(p, a->dtype, true)) {
+    p.q_tiles = tc_plan(p, true).q_tiles;
+    if (fm_status s = attn_tc_backward(p, a->dtype, grad, ws, (cudaStream_t)stream)) return s;
+  } else {
+    const Workspace w = any_layout(a);
+    p.delta = (float*)ws;
+    p.q_tiles = w.q_tiles;
+    if (grad) p.part = (float*)(ws + w.part);
+    if (fm_status s = attn_any_backward(p, a->dtype, (cudaStream_t)stream)) return s;
+  }
   if (!grad) return FM_OK;
   const int W = 2 * p.max_distance + 1;
   return bucket_sums_launch(a->buckets, p.part, (long long)p.batch * p.q_tiles, (long long)p.heads * W, W,

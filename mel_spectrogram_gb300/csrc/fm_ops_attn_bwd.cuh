@@ -1,0 +1,598 @@
+// Attention backward on the fifth-generation tensor cores.
+//
+// Two kernels of one shape, so that every sum has one owner and one order:
+//   KEYS     a block owns 128 keys of one key head and streams the queries of
+//            all heads that share it: dv += P^T dout, dk += dS^T q.
+//   queries  a block owns 128 queries of one head and streams the keys:
+//            dq += dS k, and the bias gradient, sums of dS along diagonals.
+// Both recompute scores and weights P = 2^(z - lse) with dP = dout v^T and
+// dS = P (dP - delta). Seven products instead of the five of a single kernel,
+// but no partial dq in memory and no atomics.
+//
+// An owned row is a lane of tensor memory. Streamed tiles are 64 wide, and
+// two groups of 128 threads take them in turn: each reads its S and dP, and
+// writes P and dS (16 bits) over them, from where the second products take
+// them as their A operand. Warp 8 copies, warp 9 issues products, so one
+// group's arithmetic runs beside the other group's products.
+//
+// Bound: the score products, whose 128 x 64 x 16 steps read 6 KB of shared
+// memory for 32 cycles of arithmetic (the tensor unit takes 128 bytes a cycle).
+#pragma once
+
+#include "fm_ops_attn_tc.cuh"
+
+namespace fm {
+namespace bwd {
+
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr int kCols = 64;      // rows of a streamed tile
+constexpr int kDiagPad = 192;  // room beside the bias gradient for a tile's diagonals
+constexpr int kChains = 4, kChainEntries = 48;
+// f16 operands: P is kept 2^15 larger (weights are at most 1), and dS times a
+// power of two that brings its bound 2 |dout| |v| to 2^14, so that small
+// weights and small gradients stay normal numbers and large ones in range.
+// The products' results are scaled back in 32 bits. bf16 has the range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 15.f;
+
+template <int DP, bool KEYS>
+struct Smem {
+  static constexpr int kBoxes = DP / 64;
+  static constexpr int kOwnBox = kTile * 128;
+  static constexpr int kOwn = kBoxes * kOwnBox;  // one owned operand
+  static constexpr int kBox = kCols * 128;
+  static constexpr int kHalf = kBoxes * kBox;  // one streamed operand
+  static constexpr int kStats = 2 * kHalf;     // lse and delta of the slot's queries
+  static constexpr int kSlot = 2 * kHalf + 1024;
+  static constexpr int kSlots = DP == 64 ? 6 : KEYS ? 4 : 3;
+  static constexpr int kRing = 2 * kOwn;
+  static constexpr int kBars = kRing + kSlots * kSlot;
+  static constexpr int kBias = kBars + 256;
+  // floats, whole 16-byte units: the bias by offset, the bias gradient by offset
+  __host__ __device__ static int bias_floats(int max_distance) { return (2 * (max_distance + kBiasPad) + 4) & ~3; }
+  __host__ __device__ static int diag_floats(int max_distance) { return (2 * (max_distance + kDiagPad) + 4) & ~3; }
+  static size_t bytes(int max_distance, bool bias, bool grad) {
+    size_t n = 1024 + kBias;
+    if (bias) n += sizeof(float) * (KEYS ? 2 : 1) * bias_floats(max_distance);
+    if (grad) n += sizeof(float) * (2 * diag_floats(max_distance) + 8 * kChains * kChainEntries + 512);
+    return n;
+  }
+};
+enum { kFull = 0, kEmpty = 8, kOwnFull = 16, kSFull = 17, kPReady = 19, kDone = 21 };
+
+// a barrier of a group's 128 threads that also tells whether all are well
+__device__ __forceinline__ bool group_ok(int group, bool ok) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((int)ok), "r"(group + 1)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "l"(from), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// What the kernels need beside TcParams.
+struct Extra {
+  const float* lse2;   // [batch * heads][q_pad]: base-2 lse, +inf for rows that see nothing or are not there
+  const float* delta;  // [batch * heads][q_pad]
+  const float* bias;   // [heads][2 * max_distance + 1], base 2
+  int q_pad;           // q_len rounded up to 64
+  // [batch * kv_heads] largest squared norms of a row of dout, then of v (f16)
+  const float* peak;
+};
+// the power of two for dS
+__device__ __forceinline__ float ds_scale(const Extra& x, int at, int count) {
+  const float bound = 0.5f * log2f(x.peak[at]) + 0.5f * log2f(x.peak[count + at]) + 1.f;
+  const float e = floorf(14.f - bound);
+  return fabsf(e) < 120.f ? exp2f(e) : 1.f;  // nothing, infinite or NaN: as it is
+}
+
+template <int DP, bool BF16, int MODE, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t,
+                                                      const __grid_constant__ Extra x) {
+  using L = Smem<DP, KEYS>;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int dead;
+  __shared__ int range[2];
+  const AttnParams& p = t.p;
+  const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
+  unsigned char* mem = raw + (base - smem_u32(raw));
+  auto bar = [&](int n) { return base + L::kBars + 8 * n; };
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const bool has_bias = MODE == 1 || (MODE == 2 && p.map);
+  const int D = p.max_distance, nbias = L::bias_floats(D);
+  const bool grad = !KEYS && p.part != nullptr;
+  // the group's threads meet at barriers: then they also leave together
+  const bool joined = grad || (KEYS && has_bias);
+  float* bias_mem = (float*)(mem + L::kBias);
+  float* diag_mem = bias_mem + (has_bias ? (KEYS ? 2 : 1) * nbias : 0);  // [2][ndiag]
+  const int ndiag = L::diag_floats(D);
+  float* chain_mem = diag_mem + 2 * ndiag;  // [8 warps][kChains][kChainEntries]
+  float* far_mem = chain_mem + 8 * kChains * kChainEntries;  // [2][256]
+
+  const int b = blockIdx.z;
+  const int r0 = (!KEYS && p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * kTile;
+  const int hk = KEYS ? blockIdx.y : blockIdx.y / p.group;
+  const int h0 = KEYS ? hk * p.group : blockIdx.y;
+  const RowInfo info = row_info(p, b);
+  const int owned = min(kTile, (KEYS ? p.k_len : p.q_len) - r0);
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kSlots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
+    bar_init(bar(kOwnFull), 1);
+    for (int w = 0; w < 2; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 4);
+    bar_init(bar(kDone), 1);
+    fence_bar_init();
+    dead = 0;
+    range[0] = 0x7fffffff;
+    range[1] = 0;
+    tma_prefetch(&t.qm);
+    tma_prefetch(&t.km);
+    tma_prefetch(&t.vm);
+    tma_prefetch(&t.gm);
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
+  auto fill = [&](float* to, int h, int at, int step) {
+    for (int i = at; i < nbias; i += step) to[i] = x.bias[(long long)h * (2 * D + 1) + min(max(i - kBiasPad, 0), 2 * D)];
+  };
+  if (has_bias && !KEYS) fill(bias_mem, h0, tid, kThreads);
+  if (grad)
+    for (int i = tid; i < 2 * ndiag; i += kThreads) diag_mem[i] = 0.f;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // the streamed tiles [sb, se), in steps of 64, of each head
+  int sb = 0, se;
+  if (KEYS) {
+    se = r0 < info.len ? (p.q_len + kCols - 1) / kCols : 0;
+    if (p.causal && r0 >= info.prefix) sb = min(se, max(0, r0 - info.start) / kCols);
+  } else {
+    se = (key_end(p, info, r0, owned) + kCols - 1) / kCols;
+  }
+  if (t.k_ranges) {
+    const int4 own = KEYS ? t.k_ranges[b * t.k_tiles + r0 / kTile] : t.q_ranges[b * t.q_tiles + r0 / kTile];
+    const int4* other = KEYS ? t.q_ranges + (long long)b * t.q_tiles : t.k_ranges + (long long)b * t.k_tiles;
+    for (int i = sb / 2 + tid; i < (se + 1) / 2; i += kThreads) {
+      const int4 o = other[i];
+      if (o.x <= own.y && o.y >= own.x) {
+        atomicMin(&range[0], 2 * i);
+        atomicMax(&range[1], 2 * i + 2);
+      }
+    }
+    __syncthreads();
+    sb = max(sb, range[0]);
+    se = min(se, range[1]);
+  }
+  const int per_head = max(se - sb, 0), n = per_head * (KEYS ? p.group : 1);
+
+  constexpr uint32_t kAcc = 256;  // columns: S0 T0 S1 T1 (64 each), dv or nothing, dk or dq
+  if (warp < 8) {
+    take_registers<232>();
+    const int w = warp >> 2, lane_row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t ts = tmem + lanes + w * 128, tt = ts + 64;
+    const int row = r0 + lane_row;  // the key or the query
+    const float c = p.scale * kLog2e;
+    const float sigma = BF16 ? 1.f : ds_scale(x, b * p.kv_heads + hk, p.batch * p.kv_heads);
+    const float tau = BF16 ? 1.f : sigma * exp2f(-kLift<BF16>);
+    const int32_t* kdocs = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
+    const int32_t* qdocs = p.q_docs ? p.q_docs + (long long)b * p.q_len : nullptr;
+    const int32_t* sdocs = KEYS ? qdocs : kdocs;  // of the streamed side
+    int rd = -2;                                   // this row's document; matches none if padding
+    int4 own_range = make_int4(0, 0, 1, 0);
+    if (kdocs) {
+      own_range = KEYS ? t.k_ranges[b * t.k_tiles + r0 / kTile] : t.q_ranges[b * t.q_tiles + r0 / kTile];
+      if (lane_row < owned) {
+        const int d = (KEYS ? kdocs : qdocs)[row];
+        if (d >= 0) rd = d;
+      }
+    }
+    float row_lse = 0.f, row_delta = 0.f;
+    if (!KEYS) {
+      const long long at = ((long long)b * p.heads + h0) * x.q_pad + row;
+      const bool there = row < x.q_pad;
+      row_lse = there ? x.lse2[at] : INFINITY;
+      row_delta = there ? x.delta[at] : 0.f;
+    }
+    float* bias = bias_mem + (KEYS ? w * nbias : 0);
+    float* diag = diag_mem + w * ndiag;
+    float far_lo = 0.f, far_hi = 0.f;
+    int head = -1;
+    bool ok = true;
+    for (int it = w; it < n; it += 2) {
+      const int hh = KEYS ? it / per_head : 0, c0 = (sb + (it - hh * per_head)) * kCols, h = h0 + hh;
+      const int slot = it % L::kSlots;
+      if (KEYS && has_bias && h != head) {
+        // every thread of the group is done with the head before
+        if (!group_ok(w, ok)) break;
+        fill(bias, h, lane_row, 128);
+        if (!group_ok(w, ok)) break;
+      }
+      head = h;
+      const float slope2 = MODE == 2 && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+      // columns [lo, hi) of the tile are seen by length and causality
+      int lo = 0, hi = kCols;
+      bool masked = false, clean = false;
+      if (KEYS) {
+        if (row >= info.len) hi = 0;
+        if (p.causal && row >= info.prefix) lo = row - info.start - c0;
+        masked = r0 + kTile > info.len;
+        if (p.causal && r0 + kTile > info.prefix) masked |= r0 + kTile - 1 - info.start > c0;
+      } else {
+        int end = info.len, all = info.len;
+        if (p.causal) {
+          end = min(end, max(info.start + row + 1, info.prefix));
+          all = min(all, max(info.start + r0 + 1, info.prefix));
+        }
+        hi = end - c0;
+        masked = c0 + kCols > all;
+        clean = c0 + kCols > info.len && info.len < p.k_len;
+      }
+      const int32_t* sd = nullptr;
+      if (kdocs) {
+        const int4 o = KEYS ? t.q_ranges[b * t.q_tiles + c0 / kTile] : t.k_ranges[b * t.k_tiles + c0 / kTile];
+        if (!(o.z && own_range.z && o.x == own_range.x)) sd = sdocs + c0, masked = true;
+        if (!o.z) clean = true;
+      }
+      const int there = (KEYS ? p.q_len : p.k_len) - c0;  // columns that exist
+      const int o0 = KEYS ? row - (info.start + c0) : c0 - (info.start + row);  // offset of column 0
+
+      ok = bar_wait(bar(kSFull + w), (it >> 1) & 1, &dead, t.err);
+      if (joined) {
+        if (!group_ok(w, ok)) break;
+      } else if (!__all_sync(0xffffffffu, ok)) {
+        break;
+      }
+      fence_after();
+      if (clean || KEYS) {
+        ok = bar_wait(bar(kFull + slot), (it / L::kSlots) & 1, &dead, t.err);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;  // a joined group leaves at its next barrier
+          if (!joined) break;
+        }
+      }
+      unsigned char* smem_slot = mem + L::kRing + slot * L::kSlot;
+      if (clean) {
+        // streamed frames that nothing may use become zeros before the second
+        // products read them: q and dout, or k
+        const int r = lane_row & 63;
+        const bool unused = r < there && ((!KEYS && c0 + r >= info.len) || (kdocs && sdocs[c0 + r] < 0));
+        if (unused && (KEYS || lane_row < 64)) {
+          unsigned char* to = smem_slot + (lane_row >> 6) * L::kHalf + r * 128;
+          for (int e = 0; e < L::kBoxes; ++e)
+            for (int f = 0; f < 8; ++f) *(uint4*)(to + e * L::kBox + 16 * f) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async();
+      }
+      const float* lse = (const float*)(smem_slot + L::kStats);
+      const float* delta = lse + kCols;
+
+      float s[64];
+      float slope[MODE == 2 ? 64 : 1];
+      uint32_t* u = (uint32_t*)s;
+      tmem_ld32(ts, u);
+      tmem_ld32(ts + 32, u + 32);
+      wait_ld();
+      tie32(u);
+      tie32(u + 32);
+      float cc = c;
+      if (MODE == 2) {
+        if (p.cap > 0.f) {
+          const float c2 = 2.f * kLog2e * p.scale / p.cap, out = p.cap * kLog2e;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            const float th = tanh_from(s[j] * c2);
+            s[j] = out * th;
+            slope[j] = 1.f - th * th;
+          }
+          cc = 1.f;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) slope[j] = 1.f;
+        }
+      }
+      if (has_bias) {
+        const bool above = KEYS ? o0 - 63 >= D : o0 >= D, below = KEYS ? o0 <= -D : o0 + 63 <= -D;
+        if (above || below) {
+          const float v = bias[above ? 2 * (D + kBiasPad) : 0];
+#pragma unroll
+          for (int j = 0; j < 64; ++j) s[j] = fmaf(s[j], cc, v);
+        } else {
+          const float* at = bias + (o0 + D + kBiasPad);
+#pragma unroll
+          for (int j = 0; j < 64; ++j) s[j] = fmaf(s[j], cc, KEYS ? at[-j] : at[j]);
+        }
+      } else if (MODE == 2) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) s[j] *= cc;
+      }
+      if (MODE == 2 && p.slopes) {
+        const float f0 = (float)o0;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) s[j] = fmaf(-slope2, fabsf(KEYS ? f0 - (float)j : f0 + (float)j), s[j]);
+      }
+      uint64_t seen = ~0ull;  // bit j: column j is seen
+      if (masked) {
+        const int first = max(lo, 0), last = min(hi, min(kCols, there));
+        seen = first < last ? (~0ull >> (64 - (last - first))) << first : 0ull;
+        if (sd) {
+          uint64_t same = 0;
+#pragma unroll 8
+          for (int j = 0; j < 64; ++j) same |= (uint64_t)(j < there && __ldg(sd + j) == rd) << j;
+          seen &= same;
+        }
+      }
+      uint32_t pk[32];
+#pragma unroll
+      for (int j = 0; j < 64; j += 4) {
+        float4 q = make_float4(row_lse, row_lse, row_lse, row_lse);
+        if (KEYS) q = *(const float4*)(lse + j);
+        s[j] = ex2(MODE == 0 ? fmaf(s[j], c, -q.x) : s[j] - q.x);
+        s[j + 1] = ex2(MODE == 0 ? fmaf(s[j + 1], c, -q.y) : s[j + 1] - q.y);
+        s[j + 2] = ex2(MODE == 0 ? fmaf(s[j + 2], c, -q.z) : s[j + 2] - q.z);
+        s[j + 3] = ex2(MODE == 0 ? fmaf(s[j + 3], c, -q.w) : s[j + 3] - q.w);
+      }
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) s[j] = (seen >> j & 1) ? s[j] : 0.f;
+      }
+      if (KEYS) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) pk[j] = pack2<BF16>(s[2 * j], s[2 * j + 1]);
+        tmem_st32(ts, pk);
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t d[32];
+        tmem_ld32(tt + 32 * half, d);
+        wait_ld();
+        tie32(d);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          float4 q = make_float4(row_delta, row_delta, row_delta, row_delta);
+          if (KEYS) q = *(const float4*)(delta + 32 * half + j);
+          float* a = s + 32 * half + j;
+          a[0] *= __uint_as_float(d[j]) - q.x;
+          a[1] *= __uint_as_float(d[j + 1]) - q.y;
+          a[2] *= __uint_as_float(d[j + 2]) - q.z;
+          a[3] *= __uint_as_float(d[j + 3]) - q.w;
+        }
+      }
+      if (masked) {  // 0 times what an unused frame's dP holds
+#pragma unroll
+        for (int j = 0; j < 64; ++j) s[j] = (seen >> j & 1) ? s[j] : 0.f;
+      }
+      // dS goes to the products in the inputs' type; the bias gradient below
+      // sums it in 32 bits
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float a = s[2 * j], z = s[2 * j + 1];
+        if (!BF16) a *= tau, z *= tau;
+        if (MODE == 2) a *= slope[2 * j], z *= slope[2 * j + 1];
+        pk[j] = pack2<BF16>(a, z);
+      }
+      tmem_st32(tt, pk);
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (tid % 32 == 0) bar_arrive(bar(kPReady + w));
+
+      if (grad) {
+        // offsets of the tile: o = (c0 - start - r0) + column - row
+        const int t0 = c0 - info.start - r0;
+        if (t0 - (kTile - 1) >= D || t0 + kCols - 1 <= -D) {
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sum[j & 3] += s[j];
+          const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          if (t0 > 0) far_hi += all;
+          else far_lo += all;
+        } else {
+          // Diagonal sums of the warp's 32 x 64: in four chains of 16 columns,
+          // each step hands a lane's sum to the next row's lane, which adds its
+          // element of the next column. Lane 31 finishes one diagonal a step;
+          // at the end lane r holds that of column 15 - row r.
+          const int lane = tid & 31;
+          float* mine = chain_mem + (warp * kChains) * kChainEntries;
+#pragma unroll
+          for (int g = 0; g < kChains; ++g) {
+            float f[16];
+            f[0] = s[16 * g];
+#pragma unroll
+            for (int k = 1; k < 16; ++k) {
+              const float up = __shfl_up_sync(0xffffffffu, f[k - 1], 1);
+              f[k] = s[16 * g + k] + (lane ? up : 0.f);
+            }
+            float* e = mine + g * kChainEntries;
+            if (lane == 31) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) *(float4*)(e + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+            } else {
+              e[46 - lane] = f[15];
+            }
+          }
+          ok = group_ok(w, ok);
+          // the group's four warps and their chains, diagonal by diagonal
+          for (int d = lane_row; d < kTile + kCols - 1; d += 128) {  // d = column - row + 127
+            float sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int g = 0; g < kChains; ++g) {
+                const int e = d - 96 - 16 * g + 32 * q;
+                if (e >= 0 && e < 47) sum += chain_mem[((w * 4 + q) * kChains + g) * kChainEntries + e];
+              }
+            diag[t0 + d - 127 + D + kDiagPad] += sum;
+          }
+        }
+      }
+    }
+    if (grad) far_mem[tid] = far_lo, far_mem[256 + tid] = far_hi;
+    // ---- results: a group each for dv and dk, or half of dq's columns each
+    if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(bar(kDone), 0, &dead, t.err));
+    if (ok) {
+      fence_after();
+      const bool is_dv = KEYS && w == 0;
+      const Strides st = KEYS ? (is_dv ? p.dvs : p.dks) : p.dqs;
+      uint16_t* out = (uint16_t*)(KEYS ? (is_dv ? p.dv : p.dk) : p.dq) + b * st.b + row * st.t +
+                      (KEYS ? hk : h0) * st.h;
+      const uint32_t from = tmem + lanes + kAcc + (KEYS && is_dv ? 0 : DP);
+      const float f = is_dv ? exp2f(-kLift<BF16>) : p.scale / sigma;
+      const int begin = KEYS ? 0 : w * (DP / 2), end = KEYS ? t.dim16 : min(t.dim16, begin + DP / 2);
+#pragma unroll 1
+      for (int y = begin; y < end; y += 16) {
+        uint32_t o[16];
+        if (n > 0) tmem_ld16(from + y, o);
+        wait_ld();
+        tie16(o);
+        uint32_t r[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          r[e] = n > 0 ? pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
+        if (lane_row < owned) {
+          *(uint4*)(out + y) = make_uint4(r[0], r[1], r[2], r[3]);
+          if (y + 8 < p.dim) *(uint4*)(out + y + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+        }
+      }
+      fence_before();
+    }
+  } else {
+    give_registers<40>();
+    if (warp == 8) {
+      if (tid % 32 == 0 && n > 0) {
+        // ---- copies: the owned tile once, then streamed tiles
+        const uint32_t own = bar(kOwnFull);
+        bar_expect(own, 2 * L::kOwn);
+        for (int y = 0; y < L::kBoxes; ++y)
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t to = base + y * L::kOwnBox + half * (kCols * 128);
+            const int row = r0 + half * kCols;
+            if (KEYS) {
+              tma_load(to, &t.km, own, 64 * y, row, hk * t.k_mh, b * t.k_mb);
+              tma_load(to + L::kOwn, &t.vm, own, 64 * y, row, hk * t.v_mh, b * t.v_mb);
+            } else {
+              tma_load(to, &t.qm, own, 64 * y, row, h0 * t.q_mh, b * t.q_mb);
+              tma_load(to + L::kOwn, &t.gm, own, 64 * y, row, h0 * t.g_mh, b * t.g_mb);
+            }
+          }
+        for (int it = 0; it < n; ++it) {
+          const int s = it % L::kSlots, round = it / L::kSlots;
+          if (!bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err)) break;
+          const uint32_t full = bar(kFull + s), to = base + L::kRing + s * L::kSlot;
+          const int hh = KEYS ? it / per_head : 0, c0 = (sb + (it - hh * per_head)) * kCols, h = h0 + hh;
+          bar_expect(full, 2 * L::kHalf + (KEYS ? 2 * kCols * 4 : 0));
+          for (int y = 0; y < L::kBoxes; ++y) {
+            if (KEYS) {
+              tma_load(to + y * L::kBox, &t.qm, full, 64 * y, c0, h * t.q_mh, b * t.q_mb);
+              tma_load(to + L::kHalf + y * L::kBox, &t.gm, full, 64 * y, c0, h * t.g_mh, b * t.g_mb);
+            } else {
+              tma_load(to + y * L::kBox, &t.km, full, 64 * y, c0, hk * t.k_mh, b * t.k_mb);
+              tma_load(to + L::kHalf + y * L::kBox, &t.vm, full, 64 * y, c0, hk * t.v_mh, b * t.v_mb);
+            }
+          }
+          if (KEYS) {
+            const long long at = ((long long)b * p.heads + h) * x.q_pad + c0;
+            bulk_load(to + L::kStats, x.lse2 + at, kCols * 4, full);
+            bulk_load(to + L::kStats + kCols * 4, x.delta + at, kCols * 4, full);
+          }
+        }
+      }
+    } else if (warp == 9) {
+      if (tid % 32 == 0 && n > 0) {
+        // ---- products
+        const uint32_t id_s = instr_desc(kTile, kCols, BF16, false), id_a = instr_desc(kTile, t.dim16, BF16, true);
+        const int ksteps = t.dim16 / 16;
+        auto slot_at = [&](int it) { return base + L::kRing + (it % L::kSlots) * L::kSlot; };
+        auto full = [&](int it) {
+          return bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err);
+        };
+        auto scores = [&](int it) {
+          const uint32_t d = tmem + (it & 1) * 128, from = slot_at(it);
+          for (int op = 0; op < 2; ++op)
+            for (int k = 0; k < ksteps; ++k)
+              mma_ss(d + op * 64, desc_k(base + op * L::kOwn + (k / 4) * L::kOwnBox + (k % 4) * 32),
+                     desc_k(from + op * L::kHalf + (k / 4) * L::kBox + (k % 4) * 32), id_s, k > 0);
+          mma_commit(bar(kSFull + (it & 1)));
+        };
+        bool ok = bar_wait(bar(kOwnFull), 0, &dead, t.err);
+        for (int it = 0; ok && it < 2 && it < n; ++it) {
+          ok = full(it);
+          if (ok) scores(it);
+        }
+        for (int it = 0; ok && it < n; ++it) {
+          const int w = it & 1;
+          ok = bar_wait(bar(kPReady + w), (it >> 1) & 1, &dead, t.err);
+          if (!ok) break;
+          fence_after();
+          const uint32_t from = slot_at(it);
+          if (KEYS)
+            for (int k = 0; k < kCols / 16; ++k)
+              mma_ts(tmem + kAcc, tmem + w * 128 + k * 8, desc_mn(from + L::kHalf + k * 2048, L::kBox), id_a,
+                     it > 0 || k > 0);
+          for (int k = 0; k < kCols / 16; ++k)
+            mma_ts(tmem + kAcc + DP, tmem + w * 128 + 64 + k * 8, desc_mn(from + k * 2048, L::kBox), id_a,
+                   it > 0 || k > 0);
+          mma_commit(bar(kEmpty + it % L::kSlots));
+          if (it + 2 < n) {
+            // in order of issue: these scores replace P and dS only after the
+            // products above have read them
+            ok = full(it + 2);
+            if (ok) scores(it + 2);
+          }
+        }
+        if (ok) mma_commit(bar(kDone));
+      }
+    }
+  }
+  __syncthreads();
+  if (grad) {
+    // this tile's row of partial bias gradients: the two groups, and at the
+    // ends of the map what lay beyond them
+    float* part = p.part + (((long long)b * t.q_tiles + r0 / kTile) * p.heads + h0) * (2 * D + 1);
+    const float unit = BF16 ? 1.f : exp2f(-kLift<BF16>);
+    auto both = [&](int i) { return (diag_mem[i] + diag_mem[ndiag + i]) * unit; };
+    for (int i = tid + 1; i < 2 * D; i += kThreads) part[i] = both(i + kDiagPad);
+    if (warp < 2) {
+      float s = 0.f;
+      const int lane = tid & 31;
+      for (int i = lane; i < 256; i += 32) s += far_mem[warp * 256 + i] * unit;
+      for (int i = lane; i <= kDiagPad; i += 32) s += both(warp ? 2 * D + kDiagPad + i : i);
+      s = warp_sum(s);
+      if (lane == 0) part[warp ? 2 * D : 0] = s;
+    }
+  }
+  if (dead && tid == 0) {
+    // copies still in flight land in this block's memory: give them time
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <int DP, bool BF16, bool KEYS>
+fm_status launch(const TcParams& t, const Extra& x, int mode, cudaStream_t st) {
+  const int rows = KEYS ? t.p.k_len : t.p.q_len;
+  const dim3 grid((rows + kTile - 1) / kTile, KEYS ? t.p.kv_heads : t.p.heads, t.p.batch);
+  const size_t smem = Smem<DP, KEYS>::bytes(t.p.max_distance, t.p.map != nullptr, !KEYS && t.p.part != nullptr);
+  auto k = mode == 0 ? kernel<DP, BF16, 0, KEYS> : mode == 1 ? kernel<DP, BF16, 1, KEYS> : kernel<DP, BF16, 2, KEYS>;
+  if (!allow_smem(k, smem)) return FM_ERR_CUDA;
+  k<<<grid, kThreads, smem, st>>>(t, x);
+  return launch_status();
+}
+
+}  // namespace bwd
+}  // namespace fm

@@ -1,0 +1,415 @@
+// Attention forward on the fifth-generation tensor cores.
+//
+// A block owns 256 queries of one head, as two tiles of 128, and streams the
+// keys in tiles of 128. Scores S = Q K^T and the output O += P V are tcgen05
+// products with accumulators in tensor memory; one thread per query row reads
+// its scores, keeps the running maximum and sum in registers, and writes its
+// 16-bit weights P back over them, from where the second product takes them.
+// Warps: 0-3 and 4-7 do the softmax of one query tile each, warp 8 copies
+// tiles by TMA into a ring, warp 9 issues products. While one tile's softmax
+// runs, the products of the other do.
+//
+// Bound: for head size 128 a key tile costs two 128 x 128 x 128 products a
+// query tile, 2 x 512 cycles of the tensor unit for both tiles' pairs, and
+// 2 x 16384 exponentials and about five times as many FP32 instructions, which
+// is what holds it below the tensor rate.
+//
+// Rescaling O when the maximum rises is put off until it has risen by 2^8:
+// weights then stay below 2^8, exact in the sense that the same factor divides
+// out of sum and output, and O is touched a few times per row instead of once
+// per tile.
+#pragma once
+
+#include "fm_ops_attn_tc.cuh"
+
+namespace fm {
+namespace fwd {
+
+using namespace tc;
+
+constexpr int kThreads = 384;  // warps 10 and 11 only complete a group of four
+constexpr float kRise = 8.f;
+// f16 weights are kept 2^7 larger, up to 2^15, so that small ones stay normal
+// numbers; the factor divides out with the sum. bf16 has the range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+
+template <int DP>
+struct Smem {
+  static constexpr int kBoxes = DP / 64;
+  static constexpr int kBox = kTile * 128;        // bytes of one 64-column box
+  static constexpr int kOperand = kBoxes * kBox;  // one 128-row tile
+  static constexpr int kSlots = DP == 64 ? 6 : 4;
+  static constexpr int kRing = 2 * kOperand;
+  static constexpr int kBars = kRing + kSlots * kOperand;
+  static constexpr int kBias = kBars + 256;
+  static size_t bytes(int max_distance, bool bias) {
+    return 1024 + kBias + (bias ? sizeof(float) * (2 * (max_distance + kBiasPad) + 1) : 0);
+  }
+};
+enum { kFull = 0, kEmpty = 8, kQFull = 16, kSFull = 17, kPReady = 19, kOFull = 21, kBarCount = 23 };
+
+// One row's scores of a tile, in registers: scaled, capped, biased (base 2).
+template <int MODE, bool MASKED>
+struct RowScores {
+  // s: raw products. o0: offset of column 0. lim: columns below are in length
+  // and causal range; qd / kd: this row's document and the columns'
+  static __device__ __forceinline__ void apply(float (&s)[128], const AttnParams& p, float c, const float* bias,
+                                               float slope2, int o0, int lim, int qd, const int32_t* kd) {
+    if (MODE == 2 && p.cap > 0.f) {
+      const float c2 = 2.f * kLog2e * p.scale / p.cap, out = p.cap * kLog2e;
+#pragma unroll
+      for (int j = 0; j < 128; ++j) s[j] = out * tanh_from(s[j] * c2);
+      c = 1.f;
+    }
+    const int D = p.max_distance;
+    if (MODE == 1 || (MODE == 2 && p.map)) {
+      // o0 differs by at most 127 between a tile's rows: all of a warp's rows
+      // take the same of these unless they stand near an end of the map
+      if (o0 >= D || o0 + 127 <= -D) {
+        const float b = bias[o0 >= D ? 2 * (D + kBiasPad) : 0];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = fmaf(s[j], c, b);
+      } else {
+        const float* at = bias + (o0 + D + kBiasPad);
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = fmaf(s[j], c, at[j]);
+      }
+    } else if (MODE == 2) {
+#pragma unroll
+      for (int j = 0; j < 128; ++j) s[j] *= c;
+    }
+    if (MODE == 2 && p.slopes) {
+      const float f0 = (float)o0;
+#pragma unroll
+      for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope2, fabsf(f0 + (float)j), s[j]);
+    }
+    if (MASKED) {
+#pragma unroll
+      for (int j = 0; j < 128; ++j) s[j] = j < lim ? s[j] : -INFINITY;
+      if (kd) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) {
+          const int d = j < lim ? __ldg(kd + j) : -1;
+          s[j] = d == qd ? s[j] : -INFINITY;
+        }
+      }
+    }
+  }
+};
+
+template <int DP, bool BF16, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t) {
+  using L = Smem<DP>;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int dead;
+  __shared__ int range[2];
+  const AttnParams& p = t.p;
+  const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
+  unsigned char* mem = raw + (base - smem_u32(raw));
+  float* bias = (float*)(mem + L::kBias);
+  auto bar = [&](int n) { return base + L::kBars + 8 * n; };
+  const int tid = threadIdx.x, warp = tid >> 5;
+
+  const int split = blockIdx.z % t.splits, b = blockIdx.z / t.splits, h = blockIdx.y, hk = h / p.group;
+  // causal rows late in the sequence see the most keys: they go first
+  const int q0 = (p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * 2 * kTile;
+  const RowInfo info = row_info(p, b);
+  const int nq = min(2 * kTile, p.q_len - q0);
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kSlots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
+    bar_init(bar(kQFull), 1);
+    for (int w = 0; w < 2; ++w) {
+      bar_init(bar(kSFull + w), 1);
+      bar_init(bar(kPReady + w), 4);
+      bar_init(bar(kOFull + w), 1);
+    }
+    fence_bar_init();
+    dead = 0;
+    range[0] = 0x7fffffff;
+    range[1] = 0;
+    tma_prefetch(&t.qm);
+    tma_prefetch(&t.km);
+    tma_prefetch(&t.vm);
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (MODE == 1 || (MODE == 2 && p.map)) fill_bias<BF16>(p, h, bias, tid, kThreads);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // the key tiles this block visits
+  int tb = split * t.split_tiles, te = (key_end(p, info, q0, nq) + kTile - 1) / kTile;
+  te = min(te, tb + t.split_tiles);
+  if (t.k_ranges) {
+    const int4 a = t.q_ranges[b * t.q_tiles + q0 / kTile];
+    const int4 c = q0 + kTile < p.q_len ? t.q_ranges[b * t.q_tiles + q0 / kTile + 1] : make_int4(0x7fffffff, -1, 0, 0);
+    const int lo = min(a.x, c.x), hi = max(a.y, c.y);
+    for (int i = tb + tid; i < te; i += kThreads) {
+      const int4 k = t.k_ranges[b * t.k_tiles + i];
+      if (k.x <= hi && k.y >= lo) {
+        atomicMin(&range[0], i);
+        atomicMax(&range[1], i + 1);
+      }
+    }
+    __syncthreads();
+    tb = max(tb, range[0]);
+    te = min(te, range[1]);
+  }
+  const int n = max(te - tb, 0);
+
+  constexpr uint32_t kO = 256;  // columns of O0; O1 follows at kO + DP
+  // registers: the block starts with 3 groups x 168; the softmax threads, which
+  // hold 128 scores each, take 232 and leave the others 40 (2 x 232 + 40 = 504)
+  if (warp < 8) {
+    take_registers<232>();
+    // ---- softmax: one query row a thread
+    const int w = warp >> 2, lane_row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 * (warp % 4) in bits 16 up
+    const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + kO + w * DP;
+    const int i = q0 + w * kTile + lane_row, place = info.start + i;
+    const float c = p.scale * kLog2e;
+    const float slope2 = MODE == 2 && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+    int qd = -2;  // matches no document
+    const int32_t* kdocs = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
+    int4 qr = make_int4(0, 0, 1, 0);
+    if (kdocs) {
+      qr = q0 + w * kTile < p.q_len ? t.q_ranges[b * t.q_tiles + q0 / kTile + w] : make_int4(0x7fffffff, -1, 0, 0);
+      if (i < p.q_len) {
+        const int d = p.q_docs[(long long)b * p.q_len + i];
+        if (d >= 0) qd = d;
+      }
+    }
+    // columns a row sees by length and causality: below this key
+    int seen_end = info.len;
+    if (p.causal) seen_end = min(seen_end, max(place + 1, info.prefix));
+    // the least of the tile's rows: key tiles that end below it need no mask
+    int all_end = info.len;
+    if (p.causal) all_end = min(all_end, max(info.start + q0 + w * kTile + 1, info.prefix));
+
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int k0 = (tb + j) * kTile;
+      bool masked = k0 + kTile > all_end, clean = k0 + kTile > info.len && info.len < p.k_len;
+      const int32_t* kd = nullptr;
+      if (kdocs) {
+        const int4 kr = t.k_ranges[b * t.k_tiles + tb + j];
+        if (!(qr.z && kr.z && qr.x == kr.x)) kd = kdocs + k0, masked = true;
+        if (!kr.z) clean = true;
+      }
+      ok = bar_wait(bar(kSFull + w), j & 1, &dead, t.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after();
+      if (clean) {
+        // rows of V that nothing may use become zeros: 0 weights times
+        // whatever memory holds would not be 0
+        const int it = 2 * j + 1;
+        ok = bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const int key = k0 + lane_row;
+        if (key >= info.len || (kdocs && kdocs[key] < 0)) {
+          unsigned char* row = mem + L::kRing + (it % L::kSlots) * L::kOperand + lane_row * 128;
+          for (int x = 0; x < L::kBoxes; ++x)
+            for (int e = 0; e < 8; ++e) *(uint4*)(row + x * L::kBox + 16 * e) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async();
+      }
+      float s[128];
+      uint32_t* u = (uint32_t*)s;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, u + 32 * x);
+      wait_ld();
+#pragma unroll
+      for (int x = 0; x < 4; ++x) tie32(u + 32 * x);
+      const int o0 = k0 - place;
+      if (masked) RowScores<MODE, true>::apply(s, p, c, bias, slope2, o0, seen_end - k0, qd, kd);
+      else RowScores<MODE, false>::apply(s, p, c, bias, slope2, o0, 128, 0, nullptr);
+      float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int e = 4; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
+      float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      if (MODE == 0) mx *= c;  // scale > 0 here
+      if (__any_sync(0xffffffffu, mx > m + kRise || (m == -INFINITY && mx > m))) {
+        const float top_m = fmaxf(m, mx), f = top_m == -INFINITY ? 1.f : ex2(m - top_m);
+        m = top_m;
+        l *= f;
+        if (j > 0) {
+#pragma unroll 1
+          for (int x = 0; x < DP; x += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + x, o);
+            wait_ld();
+            tie32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(to + x, o);
+          }
+        }
+      }
+      const float m0 = (m == -INFINITY ? 0.f : m) - kLift<BF16>;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float a = s[64 * half + 2 * e], z = s[64 * half + 2 * e + 1];
+          const float pa = ex2(MODE == 0 ? fmaf(a, c, -m0) : a - m0);
+          const float pz = ex2(MODE == 0 ? fmaf(z, c, -m0) : z - m0);
+          sum[e & 3] += pa + pz;
+          // weights go to the product in the inputs' type: the sum keeps 32 bits
+          pk[e] = pack2<BF16>(pa, pz);
+        }
+        tmem_st32(ts + 32 * half, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (tid % 32 == 0) bar_arrive(bar(kPReady + w));
+    }
+    // ---- the row's result
+    if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(bar(kOFull + w), 0, &dead, t.err));
+    if (ok) {
+      fence_after();
+      const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+      const long long row = ((long long)b * p.heads + h) * p.q_len + i;
+      const bool store = i < p.q_len;
+      if (t.splits > 1) {
+        const long long at = (long long)split * p.batch * p.heads * p.q_len + row;
+        if (store) t.part_lse[at] = l == 0.f ? -INFINITY : m - kLift<BF16> + log2f(l);
+#pragma unroll 1
+        for (int x = 0; x < t.dim16; x += 16) {
+          uint32_t o[16];
+          if (n > 0) tmem_ld16(to + x, o);
+          wait_ld();
+          tie16(o);
+          if (store)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              if (x + e < p.dim)
+                *(float4*)(t.part_o + at * p.dim + x + e) =
+                    n > 0 ? make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                        __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      } else {
+        if (store && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m - kLift<BF16> + log2f(l)) * kLn2;
+        uint16_t* out = (uint16_t*)p.out + b * p.os.b + i * p.os.t + h * p.os.h;
+#pragma unroll 1
+        for (int x = 0; x < t.dim16; x += 16) {
+          uint32_t o[16];
+          if (n > 0) tmem_ld16(to + x, o);
+          wait_ld();
+          tie16(o);
+          uint32_t r[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            r[e] = n > 0 ? pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
+          if (store) {
+            *(uint4*)(out + x) = make_uint4(r[0], r[1], r[2], r[3]);
+            if (x + 8 < p.dim) *(uint4*)(out + x + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+          }
+        }
+      }
+      fence_before();
+    }
+  } else {
+    give_registers<40>();
+    if (warp == 8) {
+      if (tid % 32 == 0 && n > 0) {
+        // ---- copies: q once, then K and V tiles in turn through the ring
+        bar_expect(bar(kQFull), 2 * L::kOperand);
+        for (int w = 0; w < 2; ++w)
+          for (int x = 0; x < L::kBoxes; ++x)
+            tma_load(base + w * L::kOperand + x * L::kBox, &t.qm, bar(kQFull), 64 * x, q0 + w * kTile, h * t.q_mh,
+                     b * t.q_mb);
+        for (int it = 0; it < 2 * n; ++it) {
+          const int s = it % L::kSlots, round = it / L::kSlots;
+          if (!bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err)) break;
+          bar_expect(bar(kFull + s), L::kOperand);
+          const int row = (tb + it / 2) * kTile;
+          for (int x = 0; x < L::kBoxes; ++x) {
+            const uint32_t to = base + L::kRing + s * L::kOperand + x * L::kBox;
+            if (it & 1) tma_load(to, &t.vm, bar(kFull + s), 64 * x, row, hk * t.v_mh, b * t.v_mb);
+            else tma_load(to, &t.km, bar(kFull + s), 64 * x, row, hk * t.k_mh, b * t.k_mb);
+          }
+        }
+      }
+    } else if (warp == 9) {
+      if (tid % 32 == 0 && n > 0) {
+        // ---- products
+        const uint32_t id_s = instr_desc(kTile, kTile, BF16, false), id_o = instr_desc(kTile, t.dim16, BF16, true);
+        const int ksteps = t.dim16 / 16;
+        auto scores = [&](int w, uint32_t slot) {
+          for (int k = 0; k < ksteps; ++k) {
+            const uint32_t at = (k / 4) * L::kBox + (k % 4) * 32;
+            mma_ss(tmem + w * kTile, desc_k(base + w * L::kOperand + at),
+                   desc_k(base + L::kRing + slot * L::kOperand + at), id_s, k > 0);
+          }
+          mma_commit(bar(kSFull + w));
+        };
+        auto slot_of = [&](int it) { return (uint32_t)(it % L::kSlots); };
+        auto ring_wait = [&](int it) {
+          return bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err);
+        };
+        bool ok = bar_wait(bar(kQFull), 0, &dead, t.err) && ring_wait(0);
+        if (ok) {
+          scores(0, slot_of(0));
+          scores(1, slot_of(0));
+          mma_commit(bar(kEmpty + slot_of(0)));
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          const uint32_t sv = slot_of(2 * j + 1), sk = slot_of(2 * j + 2);
+          for (int w = 0; ok && w < 2; ++w) {
+            ok = bar_wait(bar(kPReady + w), j & 1, &dead, t.err) && (w || ring_wait(2 * j + 1));
+            if (!ok) break;
+            fence_after();
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts(tmem + kO + w * DP, tmem + w * kTile + k * 8,
+                     desc_mn(base + L::kRing + sv * L::kOperand + k * 2048, L::kBox), id_o, j > 0 || k > 0);
+            if (w) mma_commit(bar(kEmpty + sv));
+            if (j + 1 < n) {
+              // the tensor unit runs products in the order of issue: these
+              // scores replace P only after the product above has read it
+              if (!w) ok = ring_wait(2 * j + 2);
+              if (!ok) break;
+              scores(w, sk);
+              if (w) mma_commit(bar(kEmpty + sk));
+            } else {
+              mma_commit(bar(kOFull + w));
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (dead && tid == 0) {
+    // copies still in flight land in this block's memory: give them time
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <int DP, bool BF16>
+fm_status launch(const TcParams& t, int mode, cudaStream_t st) {
+  const dim3 grid((t.p.q_len + 2 * kTile - 1) / (2 * kTile), t.p.heads, t.p.batch * t.splits);
+  const size_t smem = Smem<DP>::bytes(t.p.max_distance, t.p.map != nullptr);
+  auto k = mode == 0 ? kernel<DP, BF16, 0> : mode == 1 ? kernel<DP, BF16, 1> : kernel<DP, BF16, 2>;
+  if (!allow_smem(k, smem)) return FM_ERR_CUDA;
+  k<<<grid, kThreads, smem, st>>>(t);
+  return launch_status();
+}
+
+}  // namespace fwd
+}  // namespace fm

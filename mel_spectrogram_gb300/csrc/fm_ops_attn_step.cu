@@ -1,0 +1,346 @@
+// Attention of a few queries against a long cache of keys: one new token, or
+// a handful, per stream.
+//
+// Bound by reading K and V once. The queries of all heads that share a key
+// head make the rows of one 16-row operand (row = query * group + head), so
+// that the cache crosses HBM once whatever the grouping; products run on
+// mma.sync (16 rows would leave 7/8 of a tcgen05 tile empty, and the products
+// take a tenth of the time that the loads do). The key axis is split over
+// blocks, and within a block over its warps, each with its own ring of tiles
+// of 16 keys filled by cp.async: no barrier in the loop, two tiles a warp and
+// 128 KB an SM in flight. Warps join through shared memory, blocks through the
+// join kernel.
+#include "fm_ops_attn_tc.cuh"
+
+namespace fm {
+namespace {
+
+using namespace tc;
+
+constexpr int kWarps = 4, kKeys = 16, kStages = 3;
+
+template <int DP>
+constexpr int stage_bytes() { return 2 * kKeys * DP * 2; }
+template <int DP>
+constexpr size_t smem_bytes() {
+  const size_t ring = (size_t)kWarps * kStages * stage_bytes<DP>();
+  const size_t out = (size_t)kWarps * 16 * (DP + 2) * sizeof(float);  // warps' results, over the ring
+  return ring > out ? ring : out;
+}
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
+  const int n = real ? 16 : 0;  // the rest of the 16 bytes becomes zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct StepParams {
+  AttnParams p;
+  int splits, split_keys;  // keys of one split, a multiple of kWarps * kKeys
+  int row_tiles;
+  float *part_o, *part_lse;
+};
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
+  extern __shared__ __align__(128) unsigned char raw[];
+  __shared__ float stat[2][kWarps][16];
+  const AttnParams& p = t.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = blockIdx.x / t.row_tiles, rt = blockIdx.x % t.row_tiles;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const RowInfo info = row_info(p, b);
+  const int rows = p.q_len * p.group;
+  const int quad = lane >> 2, pair = 2 * (lane & 3);
+  const int k_begin = split * t.split_keys;
+  int k_end = min(info.len, k_begin + t.split_keys);
+  if (p.causal) k_end = min(k_end, max(info.start + p.q_len, info.prefix));
+
+  // this thread's two rows
+  int qi[2], qh[2], qd[2];
+  bool row_ok[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int row = rt * 16 + quad + 8 * r;
+    row_ok[r] = row < rows;
+    qi[r] = row_ok[r] ? row / p.group : 0;
+    qh[r] = hk * p.group + (row_ok[r] ? row % p.group : 0);
+    qd[r] = -2;
+    if (p.q_docs) {
+      const int d = p.q_docs[(long long)b * p.q_len + qi[r]];
+      if (d >= 0) qd[r] = d;
+    }
+  }
+  constexpr int kSteps = DP / 16;
+  const int steps = (p.dim + 15) / 16;
+  uint32_t q[kSteps][4];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = e & 1, d = 16 * s + pair + 8 * (e >> 1);
+      q[s][e] = row_ok[r] && d < p.dim
+                    ? *(const uint32_t*)((const uint16_t*)p.q + b * p.qs.b + qi[r] * p.qs.t + qh[r] * p.qs.h + d)
+                    : 0u;
+    }
+  float slope[2] = {0.f, 0.f}, below[2] = {0.f, 0.f}, above[2] = {0.f, 0.f};
+  const int D = p.max_distance;
+  const float c = p.scale * kLog2e;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    if (p.slopes) slope[r] = p.slopes[qh[r]] * kLog2e;
+    if (p.map) {
+      below[r] = kLog2e * table_value(p, (long long)p.map[0] * p.heads + qh[r], BF16);
+      above[r] = kLog2e * table_value(p, (long long)p.map[2 * D] * p.heads + qh[r], BF16);
+    }
+  }
+  const int32_t* kdocs = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
+
+  // ---- the warp's ring: tile n of the split's tiles warp, warp + 4, ...
+  const uint32_t ring = smem_u32(raw) + warp * kStages * stage_bytes<DP>();
+  const uint16_t* kbase = (const uint16_t*)p.k + b * p.ks.b + hk * p.ks.h;
+  const uint16_t* vbase = (const uint16_t*)p.v + b * p.vs.b + hk * p.vs.h;
+  const int tiles = k_end > k_begin ? (k_end - k_begin + kKeys - 1) / kKeys : 0;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  const int chunks = 2 * steps;  // 16-byte pieces of a row that are used
+  auto load = [&](int n) {
+    if (n < mine) {
+      const int k0 = k_begin + (warp + n * kWarps) * kKeys;
+      const uint32_t to = ring + (n % kStages) * stage_bytes<DP>();
+      // half a warp a row pair: 16 lanes cover up to 16 pieces of one row
+#pragma unroll
+      for (int r = 0; r < kKeys; r += (DP == 128 ? 2 : 4)) {
+        const int row = r + lane / (DP / 8), piece = lane % (DP / 8);
+        const int key = k0 + row;
+        bool real = key < k_end;
+        if (kdocs) real = real && kdocs[key] >= 0;
+        const bool data = real && piece * 8 < p.dim;
+        const long long at = data ? key : 0;  // an address to leave unread
+        const int d = data ? piece * 8 : 0;
+        const uint32_t place = row * (DP * 2) + ((piece ^ (row & 7)) << 4);
+        if (piece < chunks) {
+          copy16(to + place, kbase + at * p.ks.t + d, data);
+          copy16(to + kKeys * DP * 2 + place, vbase + at * p.vs.t + d, data);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float o[DP / 8][4];
+#pragma unroll
+  for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < kStages - 1; ++n) load(n);
+  for (int n = 0; n < mine; ++n) {
+    load(n + kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+    const int k0 = k_begin + (warp + n * kWarps) * kKeys;
+    const uint32_t K = ring + (n % kStages) * stage_bytes<DP>(), V = K + kKeys * DP * 2;
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      if (st < steps) {
+        // four 8 x 8 pieces: keys 0-7 and 8-15, dims 16 st and 16 st + 8
+        const int row = (lane & 7) + ((lane & 16) >> 1), piece = 2 * st + ((lane >> 3) & 1);
+        uint32_t kf[4];
+        ldsm4(K + row * (DP * 2) + ((piece ^ (row & 7)) << 4), kf);
+        mma16<BF16>(s[0], q[st], kf[0], kf[1]);
+        mma16<BF16>(s[1], q[st], kf[2], kf[3]);
+      }
+    }
+    // element e of s[x]: row quad + 8 (e / 2), key k0 + 8 x + pair + e % 2
+    const bool far = !p.map || (k0 - info.start - p.q_len + 1 >= D) || (k0 + kKeys - 1 - info.start <= -D);
+    bool masked = k0 + kKeys > k_end || kdocs;
+    if (p.causal) masked = masked || k0 + kKeys > max(info.start + 1, info.prefix);
+    const bool is_above = k0 > info.start;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e >> 1, key = k0 + 8 * x + pair + (e & 1), off = key - info.start - qi[r];
+        float z = s[x][e];
+        if (p.cap > 0.f) z = p.cap * kLog2e * tanh_from(z * (2.f * kLog2e * p.scale / p.cap));
+        else z *= c;
+        if (p.map) {
+          if (far) {
+            z += is_above ? above[r] : below[r];
+          } else {
+            const int at = __ldg(p.map + min(max(off, -D), D) + D);
+            z += kLog2e * table_value(p, (long long)at * p.heads + qh[r], BF16);
+          }
+        }
+        if (p.slopes) z = fmaf(-slope[r], fabsf((float)off), z);
+        if (masked) {
+          bool seen = key < k_end && !(p.causal && off > 0 && key >= info.prefix);
+          if (kdocs && seen) seen = __ldg(kdocs + key) == qd[r];
+          z = seen ? z : -INFINITY;
+        }
+        s[x][e] = z;
+      }
+    float f[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float top = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top = fmaxf(top, m[r]);
+      const float zero = top == -INFINITY ? 0.f : top;
+      f[r] = ex2(m[r] - zero);
+      m[r] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[x][2 * r + e] = ex2(s[x][2 * r + e] - zero);
+          sum += s[x][2 * r + e];
+        }
+      l[r] = l[r] * f[r] + sum;  // this thread's columns; joined at the end
+    }
+    // weights go to the product in the cache's type
+    uint32_t pf[4] = {pack2<BF16>(s[0][0], s[0][1]), pack2<BF16>(s[0][2], s[0][3]), pack2<BF16>(s[1][0], s[1][1]),
+                      pack2<BF16>(s[1][2], s[1][3])};
+    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+      for (int x = 0; x < DP / 8; ++x) {
+        o[x][0] *= f[0];
+        o[x][1] *= f[0];
+        o[x][2] *= f[1];
+        o[x][3] *= f[1];
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      if (st < steps) {
+        const int row = lane & 15, piece = 2 * st + (lane >> 4);
+        uint32_t vf[4];
+        ldsm4_t(V + row * (DP * 2) + ((piece ^ (row & 7)) << 4), vf);
+        mma16<BF16>(o[2 * st], pf, vf[0], vf[1]);
+        mma16<BF16>(o[2 * st + 1], pf, vf[2], vf[3]);
+      }
+    }
+    __syncwarp();
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // ---- the warps' results
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    if ((lane & 3) == 0) stat[0][warp][quad + 8 * r] = m[r], stat[1][warp][quad + 8 * r] = l[r];
+  }
+  __syncthreads();
+  float* all = (float*)raw;  // [warps][16][DP + 2]
+#pragma unroll
+  for (int x = 0; x < DP / 8; ++x)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      *(float2*)(all + (warp * 16 + quad + 8 * r) * (DP + 2) + 8 * x + pair) = make_float2(o[x][2 * r], o[x][2 * r + 1]);
+  __syncthreads();
+  const int valid = min(16, rows - rt * 16);
+  const int per_row = p.dim / 8;
+  for (int e = tid; e < valid * per_row; e += kWarps * 32) {
+    const int row = e / per_row, d = (e - row * per_row) * 8;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[0][w][row]);
+    const float zero = top == -INFINITY ? 0.f : top;
+    float total = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float g = ex2(stat[0][w][row] - zero);
+      total = fmaf(stat[1][w][row], g, total);
+      const float* from = all + (w * 16 + row) * (DP + 2) + d;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = fmaf(from[k], g, acc[k]);
+    }
+    const float f = total == 0.f ? 0.f : 1.f / total;
+    const int at_row = rt * 16 + row, i = at_row / p.group, h = hk * p.group + at_row % p.group;
+    const long long stat_row = ((long long)b * p.heads + h) * p.q_len + i;
+    const float lse = total == 0.f ? -INFINITY : top + log2f(total);
+    if (t.splits > 1) {
+      const long long at = (long long)split * p.batch * p.heads * p.q_len + stat_row;
+      if (d == 0) t.part_lse[at] = lse;
+      float4* to = (float4*)(t.part_o + at * p.dim + d);
+      to[0] = make_float4(acc[0] * f, acc[1] * f, acc[2] * f, acc[3] * f);
+      to[1] = make_float4(acc[4] * f, acc[5] * f, acc[6] * f, acc[7] * f);
+    } else {
+      if (d == 0 && p.lse) p.lse[stat_row] = lse * kLn2;
+      *(uint4*)((uint16_t*)p.out + b * p.os.b + i * p.os.t + h * p.os.h + d) =
+          make_uint4(pack2<BF16>(acc[0] * f, acc[1] * f), pack2<BF16>(acc[2] * f, acc[3] * f),
+                     pack2<BF16>(acc[4] * f, acc[5] * f), pack2<BF16>(acc[6] * f, acc[7] * f));
+    }
+  }
+}
+
+template <int DP, bool BF16>
+fm_status launch(const StepParams& t, cudaStream_t st) {
+  const dim3 grid(t.splits * t.row_tiles, t.p.kv_heads, t.p.batch);
+  if (!allow_smem(step<DP, BF16>, smem_bytes<DP>())) return FM_ERR_CUDA;
+  step<DP, BF16><<<grid, kWarps * 32, smem_bytes<DP>(), st>>>(t);
+  return launch_status();
+}
+}  // namespace
+
+StepPlan step_plan(const AttnParams& p) {
+  StepPlan w{};
+  w.row_tiles = (p.q_len * p.group + 15) / 16;
+  // Splits of at least 256 keys, as many as fill the SMs' blocks (two of 96 KB
+  // with head size 128, four of 48 KB with 64) in whole waves.
+  const long long slots = (long long)num_sms() * (p.dim <= 64 ? 4 : 2);
+  const long long blocks = (long long)p.batch * p.kv_heads * w.row_tiles;
+  const long long most = p.k_len / 256 > 1 ? p.k_len / 256 : 1;
+  long long best = 1;
+  double best_use = 0;
+  for (long long waves = 1; waves <= 4; ++waves) {
+    long long s = waves * slots / blocks;
+    if (s < 1) continue;
+    if (s > most) s = most;
+    const long long n = s * blocks;
+    const double use = (double)n / (double)((n + slots - 1) / slots * slots);
+    if (use > best_use + 0.02) best = s, best_use = use;
+  }
+  const int unit = kWarps * kKeys;
+  w.split_keys = (int)(((p.k_len + best - 1) / best + unit - 1) / unit * unit);
+  if (w.split_keys < unit) w.split_keys = unit;
+  w.splits = (p.k_len + w.split_keys - 1) / w.split_keys;
+  if (w.splits < 1) w.splits = 1;
+  return w;
+}
+
+fm_status attn_step(const AttnParams& p, int64_t dtype, const StepPlan& w, float* part_o, float* part_lse,
+                    cudaStream_t st) {
+  StepParams t{p, w.splits, w.split_keys, w.row_tiles, part_o, part_lse};
+  const bool bf16 = dtype == FM_BF16;
+  return p.dim <= 64 ? (bf16 ? launch<64, true>(t, st) : launch<64, false>(t, st))
+                     : (bf16 ? launch<128, true>(t, st) : launch<128, false>(t, st));
+}
+}  // namespace fm

@@ -1,0 +1,394 @@
+// Host side of the tensor-core attention kernels, and the small kernels around
+// them: document ranges of tiles before, the join of split results after.
+#include "fm_ops_attn_bwd.cuh"
+
+#include <cudaTypedefs.h>
+
+namespace fm {
+
+__device__ unsigned g_ops_error;
+
+unsigned* ops_error_word() {
+  static unsigned* known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (known[dev] == nullptr) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_ops_error) != cudaSuccess) return nullptr;
+    known[dev] = (unsigned*)p;
+  }
+  return known[dev];
+}
+
+fm_status attn_fwd_bf16_64(const TcParams& t, int mode, cudaStream_t st);
+fm_status attn_fwd_bf16_128(const TcParams& t, int mode, cudaStream_t st);
+fm_status attn_fwd_f16_64(const TcParams& t, int mode, cudaStream_t st);
+fm_status attn_fwd_f16_128(const TcParams& t, int mode, cudaStream_t st);
+
+#define FM_BWD(name) fm_status name(const TcParams& t, const bwd::Extra& x, int mode, cudaStream_t st)
+FM_BWD(attn_bwd_keys_bf16_64);
+FM_BWD(attn_bwd_keys_bf16_128);
+FM_BWD(attn_bwd_keys_f16_64);
+FM_BWD(attn_bwd_keys_f16_128);
+FM_BWD(attn_bwd_queries_bf16_64);
+FM_BWD(attn_bwd_queries_bf16_128);
+FM_BWD(attn_bwd_queries_f16_64);
+FM_BWD(attn_bwd_queries_f16_128);
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return (PFN_cuTensorMapEncodeTiled_v12000) nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// Whether a tensor [batch][len][heads][dim] can be read by 16-byte rows: a
+// stride of 0 (a broadcast head or batch) becomes a dimension of one entry.
+bool rows_ok(const void* base, const Strides& s, int batch, int len, int heads) {
+  auto ok = [](long long stride, int extent, bool broadcast) {
+    return extent <= 1 || (broadcast && stride == 0) || (stride > 0 && stride % 8 == 0 && stride < (1LL << 38));
+  };
+  return ((uintptr_t)base & 15) == 0 && ok(s.t, len, false) && ok(s.h, heads, true) && ok(s.b, batch, true);
+}
+
+bool encode(CUtensorMap* m, const void* base, const Strides& s, int batch, int len, int heads, int dim, int rows,
+            bool bf16, int* mh, int* mb) {
+  *mh = heads > 1 && s.h != 0;
+  *mb = batch > 1 && s.b != 0;
+  const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)len, (cuuint64_t)(*mh ? heads : 1),
+                              (cuuint64_t)(*mb ? batch : 1)};
+  auto bytes = [&](long long stride, bool used) { return (cuuint64_t)(used ? stride * 2 : 16); };
+  const cuuint64_t strides[3] = {bytes(s.t, len > 1), bytes(s.h, *mh), bytes(s.b, *mb)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
+  return encoder() != nullptr &&
+         encoder()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Ids of each tile of 128 frames: {lowest, highest, all one id}; padding
+// frames count only against the last.
+__global__ void __launch_bounds__(kTile) doc_ranges(const int32_t* q_docs, const int32_t* k_docs, int q_len, int k_len,
+                                                    int q_tiles, int k_tiles, int4* out) {
+  __shared__ int lo, hi, valid;
+  const int x = blockIdx.x, b = blockIdx.y;
+  const bool keys = x >= q_tiles;
+  const int tile = keys ? x - q_tiles : x, len = keys ? k_len : q_len;
+  const int at = tile * kTile + threadIdx.x;
+  const int id = at < len ? (keys ? k_docs : q_docs)[(long long)b * len + at] : -1;
+  if (threadIdx.x == 0) lo = 0x7fffffff, hi = -1, valid = 0;
+  __syncthreads();
+  if (id >= 0) {
+    atomicMin(&lo, id);
+    atomicMax(&hi, id);
+    atomicAdd(&valid, 1);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int4* to = keys ? out + (long long)gridDim.y * q_tiles + (long long)b * k_tiles : out + (long long)b * q_tiles;
+    to[tile] = make_int4(lo, hi, valid == kTile && lo == hi, 0);
+  }
+}
+
+// out = sum of the splits' results, weighted by 2^(lse - highest lse). A block
+// a row: its eight warps take every eighth split, four elements a lane, and
+// are added up in order.
+template <bool BF16>
+__global__ void __launch_bounds__(256) join(const AttnParams p, int splits, const float* part_o, const float* part_lse) {
+  __shared__ float tops[8], totals[8];
+  __shared__ float4 sums[8][32];
+  const long long rows = (long long)p.batch * p.heads * p.q_len, row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  for (int s = threadIdx.x; s < splits; s += 256) top = fmaxf(top, part_lse[s * rows + row]);
+  top = warp_max(top);
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+  top = tops[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) top = fmaxf(top, tops[w]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float total = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // dim <= 128
+  const bool mine = 4 * lane < p.dim;
+#pragma unroll 4
+  for (int s = warp; s < splits; s += 8) {
+    const float lse = part_lse[s * rows + row], w = lse == -INFINITY ? 0.f : exp2f(lse - base);
+    total += w;
+    if (mine) {
+      const float4 o = *(const float4*)(part_o + (s * rows + row) * p.dim + 4 * lane);
+      acc.x = fmaf(w, o.x, acc.x);
+      acc.y = fmaf(w, o.y, acc.y);
+      acc.z = fmaf(w, o.z, acc.z);
+      acc.w = fmaf(w, o.w, acc.w);
+    }
+  }
+  sums[warp][lane] = acc;
+  if (lane == 0) totals[warp] = total;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) {
+    const float4 o = sums[w][lane];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
+    total += totals[w];
+  }
+  const int i = (int)(row % p.q_len), h = (int)(row / p.q_len % p.heads), b = (int)(row / p.q_len / p.heads);
+  const float f = total == 0.f ? 0.f : 1.f / total;
+  if (p.lse && lane == 0) p.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+  if (mine) {
+    uint16_t* out = (uint16_t*)p.out + b * p.os.b + i * p.os.t + h * p.os.h + 4 * lane;
+    *(uint2*)out = make_uint2(tc::pack2<BF16>(acc.x * f, acc.y * f), tc::pack2<BF16>(acc.z * f, acc.w * f));
+  }
+}
+
+// the largest of a block's values (not negative), into *to
+__device__ __forceinline__ void block_peak(float v, float* to) {
+  __shared__ float tops[8];
+  v = warp_max(v);
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) v = fmaxf(v, tops[w]);
+    atomicMax((int*)to, __float_as_int(v));  // bits of such floats are ordered as ints; a maximum has no order
+  }
+}
+
+// Statistics of the backward pass by query, padded to whole tiles of 64:
+// base-2 lse (+inf where a query sees nothing or is padding: every weight
+// 2^(z - inf) is 0) less `lift`, and delta = dout . out. 16 lanes a row, 8
+// elements each; a block's 16 rows are of one head. peak: the largest squared
+// norm of a row of dout, by key head.
+template <typename T>
+__global__ void __launch_bounds__(256) bwd_stats(const AttnParams p, int q_pad, float lift, float* lse2, float* delta,
+                                                 float* peak) {
+  const long long rows = (long long)p.batch * p.heads * q_pad, row = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15;
+  const int i = (int)(row % q_pad), h = (int)(row / q_pad % p.heads), b = (int)(row / q_pad / p.heads);
+  const bool there = i < p.q_len && (p.q_docs == nullptr || p.q_docs[(long long)b * p.q_len + i] >= 0);
+  float s = 0.f, norm = 0.f;
+  if (there && lane * 8 < p.dim) {
+    const Pack<T, 8> g = *(const Pack<T, 8>*)((const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h + lane * 8);
+    const Pack<T, 8> o = *(const Pack<T, 8>*)((const T*)p.out_in + b * p.os.b + i * p.os.t + h * p.os.h + lane * 8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float d = to_f(g.v[k]);
+      s = fmaf(d, to_f(o.v[k]), s);
+      norm = fmaf(d, d, norm);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o, 16);
+    norm += __shfl_xor_sync(0xffffffffu, norm, o, 16);
+  }
+  if (peak) block_peak(norm, peak + b * p.kv_heads + h / p.group);
+  if (lane == 0) {
+    const float l = there ? p.lse[((long long)b * p.heads + h) * p.q_len + i] : -INFINITY;
+    lse2[row] = l == -INFINITY ? INFINITY : l * kLog2e - lift;
+    delta[row] = s;
+  }
+}
+
+// The largest squared norm of a row of v that counts, by batch entry and key
+// head; 16 rows at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) bwd_v_peak(const AttnParams p, float* peak) {
+  const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 15;
+  const int len = row_info(p, b).len;
+  float top = 0.f;
+  for (int j0 = blockIdx.x * 16; j0 < len; j0 += gridDim.x * 16) {
+    const int j = j0 + (threadIdx.x >> 4);
+    float norm = 0.f;
+    if (j < len && lane * 8 < p.dim && (p.k_docs == nullptr || p.k_docs[(long long)b * p.k_len + j] >= 0)) {
+      const Pack<T, 8> v = *(const Pack<T, 8>*)((const T*)p.v + b * p.vs.b + j * p.vs.t + h * p.vs.h + lane * 8);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) norm = fmaf(to_f(v.v[k]), to_f(v.v[k]), norm);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, o, 16);
+    top = fmaxf(top, norm);
+  }
+  block_peak(top, peak + b * p.kv_heads + h);
+}
+
+// bias[h][o + max_distance] in base 2
+__global__ void __launch_bounds__(256) bwd_bias(const AttnParams p, int bf16, float* bias) {
+  const int W = 2 * p.max_distance + 1, i = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y;
+  if (i < W) bias[(long long)h * W + i] = kLog2e * table_value(p, (long long)p.map[i] * p.heads + h, bf16);
+}
+
+// Rows (queries x heads that share a key head) up to which the few-query
+// kernel runs: two operands of 16.
+constexpr int kStepRows = 32;
+
+int mode_of(const AttnParams& p) {
+  if (p.cap > 0.f || p.slopes || !(p.scale > 0.f)) return 2;
+  return p.map ? 1 : 0;
+}
+int64_t align256(int64_t n) { return (n + 255) & ~(int64_t)255; }
+}  // namespace
+
+bool tc_layout_ok(const AttnParams& p, int64_t dtype, bool backward) {
+  if (dtype == FM_F32 || p.dim > 128 || p.dim % 8 || p.k_len == 0 || encoder() == nullptr) return false;
+  if (backward && !(p.q_len > 0 && rows_ok(p.dout, p.dos, p.batch, p.q_len, p.heads) &&
+                    rows_ok(p.out_in, p.os, p.batch, p.q_len, p.heads) &&
+                    rows_ok(p.dq, p.dqs, p.batch, p.q_len, p.heads) &&
+                    rows_ok(p.dk, p.dks, p.batch, p.k_len, p.kv_heads) &&
+                    rows_ok(p.dv, p.dvs, p.batch, p.k_len, p.kv_heads)))
+    return false;
+  return rows_ok(p.q, p.qs, p.batch, p.q_len, p.heads) && rows_ok(p.k, p.ks, p.batch, p.k_len, p.kv_heads) &&
+         rows_ok(p.v, p.vs, p.batch, p.k_len, p.kv_heads) && rows_ok(p.out, p.os, p.batch, p.q_len, p.heads);
+}
+
+TcPlan tc_plan(const AttnParams& p, bool backward) {
+  TcPlan w{};
+  w.q_tiles = (p.q_len + kTile - 1) / kTile;
+  w.k_tiles = (p.k_len + kTile - 1) / kTile;
+  w.splits = 1;
+  w.split_tiles = w.k_tiles;
+  if (!backward && (long long)p.q_len * p.group <= kStepRows) {
+    w.step = step_plan(p);
+    w.splits = w.step.splits;
+  } else if (!backward) {
+    // Too few blocks for the SMs and a long key axis: split it, four tiles a
+    // split at least (a split costs a pass of its rows through the join).
+    const long long blocks = (long long)((w.q_tiles + 1) / 2) * p.heads * p.batch;
+    const int sms = num_sms();
+    if (blocks * 2 <= sms && w.k_tiles >= 8) {
+      long long s = sms / blocks;
+      if (s > w.k_tiles / 4) s = w.k_tiles / 4;
+      w.split_tiles = (int)((w.k_tiles + s - 1) / s);
+      w.splits = (w.k_tiles + w.split_tiles - 1) / w.split_tiles;
+    }
+  }
+  int64_t at = 0;
+  w.ranges = at;
+  if (p.q_docs) at += align256((int64_t)sizeof(int4) * p.batch * (w.q_tiles + w.k_tiles));
+  const int64_t rows = (int64_t)p.batch * p.heads * p.q_len;
+  w.part_o = at;
+  if (w.splits > 1) at += align256(rows * w.splits * p.dim * (int64_t)sizeof(float));
+  w.part_lse = at;
+  if (w.splits > 1) at += align256(rows * w.splits * (int64_t)sizeof(float));
+  w.stats = at;
+  if (backward) at += align256((int64_t)sizeof(float) * 2 * p.batch * p.heads * ((p.q_len + 63) / 64 * 64));
+  w.peak = at;
+  if (backward) at += align256((int64_t)sizeof(float) * 2 * p.batch * p.kv_heads);
+  w.bias = at;
+  if (backward && p.map) at += align256((int64_t)sizeof(float) * p.heads * (2 * (int64_t)p.max_distance + 1));
+  w.total = at;
+  return w;
+}
+
+fm_status tc_setup(TcParams& t, const AttnParams& p, int64_t dtype, const TcPlan& w, char* ws, int q_rows, int k_rows,
+                   cudaStream_t st) {
+  const bool bf16 = dtype == FM_BF16;
+  t.p = p;
+  t.err = ops_error_word();
+  if (t.err == nullptr) return FM_ERR_CUDA;
+  t.q_tiles = w.q_tiles;
+  t.k_tiles = w.k_tiles;
+  t.dim16 = (p.dim + 15) / 16 * 16;
+  t.splits = w.splits;
+  t.split_tiles = w.split_tiles;
+  if (!encode(&t.qm, p.q, p.qs, p.batch, p.q_len, p.heads, p.dim, q_rows, bf16, &t.q_mh, &t.q_mb) ||
+      !encode(&t.km, p.k, p.ks, p.batch, p.k_len, p.kv_heads, p.dim, k_rows, bf16, &t.k_mh, &t.k_mb) ||
+      !encode(&t.vm, p.v, p.vs, p.batch, p.k_len, p.kv_heads, p.dim, k_rows, bf16, &t.v_mh, &t.v_mb))
+    return FM_ERR_CUDA;
+  if (p.dout && !encode(&t.gm, p.dout, p.dos, p.batch, p.q_len, p.heads, p.dim, q_rows, bf16, &t.g_mh, &t.g_mb))
+    return FM_ERR_CUDA;
+  if (p.q_docs) {
+    int4* r = (int4*)(ws + w.ranges);
+    doc_ranges<<<dim3(w.q_tiles + w.k_tiles, p.batch), kTile, 0, st>>>(p.q_docs, p.k_docs, p.q_len, p.k_len,
+                                                                       w.q_tiles, w.k_tiles, r);
+    t.q_ranges = r;
+    t.k_ranges = r + (int64_t)p.batch * w.q_tiles;
+  }
+  return FM_OK;
+}
+
+fm_status attn_tc_forward(const AttnParams& p, int64_t dtype, char* ws, cudaStream_t st) {
+  const TcPlan w = tc_plan(p, false);
+  const bool bf16 = dtype == FM_BF16;
+  TcParams t{};
+  t.part_o = (float*)(ws + w.part_o);
+  t.part_lse = (float*)(ws + w.part_lse);
+  fm_status s = FM_OK;
+  if (w.step.splits > 0) {
+    s = attn_step(p, dtype, w.step, t.part_o, t.part_lse, st);
+  } else {
+    s = tc_setup(t, p, dtype, w, ws, kTile, kTile, st);
+    const int mode = mode_of(p);
+    if (s == FM_OK)
+      s = p.dim <= 64 ? (bf16 ? attn_fwd_bf16_64(t, mode, st) : attn_fwd_f16_64(t, mode, st))
+                      : (bf16 ? attn_fwd_bf16_128(t, mode, st) : attn_fwd_f16_128(t, mode, st));
+  }
+  if (s != FM_OK || w.splits == 1) return s;
+  const long long rows = (long long)p.batch * p.heads * p.q_len;
+  const unsigned blocks = (unsigned)rows;
+  if (bf16) join<true><<<blocks, 256, 0, st>>>(p, w.splits, t.part_o, t.part_lse);
+  else join<false><<<blocks, 256, 0, st>>>(p, w.splits, t.part_o, t.part_lse);
+  return launch_status();
+}
+
+fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cudaStream_t st) {
+  const TcPlan w = tc_plan(p, true);
+  TcParams t{};
+  if (grad) p.part = (float*)(ws + w.total);
+  if (fm_status s = tc_setup(t, p, dtype, w, ws, bwd::kCols, bwd::kCols, st)) return s;
+  const bool bf16 = dtype == FM_BF16;
+  bwd::Extra x{};
+  x.q_pad = (p.q_len + 63) / 64 * 64;
+  const long long rows = (long long)p.batch * p.heads * x.q_pad;
+  float* lse2 = (float*)(ws + w.stats);
+  x.lse2 = lse2;
+  x.delta = lse2 + rows;
+  const unsigned blocks = (unsigned)(rows / 16);  // q_pad is a multiple of 64
+  if (bf16) {
+    bwd_stats<__nv_bfloat16><<<blocks, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, lse2 + rows, nullptr);
+  } else {
+    float* peak = (float*)(ws + w.peak);
+    x.peak = peak;
+    const int count = p.batch * p.kv_heads;
+    if (cudaMemsetAsync(peak, 0, sizeof(float) * 2 * count, st) != cudaSuccess) return FM_ERR_CUDA;
+    bwd_stats<__half><<<blocks, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, lse2 + rows, peak);
+    const int rows16 = (p.k_len + 15) / 16;
+    bwd_v_peak<__half><<<dim3(rows16 < 16 ? rows16 : 16, p.kv_heads, p.batch), 256, 0, st>>>(p, peak + count);
+  }
+  if (p.map) {
+    float* bias = (float*)(ws + w.bias);
+    bwd_bias<<<dim3((2 * p.max_distance + 256) / 256, p.heads), 256, 0, st>>>(p, bf16, bias);
+    x.bias = bias;
+  }
+  const int mode = mode_of(p);
+  using Fn = fm_status (*)(const TcParams&, const bwd::Extra&, int, cudaStream_t);
+  const bool small = p.dim <= 64;
+  const Fn queries = small ? (bf16 ? attn_bwd_queries_bf16_64 : attn_bwd_queries_f16_64)
+                           : (bf16 ? attn_bwd_queries_bf16_128 : attn_bwd_queries_f16_128);
+  const Fn keys = small ? (bf16 ? attn_bwd_keys_bf16_64 : attn_bwd_keys_f16_64)
+                        : (bf16 ? attn_bwd_keys_bf16_128 : attn_bwd_keys_f16_128);
+  if (fm_status s = queries(t, x, mode, st)) return s;
+  return keys(t, x, mode, st);
+}
+}  // namespace fm
+
+extern "C" fm_status fm_ops_poll_error(void) {
+  unsigned* word = fm::ops_error_word();
+  if (word == nullptr) return FM_ERR_CUDA;
+  unsigned v = 0;
+  if (cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return FM_ERR_CUDA;
+  if (v != 0 && cudaMemset(word, 0, sizeof v) != cudaSuccess) return FM_ERR_CUDA;
+  return (fm_status)v;
+}

@@ -1,0 +1,210 @@
+// Inline PTX of the tensor-core attention kernels: mbarriers with bounded
+// waits, TMA tile loads, and the tcgen05 matrix unit with its tensor memory.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace fm {
+namespace tc {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// ---- mbarriers --------------------------------------------------------------
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// A wait that ends: after two seconds or 2^26 polls it gives up, records the
+// error and returns false, and so does every wait that finds the error (its
+// own block's flag, or the device's word) while it polls. A role that got
+// false runs to its end without touching tensor memory or issuing copies.
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead, unsigned* err) {
+  const unsigned long long begin = now_ns();
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (bar_try(bar, parity)) return true;
+    if (*dead) return false;
+    if (*(volatile unsigned*)err != 0 || now_ns() - begin > 2000000000ull) break;
+  }
+  *dead = 1;
+  atomicExch(err, 5u /* FM_ERR_KERNEL_TIMEOUT */);
+  return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead, unsigned* err) {
+#pragma unroll 1
+  for (int k = 0; k < 32; ++k)
+    if (bar_try(bar, parity)) return true;
+  return bar_wait_slow(bar, parity, dead, err);
+}
+
+// ---- TMA --------------------------------------------------------------------
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+// box of 64 elements x rows x 1 x 1 at {x, token, head, batch}
+__device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* m, uint32_t bar, int x, int t, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(to),
+      "l"(m), "r"(bar), "r"(x), "r"(t), "r"(h), "r"(b)
+      : "memory");
+}
+// orders this thread's shared-memory writes before later reads by the
+// asynchronous units (TMA, tcgen05)
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_bar_init() {
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// ---- tensor memory ----------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define FM_R8(b, o) "=r"(b[o]), "=r"(b[o + 1]), "=r"(b[o + 2]), "=r"(b[o + 3]), "=r"(b[o + 4]), "=r"(b[o + 5]), "=r"(b[o + 6]), "=r"(b[o + 7])
+#define FM_I8(b, o) "r"(b[o]), "r"(b[o + 1]), "r"(b[o + 2]), "r"(b[o + 3]), "r"(b[o + 4]), "r"(b[o + 5]), "r"(b[o + 6]), "r"(b[o + 7])
+#define FM_P8(b, o) "+r"(b[o]), "+r"(b[o + 1]), "+r"(b[o + 2]), "+r"(b[o + 3]), "+r"(b[o + 4]), "+r"(b[o + 5]), "+r"(b[o + 6]), "+r"(b[o + 7])
+
+// 32 columns of this warp's 32 lanes: thread t gets lane t's row
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : FM_R8(r, 0), FM_R8(r, 8), FM_R8(r, 16), FM_R8(r, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : FM_R8(r, 0), FM_R8(r, 8)
+      : "r"(addr)
+      : "memory");
+}
+// ties loaded registers to the wait before it: what uses them stays behind
+__device__ __forceinline__ void tie32(uint32_t* r) {
+  asm volatile("" : FM_P8(r, 0), FM_P8(r, 8), FM_P8(r, 16), FM_P8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tie16(uint32_t* r) { asm volatile("" : FM_P8(r, 0), FM_P8(r, 8)::"memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::FM_I8(r, 0),
+      FM_I8(r, 8), FM_I8(r, 16), FM_I8(r, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::FM_I8(r, 0),
+      FM_I8(r, 8), "r"(addr)
+      : "memory");
+}
+
+// ---- matrix products --------------------------------------------------------
+// Shared-memory operands are tiles of 128-byte rows with the 128-byte swizzle
+// that TMA writes: 8 rows make a 1024-byte group, groups follow one another.
+// K-major (the summed index runs along the row): a step of 16 elements is 32
+// bytes further. MN-major (the summed index runs over rows): a step of 16 is
+// two groups, 2048 bytes, further, and `across` is the distance between
+// tiles of 64 columns.
+constexpr uint64_t kDescCommon = (uint64_t)1 << 46 | (uint64_t)2 << 61;
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return kDescCommon | (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32;
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t across) {
+  return kDescCommon | (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(across >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32;
+}
+// f32 accumulators; A and B both bf16 or both f16; B K-major or MN-major
+__device__ __forceinline__ uint32_t instr_desc(int m, int n, bool bf16, bool b_mn) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(m >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// arrives on bar once every product issued so far by this thread is done
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ---- registers of a group of four warps -------------------------------------
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- arithmetic -------------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// tanh(x) = 1 - 2 / (e^2x + 1); k2 = 2 log2(e), folded into x by the caller:
+// x2 = 2 log2(e) x. Saturates cleanly at both ends.
+__device__ __forceinline__ float tanh_from(float x2) { return fmaf(-2.f, rcp(ex2(x2) + 1.f), 1.f); }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace tc
+}  // namespace fm

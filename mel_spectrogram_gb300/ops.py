@@ -33,6 +33,7 @@ EXPORTS = [
     "fm_attention_forward",
     "fm_attention_backward",
     "fm_attention_workspace",
+    "fm_ops_poll_error",
 ]
 
 _TYPES = {torch.float32: fb.FM_F32, torch.float16: fb.FM_F16, torch.bfloat16: fb.FM_BF16}
@@ -62,6 +63,7 @@ def _lib():
         L.fm_buckets_create.argtypes, L.fm_buckets_create.restype = [C.POINTER(vp), ci, ci, ci], ci
         L.fm_buckets_map.argtypes, L.fm_buckets_map.restype = [vp, vp], ci
         L.fm_buckets_destroy.argtypes, L.fm_buckets_destroy.restype = [vp], ci
+        L.fm_ops_poll_error.argtypes, L.fm_ops_poll_error.restype = [], ci
         _bound = L
     return _bound
 
@@ -313,6 +315,14 @@ def relative_bias(table: torch.Tensor, q_len: int, k_len: int, q_start: int | No
 
 # ---------------------------------------------------------------------------
 # attention
+
+def poll_error(device: torch.device | str = "cuda") -> int:
+    """Wait for the device, then take and clear the operators' error status:
+    FM_OK, or FM_ERR_KERNEL_TIMEOUT where a bounded wait in a kernel gave up."""
+    with torch.cuda.device(torch.device(device)):
+        torch.cuda.synchronize()
+        return int(_lib().fm_ops_poll_error())
+
 
 class _Call:
     """What one attention call's passes share besides the tensors."""

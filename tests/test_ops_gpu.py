@@ -515,3 +515,9 @@ def test_refusals(ops):
     (d,) = torch.autograd.grad(ops.layer_norm(xg).square().sum(), xg, create_graph=True)
     with pytest.raises(RuntimeError):
         torch.autograd.grad(d.sum(), xg)
+
+
+def test_no_kernel_gave_up(ops):
+    from mel_spectrogram_gb300 import FM_OK
+
+    assert ops.poll_error() == FM_OK
