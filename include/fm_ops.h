@@ -143,6 +143,9 @@ int64_t fm_relative_bias_workspace(const fm_relative_bias_args* args);
  *   lse    : [batch][heads][q_len] f32, log of the softmax's sum; the forward
  *            writes it (NULL: not wanted), the backward reads it.
  *   out    : the backward reads what the forward wrote.
+ *   out_rest: of dtype and out's strides, what rounding took from out; NULL:
+ *            not wanted. Where the backward gets the one that the forward
+ *            wrote, its sum of dout * out is that of the unrounded output.
  *   dtable : [num_buckets][heads] of table_dtype; NULL where not wanted.
  *   workspace: fm_attention_workspace(args, backward) bytes, 16-byte aligned.
  */
@@ -156,6 +159,7 @@ typedef struct {
   void* out;
   int64_t q_s[3], k_s[3], v_s[3], out_s[3];
   float* lse;
+  void* out_rest;
   const int32_t *q_docs, *k_docs, *k_lens, *q_start, *prefix;
   int64_t q_start_all;
   const fm_buckets* buckets;

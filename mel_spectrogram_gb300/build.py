@@ -8,10 +8,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +25,10 @@ LIB = os.path.join(PKG, "libfm_mel.so")
 BUILD_CHECK = os.path.join(PKG, "_build_check")
 LIB_CHECK = os.path.join(PKG, "libfm_mel_check.so")
 CHECK_FLAGS = ["-DFM_BOUNDS_CHECK"]
+# the operators as functions on tensors: one C++ file against torch's headers,
+# linked to libfm_mel.so beside it
+TORCH_SRC = os.path.join(CSRC, "torch", "fm_torch.cpp")
+TORCH_LIB = os.path.join(PKG, "_fm_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2",
@@ -41,6 +47,13 @@ def _sources(build_dir: str = BUILD) -> list[str]:
     if build_dir == BUILD_CHECK:  # the frame-encoder operators have no index-checked build
         found = [f for f in found if not os.path.basename(f).startswith("fm_ops_")]
     return found
+
+
+def _weight(src: str) -> int:
+    """A rough compile time: the attention kernels and the unrolled transforms
+    take longest."""
+    name = os.path.basename(src)
+    return 2 if "_attn_" in name else 1 if "odd" in name or "hops" in name or "longhop" in name else 0
 
 
 def _headers() -> list[str]:
@@ -68,6 +81,38 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
     return r.stderr
 
 
+def _compile_torch() -> str:
+    """The object of fm_torch.cpp; "" where torch is not installed."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return ""
+    out = os.path.join(BUILD, "fm_torch.cpp.o")
+    if not _stale(out, [TORCH_SRC, *_headers(), __file__]):
+        return out
+    inc = os.path.join(os.path.dirname(spec.origin), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}", f"-isystem{inc}",
+           f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-isystem{cuda}",
+           f"-isystem{sysconfig.get_paths()['include']}", "-c", TORCH_SRC, "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for fm_torch.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return out
+
+
+def _link_torch(obj: str) -> None:
+    if not _stale(TORCH_LIB, [obj, LIB]):
+        return
+    libs = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = TORCH_LIB + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libfm_mel.so", f"-L{libs}", "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+
+
 def build(verbose: bool = False, extra: list[str] | None = None, jobs: int | None = None,
           check: bool = False) -> str:
     """Compile and link libfm_mel.so (check=True: the index-checked debug
@@ -86,12 +131,17 @@ def build_many(checks: list[bool], verbose: bool = False, extra: list[str] | Non
     for bdir, _, flags in targets:
         os.makedirs(bdir, exist_ok=True)
         todo += [(s, flags, bdir) for s in _sources(bdir) if extra or _stale(_obj(s, bdir), [s, *hdrs, __file__])]
-    if todo:
-        n = jobs or min(len(todo), max(1, os.cpu_count() or 1))
+    # the largest translation units first, so that none is left for the end
+    todo.sort(key=lambda t: -_weight(t[0]))
+    n = jobs or max(1, os.cpu_count() or 1)
+    torch_obj = ""
+    if todo or False in checks:
         with cf.ThreadPoolExecutor(n) as ex:
+            binding = ex.submit(_compile_torch) if False in checks else None
             for (src, _, _), log in zip(todo, ex.map(lambda t: _compile(*t), todo)):
                 if verbose and log.strip():
                     print(f"[{os.path.basename(src)}]\n{log}", file=sys.stderr)
+            torch_obj = binding.result() if binding else ""
     for bdir, lib, _ in targets:
         objs = [_obj(s, bdir) for s in _sources(bdir)]
         if any(t[2] == bdir for t in todo) or _stale(lib, objs):
@@ -101,6 +151,8 @@ def build_many(checks: list[bool], verbose: bool = False, extra: list[str] | Non
             if r.returncode != 0:
                 raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
             os.replace(tmp, lib)
+    if torch_obj:
+        _link_torch(torch_obj)
     return [lib for _, lib, _ in targets]
 
 

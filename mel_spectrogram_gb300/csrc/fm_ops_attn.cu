@@ -43,6 +43,7 @@ AttnParams params(const fm_attention_args* a) {
   p.q = a->q, p.k = a->k, p.v = a->v;
   p.qs = strides(a->q_s), p.ks = strides(a->k_s), p.vs = strides(a->v_s), p.os = strides(a->out_s);
   p.lse = a->lse;
+  p.rest = a->dtype == FM_F32 ? nullptr : a->out_rest;
   p.q_docs = a->q_docs, p.k_docs = a->k_docs, p.k_lens = a->k_lens, p.q_start = a->q_start, p.prefix = a->prefix;
   p.start_end = a->q_start_all == FM_Q_START_END;
   const int64_t far = 1 << 29;

@@ -19,6 +19,7 @@ struct AttnParams {
   void *out, *dq, *dk, *dv;
   Strides qs, ks, vs, os, dos, dqs, dks, dvs;
   float* lse;
+  void* rest;  // what rounding took from the output, in the output's layout; NULL: not wanted
   const int32_t *q_docs, *k_docs, *k_lens, *q_start, *prefix;
   int start_end, start_all;  // where q_start is NULL: queries end with the keys, or start at start_all
   const int32_t* map;        // NULL: no bucket bias

@@ -154,7 +154,7 @@ __device__ __forceinline__ void clear(float4 (&acc)[4][G]) {
 }
 template <typename T, int G>
 __device__ __forceinline__ void put(T* to, long long stride, int n, int dim, const float4 (&acc)[4][G],
-                                    const float (&f)[4], int tx, int ty) {
+                                    const float (&f)[4], int tx, int ty, T* rest = nullptr) {
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int row = ty * 4 + r;
@@ -165,7 +165,11 @@ __device__ __forceinline__ void put(T* to, long long stride, int n, int dim, con
       const float v[4] = {acc[r][g].x, acc[r][g].y, acc[r][g].z, acc[r][g].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (d + k < dim) to[row * stride + d + k] = from_f<T>(v[k] * f[r]);
+        if (d + k < dim) {
+          const T rounded = from_f<T>(v[k] * f[r]);
+          to[row * stride + d + k] = rounded;
+          if (rest) rest[row * stride + d + k] = from_f<T>(v[k] * f[r] - to_f(rounded));
+        }
     }
   }
 }
@@ -235,7 +239,8 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
     if (p.lse && tx == 0 && i < p.q_len)
       p.lse[((long long)b * p.heads + h) * p.q_len + i] = l[r] == 0.f ? -INFINITY : m[r] + logf(l[r]);
   }
-  put((T*)p.out + b * p.os.b + i0 * p.os.t + h * p.os.h, p.os.t, nq, p.dim, acc, f, tx, ty);
+  const long long at = b * p.os.b + i0 * p.os.t + h * p.os.h;
+  put((T*)p.out + at, p.os.t, nq, p.dim, acc, f, tx, ty, p.rest ? (T*)p.rest + at : nullptr);
 }
 
 constexpr int kBwdCols = 32;  // rows of the streamed tile
@@ -371,9 +376,11 @@ __global__ void __launch_bounds__(256) any_delta(const AttnParams p) {
   const int i = (int)(row % p.q_len), h = (int)(row / p.q_len % p.heads), b = (int)(row / p.q_len / p.heads);
   const T* g = (const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h;
   const T* o = (const T*)p.out_in + b * p.os.b + i * p.os.t + h * p.os.h;
+  const T* rest = p.rest ? (const T*)p.rest + b * p.os.b + i * p.os.t + h * p.os.h : nullptr;
   float s = 0.f;
   if (p.q_docs == nullptr || p.q_docs[(long long)b * p.q_len + i] >= 0)
-    for (int d = threadIdx.x & 31; d < p.dim; d += 32) s = fmaf(to_f(g[d]), to_f(o[d]), s);
+    for (int d = threadIdx.x & 31; d < p.dim; d += 32)
+      s = fmaf(to_f(g[d]), to_f(o[d]) + (rest ? to_f(rest[d]) : 0.f), s);
   s = warp_sum(s);
   if ((threadIdx.x & 31) == 0) p.delta[row] = s;
 }

@@ -299,7 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         }
       } else {
         if (store && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m - kLift<BF16> + log2f(l)) * kLn2;
-        uint16_t* out = (uint16_t*)p.out + b * p.os.b + i * p.os.t + h * p.os.h;
+        const long long place_out = b * p.os.b + i * p.os.t + h * p.os.h;
+        uint16_t* out = (uint16_t*)p.out + place_out;
+        uint16_t* rest = p.rest ? (uint16_t*)p.rest + place_out : nullptr;
 #pragma unroll 1
         for (int x = 0; x < t.dim16; x += 16) {
           uint32_t o[16];
@@ -313,6 +315,15 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
           if (store) {
             *(uint4*)(out + x) = make_uint4(r[0], r[1], r[2], r[3]);
             if (x + 8 < p.dim) *(uint4*)(out + x + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+          }
+          if (rest) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              r[e] = n > 0 ? rest2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f, r[e]) : 0u;
+            if (store) {
+              *(uint4*)(rest + x) = make_uint4(r[0], r[1], r[2], r[3]);
+              if (x + 8 < p.dim) *(uint4*)(rest + x + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+            }
           }
         }
       }

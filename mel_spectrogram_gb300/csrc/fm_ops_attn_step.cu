@@ -294,9 +294,16 @@ __global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
       to[1] = make_float4(acc[4] * f, acc[5] * f, acc[6] * f, acc[7] * f);
     } else {
       if (d == 0 && p.lse) p.lse[stat_row] = lse * kLn2;
-      *(uint4*)((uint16_t*)p.out + b * p.os.b + i * p.os.t + h * p.os.h + d) =
-          make_uint4(pack2<BF16>(acc[0] * f, acc[1] * f), pack2<BF16>(acc[2] * f, acc[3] * f),
-                     pack2<BF16>(acc[4] * f, acc[5] * f), pack2<BF16>(acc[6] * f, acc[7] * f));
+      const long long at = b * p.os.b + i * p.os.t + h * p.os.h + d;
+      uint32_t r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = pack2<BF16>(acc[2 * k] * f, acc[2 * k + 1] * f);
+      *(uint4*)((uint16_t*)p.out + at) = make_uint4(r[0], r[1], r[2], r[3]);
+      if (p.rest) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = rest2<BF16>(acc[2 * k] * f, acc[2 * k + 1] * f, r[k]);
+        *(uint4*)((uint16_t*)p.rest + at) = make_uint4(r[0], r[1], r[2], r[3]);
+      }
     }
   }
 }

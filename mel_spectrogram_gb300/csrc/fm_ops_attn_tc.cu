@@ -148,8 +148,12 @@ __global__ void __launch_bounds__(256) join(const AttnParams p, int splits, cons
   const float f = total == 0.f ? 0.f : 1.f / total;
   if (p.lse && lane == 0) p.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
   if (mine) {
-    uint16_t* out = (uint16_t*)p.out + b * p.os.b + i * p.os.t + h * p.os.h + 4 * lane;
-    *(uint2*)out = make_uint2(tc::pack2<BF16>(acc.x * f, acc.y * f), tc::pack2<BF16>(acc.z * f, acc.w * f));
+    const long long at = b * p.os.b + i * p.os.t + h * p.os.h + 4 * lane;
+    const uint2 r = make_uint2(tc::pack2<BF16>(acc.x * f, acc.y * f), tc::pack2<BF16>(acc.z * f, acc.w * f));
+    *(uint2*)((uint16_t*)p.out + at) = r;
+    if (p.rest)
+      *(uint2*)((uint16_t*)p.rest + at) =
+          make_uint2(tc::rest2<BF16>(acc.x * f, acc.y * f, r.x), tc::rest2<BF16>(acc.z * f, acc.w * f, r.y));
   }
 }
 
@@ -181,11 +185,14 @@ __global__ void __launch_bounds__(256) bwd_stats(const AttnParams p, int q_pad, 
   float s = 0.f, norm = 0.f;
   if (there && lane * 8 < p.dim) {
     const Pack<T, 8> g = *(const Pack<T, 8>*)((const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h + lane * 8);
-    const Pack<T, 8> o = *(const Pack<T, 8>*)((const T*)p.out_in + b * p.os.b + i * p.os.t + h * p.os.h + lane * 8);
+    const long long at = b * p.os.b + i * p.os.t + h * p.os.h + lane * 8;
+    const Pack<T, 8> o = *(const Pack<T, 8>*)((const T*)p.out_in + at);
+    Pack<T, 8> rest{};
+    if (p.rest) rest = *(const Pack<T, 8>*)((const T*)p.rest + at);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float d = to_f(g.v[k]);
-      s = fmaf(d, to_f(o.v[k]), s);
+      s = fmaf(d, to_f(o.v[k]) + to_f(rest.v[k]), s);
       norm = fmaf(d, d, norm);
     }
   }
@@ -249,6 +256,7 @@ bool tc_layout_ok(const AttnParams& p, int64_t dtype, bool backward) {
                     rows_ok(p.dk, p.dks, p.batch, p.k_len, p.kv_heads) &&
                     rows_ok(p.dv, p.dvs, p.batch, p.k_len, p.kv_heads)))
     return false;
+  if (((uintptr_t)p.rest & 15) != 0) return false;
   return rows_ok(p.q, p.qs, p.batch, p.q_len, p.heads) && rows_ok(p.k, p.ks, p.batch, p.k_len, p.kv_heads) &&
          rows_ok(p.v, p.vs, p.batch, p.k_len, p.kv_heads) && rows_ok(p.out, p.os, p.batch, p.q_len, p.heads);
 }

@@ -206,5 +206,20 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// what packing took from each of the two
+template <bool BF16>
+__device__ __forceinline__ uint32_t rest2(float lo, float hi, uint32_t packed) {
+  float a, z;
+  if (BF16) {
+    a = __uint_as_float(packed << 16);
+    z = __uint_as_float(packed & 0xffff0000u);
+  } else {
+    const __half2 h = *reinterpret_cast<const __half2*>(&packed);
+    a = __low2float(h);
+    z = __high2float(h);
+  }
+  return pack2<BF16>(lo - a, hi - z);
+}
+
 }  // namespace tc
 }  // namespace fm
