@@ -303,6 +303,10 @@ TcPlan tc_plan(const AttnParams& p, bool backward) {
 fm_status tc_setup(TcParams& t, const AttnParams& p, int64_t dtype, const TcPlan& w, char* ws, int q_rows, int k_rows,
                    cudaStream_t st) {
   const bool bf16 = dtype == FM_BF16;
+  // the encoder is a driver call: it needs the device's context on this
+  // thread, which a thread that only took cached memory so far does not have
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return FM_ERR_CUDA;
   t.p = p;
   t.err = ops_error_word();
   if (t.err == nullptr) return FM_ERR_CUDA;

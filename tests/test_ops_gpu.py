@@ -464,6 +464,30 @@ def test_attention_graph(ops):
         ref.close(out, *ref.attention(q, k, v, table=table, k_lens=lens)["out"], "replayed")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_on_new_threads(ops, dtype):
+    # a thread whose first CUDA work is the operator, its memory from the cache
+    import threading
+
+    q, k, v, dy, g = make((2, 300, 300, 4, 2, 64), dtype)
+    got = {}
+
+    def once(name):
+        leaves = [t.detach().requires_grad_() for t in (q, k, v)]
+        out = ops.attention(*leaves, causal=True)
+        got[name] = [out.detach(), *torch.autograd.grad(out, leaves, dy)]
+
+    once("here")
+    again = got.pop("here")
+    torch.cuda.synchronize()
+    for n in range(3):
+        t = threading.Thread(target=once, args=(n,))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(again, got.pop(n)))
+
+
 # ---------------------------------------------------------------------------
 # refusals
 
