@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
   unsigned char* mem = raw + (base - smem_u32(raw));
   auto bar = [&](int n) { return base + L::kBars + 8 * n; };
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one per warp
   const bool has_bias = MODE == 1 || (MODE == 2 && p.map);
   const int D = p.max_distance, nbias = L::bias_floats(D);
   const bool grad = !KEYS && p.part != nullptr;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
 
   constexpr uint32_t kAcc = 256;  // columns: S0 T0 S1 T1 (64 each), dv or nothing, dk or dq
   if (warp < 8) {
-    take_registers<232>();
+    take_registers<224>();
     const int w = warp >> 2, lane_row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t ts = tmem + lanes + w * 128, tt = ts + 64;
@@ -288,12 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       float cc = c;
       if (MODE == 2) {
         if (p.cap > 0.f) {
-          const float c2 = 2.f * kLog2e * p.scale / p.cap, out = p.cap * kLog2e;
+          cap_scores(s, p.scale, p.cap);
+          const float2 in = both(1.f / (p.cap * kLog2e));
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            const float th = tanh_from(s[j] * c2);
-            s[j] = out * th;
-            slope[j] = 1.f - th * th;
+          for (int j = 0; j < 64; j += 2) {
+            const float2 th = mul2(make_float2(s[j], s[j + 1]), in), f = fma2(make_float2(-th.x, -th.y), th, both(1.f));
+            slope[j] = f.x;
+            slope[j + 1] = f.y;
           }
           cc = 1.f;
         } else {
@@ -302,24 +303,48 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         }
       }
       if (has_bias) {
-        const bool above = KEYS ? o0 - 63 >= D : o0 >= D, below = KEYS ? o0 <= -D : o0 + 63 <= -D;
+        // one choice for a warp's rows, as in the forward pass
+        const bool above = __all_sync(0xffffffffu, (KEYS ? o0 - 63 : o0) >= D);
+        const bool below = __all_sync(0xffffffffu, (KEYS ? o0 : o0 + 63) <= -D);
         if (above || below) {
-          const float v = bias[above ? 2 * (D + kBiasPad) : 0];
+          const float2 v = both(bias[above ? 2 * (D + kBiasPad) : 0]);
 #pragma unroll
-          for (int j = 0; j < 64; ++j) s[j] = fmaf(s[j], cc, v);
+          for (int j = 0; j < 64; j += 2) {
+            const float2 z = fma2(make_float2(s[j], s[j + 1]), both(cc), v);
+            s[j] = z.x;
+            s[j + 1] = z.y;
+          }
         } else {
           const float* at = bias + (o0 + D + kBiasPad);
 #pragma unroll
-          for (int j = 0; j < 64; ++j) s[j] = fmaf(s[j], cc, KEYS ? at[-j] : at[j]);
+          for (int j = 0; j < 64; j += 2) {
+            const float2 v = KEYS ? make_float2(at[-j], at[-j - 1]) : make_float2(at[j], at[j + 1]);
+            const float2 z = fma2(make_float2(s[j], s[j + 1]), both(cc), v);
+            s[j] = z.x;
+            s[j + 1] = z.y;
+          }
         }
-      } else if (MODE == 2) {
+      } else if (MODE == 2 && !(p.cap > 0.f)) {
 #pragma unroll
         for (int j = 0; j < 64; ++j) s[j] *= cc;
       }
       if (MODE == 2 && p.slopes) {
-        const float f0 = (float)o0;
+        const int far_end = KEYS ? o0 - 63 : o0 + 63;
+        if (__all_sync(0xffffffffu, o0 >= 0 && far_end >= 0) || __all_sync(0xffffffffu, o0 <= 0 && far_end <= 0)) {
+          // one sign: |o| slope is linear in the column
+          const float g = o0 > 0 || far_end > 0 ? -slope2 : slope2, base_z = g * (float)o0, step = KEYS ? -g : g;
 #pragma unroll
-        for (int j = 0; j < 64; ++j) s[j] = fmaf(-slope2, fabsf(KEYS ? f0 - (float)j : f0 + (float)j), s[j]);
+          for (int j = 0; j < 64; j += 2) {
+            const float2 z = add2(make_float2(s[j], s[j + 1]),
+                                  fma2(both(step), make_float2((float)j, (float)(j + 1)), both(base_z)));
+            s[j] = z.x;
+            s[j + 1] = z.y;
+          }
+        } else {
+          const float f0 = (float)o0;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) s[j] = fmaf(-slope2, fabsf(KEYS ? f0 - (float)j : f0 + (float)j), s[j]);
+        }
       }
       uint64_t seen = ~0ull;  // bit j: column j is seen
       if (masked) {
@@ -337,10 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       for (int j = 0; j < 64; j += 4) {
         float4 q = make_float4(row_lse, row_lse, row_lse, row_lse);
         if (KEYS) q = *(const float4*)(lse + j);
-        s[j] = ex2(MODE == 0 ? fmaf(s[j], c, -q.x) : s[j] - q.x);
-        s[j + 1] = ex2(MODE == 0 ? fmaf(s[j + 1], c, -q.y) : s[j + 1] - q.y);
-        s[j + 2] = ex2(MODE == 0 ? fmaf(s[j + 2], c, -q.z) : s[j + 2] - q.z);
-        s[j + 3] = ex2(MODE == 0 ? fmaf(s[j + 3], c, -q.w) : s[j + 3] - q.w);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const float2 z = make_float2(s[j + e], s[j + e + 1]), n2 = e ? make_float2(-q.z, -q.w) : make_float2(-q.x, -q.y);
+          const float2 a = MODE == 0 ? fma2(z, both(c), n2) : add2(z, n2);
+          s[j + e] = ex2(a.x);
+          s[j + e + 1] = ex2(a.y);
+        }
       }
       if (masked) {
 #pragma unroll
@@ -362,10 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
           float4 q = make_float4(row_delta, row_delta, row_delta, row_delta);
           if (KEYS) q = *(const float4*)(delta + 32 * half + j);
           float* a = s + 32 * half + j;
-          a[0] *= __uint_as_float(d[j]) - q.x;
-          a[1] *= __uint_as_float(d[j + 1]) - q.y;
-          a[2] *= __uint_as_float(d[j + 2]) - q.z;
-          a[3] *= __uint_as_float(d[j + 3]) - q.w;
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const float2 g = add2(make_float2(__uint_as_float(d[j + e]), __uint_as_float(d[j + e + 1])),
+                                  e ? make_float2(-q.z, -q.w) : make_float2(-q.x, -q.y));
+            const float2 r = mul2(make_float2(a[e], a[e + 1]), g);
+            a[e] = r.x;
+            a[e + 1] = r.y;
+          }
         }
       }
       if (masked) {  // 0 times what an unused frame's dP holds
@@ -376,10 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       // sums it in 32 bits
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        float a = s[2 * j], z = s[2 * j + 1];
-        if (!BF16) a *= tau, z *= tau;
-        if (MODE == 2) a *= slope[2 * j], z *= slope[2 * j + 1];
-        pk[j] = pack2<BF16>(a, z);
+        float2 a = make_float2(s[2 * j], s[2 * j + 1]);
+        if (!BF16) a = mul2(a, both(tau));
+        if (MODE == 2) a = mul2(a, make_float2(slope[2 * j], slope[2 * j + 1]));
+        pk[j] = pack2<BF16>(a.x, a.y);
       }
       tmem_st32(tt, pk);
       wait_st();
@@ -467,10 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       fence_before();
     }
   } else {
-    give_registers<40>();
-    if (warp == 8) {
-      if (tid % 32 == 0 && n > 0) {
-        // ---- copies: the owned tile once, then streamed tiles
+    give_registers<56>();
+    const uint32_t lead = elect();
+    if (warp == 8 && n > 0) {
+      // ---- copies: the owned tile once, then streamed tiles
+      if (lead) {
         const uint32_t own = bar(kOwnFull);
         bar_expect(own, 2 * L::kOwn);
         for (int y = 0; y < L::kBoxes; ++y)
@@ -485,12 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
               tma_load(to + L::kOwn, &t.gm, own, 64 * y, row, h0 * t.g_mh, b * t.g_mb);
             }
           }
-        for (int it = 0; it < n; ++it) {
-          const int s = it % L::kSlots, round = it / L::kSlots;
-          if (!bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err)) break;
+      }
+      int tile = sb, h = h0;
+      for (int it = 0; it < n; ++it) {
+        const int s = it % L::kSlots, round = it / L::kSlots;
+        const bool ok = bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lead) {
           const uint32_t full = bar(kFull + s), to = base + L::kRing + s * L::kSlot;
-          const int hh = KEYS ? it / per_head : 0, c0 = (sb + (it - hh * per_head)) * kCols, h = h0 + hh;
+          const int c0 = tile * kCols;
           bar_expect(full, 2 * L::kHalf + (KEYS ? 2 * kCols * 4 : 0));
+#pragma unroll
           for (int y = 0; y < L::kBoxes; ++y) {
             if (KEYS) {
               tma_load(to + y * L::kBox, &t.qm, full, 64 * y, c0, h * t.q_mh, b * t.q_mb);
@@ -506,52 +544,62 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
             bulk_load(to + L::kStats + kCols * 4, x.delta + at, kCols * 4, full);
           }
         }
+        __syncwarp();
+        if (++tile == se) tile = sb, ++h;
       }
-    } else if (warp == 9) {
-      if (tid % 32 == 0 && n > 0) {
-        // ---- products
-        const uint32_t id_s = instr_desc(kTile, kCols, BF16, false), id_a = instr_desc(kTile, t.dim16, BF16, true);
-        const int ksteps = t.dim16 / 16;
-        auto slot_at = [&](int it) { return base + L::kRing + (it % L::kSlots) * L::kSlot; };
-        auto full = [&](int it) {
-          return bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err);
-        };
-        auto scores = [&](int it) {
-          const uint32_t d = tmem + (it & 1) * 128, from = slot_at(it);
-          for (int op = 0; op < 2; ++op)
-            for (int k = 0; k < ksteps; ++k)
-              mma_ss(d + op * 64, desc_k(base + op * L::kOwn + (k / 4) * L::kOwnBox + (k % 4) * 32),
-                     desc_k(from + op * L::kHalf + (k / 4) * L::kBox + (k % 4) * 32), id_s, k > 0);
-          mma_commit(bar(kSFull + (it & 1)));
-        };
-        bool ok = bar_wait(bar(kOwnFull), 0, &dead, t.err);
-        for (int it = 0; ok && it < 2 && it < n; ++it) {
-          ok = full(it);
-          if (ok) scores(it);
-        }
-        for (int it = 0; ok && it < n; ++it) {
-          const int w = it & 1;
-          ok = bar_wait(bar(kPReady + w), (it >> 1) & 1, &dead, t.err);
-          if (!ok) break;
-          fence_after();
-          const uint32_t from = slot_at(it);
-          if (KEYS)
-            for (int k = 0; k < kCols / 16; ++k)
-              mma_ts(tmem + kAcc, tmem + w * 128 + k * 8, desc_mn(from + L::kHalf + k * 2048, L::kBox), id_a,
-                     it > 0 || k > 0);
+    } else if (warp == 9 && n > 0) {
+      // ---- products
+      const uint32_t id_s = instr_desc(kTile, kCols, BF16, false), id_a = instr_desc(kTile, t.dim16, BF16, true);
+      const int ksteps = t.dim16 / 16;
+      auto wait = [&](int n_bar, uint32_t parity) {
+        const bool ok = bar_wait(bar(n_bar), parity, &dead, t.err);
+        return __all_sync(0xffffffffu, ok) != 0;
+      };
+      auto scores = [&](int w, int slot) {
+        const uint32_t d = tmem + w * 128, from = base + L::kRing + slot * L::kSlot;
+#pragma unroll
+        for (int op = 0; op < 2; ++op)
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)
+            mma_ss(k < ksteps ? lead : 0u, d + op * 64,
+                   desc_k(base + op * L::kOwn + (k / 4) * L::kOwnBox + (k % 4) * 32),
+                   desc_k(from + op * L::kHalf + (k / 4) * L::kBox + (k % 4) * 32), id_s, k > 0);
+        mma_commit(lead, bar(kSFull + w));
+      };
+      // the ring's slot and round two tiles ahead of the one being summed
+      int ahead = 0, round = 0, slot = 0;
+      bool ok = wait(kOwnFull, 0);
+      auto next_scores = [&](int w) {
+        ok = ok && wait(kFull + ahead, round);
+        if (!ok) return;
+        scores(w, ahead);
+        if (++ahead == L::kSlots) ahead = 0, round ^= 1;
+      };
+      next_scores(0);
+      if (n > 1) next_scores(1);
+      for (int it = 0; ok && it < n; ++it) {
+        const int w = it & 1;
+        ok = wait(kPReady + w, (it >> 1) & 1);
+        if (!ok) break;
+        fence_after();
+        const uint32_t from = base + L::kRing + slot * L::kSlot;
+        if (KEYS) {
+#pragma unroll
           for (int k = 0; k < kCols / 16; ++k)
-            mma_ts(tmem + kAcc + DP, tmem + w * 128 + 64 + k * 8, desc_mn(from + k * 2048, L::kBox), id_a,
+            mma_ts(lead, tmem + kAcc, tmem + w * 128 + k * 8, desc_mn(from + L::kHalf + k * 2048, L::kBox), id_a,
                    it > 0 || k > 0);
-          mma_commit(bar(kEmpty + it % L::kSlots));
-          if (it + 2 < n) {
-            // in order of issue: these scores replace P and dS only after the
-            // products above have read them
-            ok = full(it + 2);
-            if (ok) scores(it + 2);
-          }
         }
-        if (ok) mma_commit(bar(kDone));
+#pragma unroll
+        for (int k = 0; k < kCols / 16; ++k)
+          mma_ts(lead, tmem + kAcc + DP, tmem + w * 128 + 64 + k * 8, desc_mn(from + k * 2048, L::kBox), id_a,
+                 it > 0 || k > 0);
+        mma_commit(lead, bar(kEmpty + slot));
+        if (++slot == L::kSlots) slot = 0;
+        // in order of issue: these scores replace P and dS only after the
+        // products above have read them
+        if (it + 2 < n) next_scores(w);
       }
+      if (ok) mma_commit(lead, bar(kDone));
     }
   }
   __syncthreads();

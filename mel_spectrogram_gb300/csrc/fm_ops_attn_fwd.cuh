@@ -57,32 +57,55 @@ struct RowScores {
   static __device__ __forceinline__ void apply(float (&s)[128], const AttnParams& p, float c, const float* bias,
                                                float slope2, int o0, int lim, int qd, const int32_t* kd) {
     if (MODE == 2 && p.cap > 0.f) {
-      const float c2 = 2.f * kLog2e * p.scale / p.cap, out = p.cap * kLog2e;
-#pragma unroll
-      for (int j = 0; j < 128; ++j) s[j] = out * tanh_from(s[j] * c2);
+      cap_scores(s, p.scale, p.cap);
       c = 1.f;
     }
     const int D = p.max_distance;
     if (MODE == 1 || (MODE == 2 && p.map)) {
-      // o0 differs by at most 127 between a tile's rows: all of a warp's rows
-      // take the same of these unless they stand near an end of the map
-      if (o0 >= D || o0 + 127 <= -D) {
-        const float b = bias[o0 >= D ? 2 * (D + kBiasPad) : 0];
+      // rows of a warp differ by 31 in o0: one choice for all of them (the
+      // array holds copies of its ends far enough)
+      const bool above = __all_sync(0xffffffffu, o0 >= D), below = __all_sync(0xffffffffu, o0 + 127 <= -D);
+      if (above || below) {
+        const float2 b = both(bias[above ? 2 * (D + kBiasPad) : 0]);
 #pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = fmaf(s[j], c, b);
+        for (int j = 0; j < 128; j += 2) {
+          const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c), b);
+          s[j] = z.x;
+          s[j + 1] = z.y;
+        }
       } else {
         const float* at = bias + (o0 + D + kBiasPad);
 #pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = fmaf(s[j], c, at[j]);
+        for (int j = 0; j < 128; j += 2) {
+          const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c), make_float2(at[j], at[j + 1]));
+          s[j] = z.x;
+          s[j + 1] = z.y;
+        }
       }
-    } else if (MODE == 2) {
+    } else if (MODE == 2 && !(p.cap > 0.f)) {
 #pragma unroll
-      for (int j = 0; j < 128; ++j) s[j] *= c;
+      for (int j = 0; j < 128; j += 2) {
+        const float2 z = mul2(make_float2(s[j], s[j + 1]), both(c));
+        s[j] = z.x;
+        s[j + 1] = z.y;
+      }
     }
     if (MODE == 2 && p.slopes) {
-      const float f0 = (float)o0;
+      if (__all_sync(0xffffffffu, o0 >= 0) || __all_sync(0xffffffffu, o0 + 127 <= 0)) {
+        // one sign: |o0 + j| slope is linear in j
+        const float g = o0 >= 0 ? -slope2 : slope2, base = g * (float)o0;
 #pragma unroll
-      for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope2, fabsf(f0 + (float)j), s[j]);
+        for (int j = 0; j < 128; j += 2) {
+          const float2 z = add2(make_float2(s[j], s[j + 1]),
+                                fma2(both(g), make_float2((float)j, (float)(j + 1)), both(base)));
+          s[j] = z.x;
+          s[j + 1] = z.y;
+        }
+      } else {
+        const float f0 = (float)o0;
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope2, fabsf(f0 + (float)j), s[j]);
+      }
     }
     if (MASKED) {
 #pragma unroll
@@ -110,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   unsigned char* mem = raw + (base - smem_u32(raw));
   float* bias = (float*)(mem + L::kBias);
   auto bar = [&](int n) { return base + L::kBars + 8 * n; };
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one per warp
 
   const int split = blockIdx.z % t.splits, b = blockIdx.z / t.splits, h = blockIdx.y, hk = h / p.group;
   // causal rows late in the sequence see the most keys: they go first
@@ -163,9 +186,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
 
   constexpr uint32_t kO = 256;  // columns of O0; O1 follows at kO + DP
   // registers: the block starts with 3 groups x 168; the softmax threads, which
-  // hold 128 scores each, take 232 and leave the others 40 (2 x 232 + 40 = 504)
+  // hold 128 scores each, take 224 and leave the others 56 (2 x 224 + 56 = 504)
   if (warp < 8) {
-    take_registers<232>();
+    take_registers<224>();
     // ---- softmax: one query row a thread
     const int w = warp >> 2, lane_row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 * (warp % 4) in bits 16 up
@@ -251,22 +274,23 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         }
       }
       const float m0 = (m == -INFINITY ? 0.f : m) - kLift<BF16>;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float a = s[64 * half + 2 * e], z = s[64 * half + 2 * e + 1];
-          const float pa = ex2(MODE == 0 ? fmaf(a, c, -m0) : a - m0);
-          const float pz = ex2(MODE == 0 ? fmaf(z, c, -m0) : z - m0);
-          sum[e & 3] += pa + pz;
+          const float2 z = make_float2(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]);
+          const float2 a = MODE == 0 ? fma2(z, both(c), both(-m0)) : add2(z, both(-m0));
+          const float2 q = make_float2(ex2(a.x), ex2(a.y));
+          sum[e & 1] = add2(sum[e & 1], q);
           // weights go to the product in the inputs' type: the sum keeps 32 bits
-          pk[e] = pack2<BF16>(pa, pz);
+          pk[e] = pack2<BF16>(q.x, q.y);
         }
         tmem_st32(ts + 32 * half, pk);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
       wait_st();
       fence_before();
       __syncwarp();
@@ -330,72 +354,88 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       fence_before();
     }
   } else {
-    give_registers<40>();
-    if (warp == 8) {
-      if (tid % 32 == 0 && n > 0) {
-        // ---- copies: q once, then K and V tiles in turn through the ring
+    give_registers<56>();
+    const uint32_t lead = elect();
+    if (warp == 8 && n > 0) {
+      // ---- copies: q once, then K and V tiles in turn through the ring
+      if (lead) {
         bar_expect(bar(kQFull), 2 * L::kOperand);
         for (int w = 0; w < 2; ++w)
           for (int x = 0; x < L::kBoxes; ++x)
             tma_load(base + w * L::kOperand + x * L::kBox, &t.qm, bar(kQFull), 64 * x, q0 + w * kTile, h * t.q_mh,
                      b * t.q_mb);
-        for (int it = 0; it < 2 * n; ++it) {
-          const int s = it % L::kSlots, round = it / L::kSlots;
-          if (!bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err)) break;
+      }
+      for (int it = 0; it < 2 * n; ++it) {
+        const int s = it % L::kSlots, round = it / L::kSlots;
+        const bool ok = bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lead) {
           bar_expect(bar(kFull + s), L::kOperand);
           const int row = (tb + it / 2) * kTile;
+          const uint32_t to = base + L::kRing + s * L::kOperand;
+#pragma unroll
           for (int x = 0; x < L::kBoxes; ++x) {
-            const uint32_t to = base + L::kRing + s * L::kOperand + x * L::kBox;
-            if (it & 1) tma_load(to, &t.vm, bar(kFull + s), 64 * x, row, hk * t.v_mh, b * t.v_mb);
-            else tma_load(to, &t.km, bar(kFull + s), 64 * x, row, hk * t.k_mh, b * t.k_mb);
+            if (it & 1) tma_load(to + x * L::kBox, &t.vm, bar(kFull + s), 64 * x, row, hk * t.v_mh, b * t.v_mb);
+            else tma_load(to + x * L::kBox, &t.km, bar(kFull + s), 64 * x, row, hk * t.k_mh, b * t.k_mb);
           }
         }
+        __syncwarp();
       }
-    } else if (warp == 9) {
-      if (tid % 32 == 0 && n > 0) {
-        // ---- products
-        const uint32_t id_s = instr_desc(kTile, kTile, BF16, false), id_o = instr_desc(kTile, t.dim16, BF16, true);
-        const int ksteps = t.dim16 / 16;
-        auto scores = [&](int w, uint32_t slot) {
-          for (int k = 0; k < ksteps; ++k) {
-            const uint32_t at = (k / 4) * L::kBox + (k % 4) * 32;
-            mma_ss(tmem + w * kTile, desc_k(base + w * L::kOperand + at),
-                   desc_k(base + L::kRing + slot * L::kOperand + at), id_s, k > 0);
-          }
-          mma_commit(bar(kSFull + w));
-        };
-        auto slot_of = [&](int it) { return (uint32_t)(it % L::kSlots); };
-        auto ring_wait = [&](int it) {
-          return bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err);
-        };
-        bool ok = bar_wait(bar(kQFull), 0, &dead, t.err) && ring_wait(0);
-        if (ok) {
-          scores(0, slot_of(0));
-          scores(1, slot_of(0));
-          mma_commit(bar(kEmpty + slot_of(0)));
+    } else if (warp == 9 && n > 0) {
+      // ---- products
+      const uint32_t id_s = instr_desc(kTile, kTile, BF16, false), id_o = instr_desc(kTile, t.dim16, BF16, true);
+      const int ksteps = t.dim16 / 16;
+      auto scores = [&](int w, int slot) {
+        const uint32_t a = base + w * L::kOperand, from = base + L::kRing + slot * L::kOperand;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t at = (k / 4) * L::kBox + (k % 4) * 32;
+          mma_ss(k < ksteps ? lead : 0u, tmem + w * kTile, desc_k(a + at), desc_k(from + at), id_s, k > 0);
         }
-        for (int j = 0; ok && j < n; ++j) {
-          const uint32_t sv = slot_of(2 * j + 1), sk = slot_of(2 * j + 2);
-          for (int w = 0; ok && w < 2; ++w) {
-            ok = bar_wait(bar(kPReady + w), j & 1, &dead, t.err) && (w || ring_wait(2 * j + 1));
+        mma_commit(lead, bar(kSFull + w));
+      };
+      auto wait = [&](int n_bar, uint32_t parity) {
+        const bool ok = bar_wait(bar(n_bar), parity, &dead, t.err);
+        return __all_sync(0xffffffffu, ok) != 0;
+      };
+      // slot and round of the ring's next entries: V of this tile, K of the next
+      int sv = 1, rv = 0, sk = 2, rk = 0;
+      auto advance = [&](int& s, int& r) {
+        s += 2;
+        if (s >= L::kSlots) s -= L::kSlots, r ^= 1;
+      };
+      bool ok = wait(kQFull, 0) && wait(kFull, 0);
+      if (ok) {
+        scores(0, 0);
+        scores(1, 0);
+        mma_commit(lead, bar(kEmpty));
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        const bool more = j + 1 < n;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          ok = ok && (w || wait(kFull + sv, rv)) && wait(kPReady + w, j & 1);
+          if (!ok) break;
+          fence_after();
+          const uint32_t from = base + L::kRing + sv * L::kOperand;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(lead, tmem + kO + w * DP, tmem + w * kTile + k * 8, desc_mn(from + k * 2048, L::kBox), id_o,
+                   j > 0 || k > 0);
+          if (w) mma_commit(lead, bar(kEmpty + sv));
+          if (more) {
+            // the tensor unit runs products in the order of issue: these
+            // scores replace P only after the product above has read it
+            ok = w || wait(kFull + sk, rk);
             if (!ok) break;
-            fence_after();
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tmem + kO + w * DP, tmem + w * kTile + k * 8,
-                     desc_mn(base + L::kRing + sv * L::kOperand + k * 2048, L::kBox), id_o, j > 0 || k > 0);
-            if (w) mma_commit(bar(kEmpty + sv));
-            if (j + 1 < n) {
-              // the tensor unit runs products in the order of issue: these
-              // scores replace P only after the product above has read it
-              if (!w) ok = ring_wait(2 * j + 2);
-              if (!ok) break;
-              scores(w, sk);
-              if (w) mma_commit(bar(kEmpty + sk));
-            } else {
-              mma_commit(bar(kOFull + w));
-            }
+            scores(w, sk);
+            if (w) mma_commit(lead, bar(kEmpty + sk));
+          } else {
+            mma_commit(lead, bar(kOFull + w));
           }
         }
+        advance(sv, rv);
+        advance(sk, rk);
       }
     }
   }

@@ -154,23 +154,34 @@ __device__ __forceinline__ uint32_t instr_desc(int m, int n, bool bf16, bool b_m
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
          (uint32_t)(m >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// Products are issued by a whole converged warp, of which one lane (`lead`)
+// executes them: addresses and descriptors then stay in uniform registers.
+// Issued from one lane's own branch they cost about a hundred cycles each.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead)
       : "memory");
 }
 // arrives on bar once every product issued so far by this thread is done
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+      : "memory");
 }
 
 // ---- registers of a group of four warps -------------------------------------
@@ -197,6 +208,75 @@ __device__ __forceinline__ float rcp(float x) {
 // tanh(x) = 1 - 2 / (e^2x + 1); k2 = 2 log2(e), folded into x by the caller:
 // x2 = 2 log2(e) x. Saturates cleanly at both ends.
 __device__ __forceinline__ float tanh_from(float x2) { return fmaf(-2.f, rcp(ex2(x2) + 1.f), 1.f); }
+
+// pairs of 32-bit floats in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Scores capped and brought to base 2: z = cap log2(e) tanh(s scale / cap).
+// Where every score of a warp's tile is small against the cap (|x| <= 3/4,
+// the usual case) tanh(x) / x is a polynomial of degree 5 in x^2, fitted for
+// the least relative error there (2.9e-8): five packed multiply-adds instead of
+// two trips to the special-function unit, which the weights' 2^z needs.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&s)[N], float scale, float cap) {
+  const float k = scale / cap, out = cap * 1.4426950408889634f;
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < N; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(s[j]));
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  if (__all_sync(0xffffffffu, most * fabsf(k) <= 0.75f)) {
+    const float k2 = k * k, f = out * k;
+    const float tanh_over_x[6] = {0.999999971f,   -0.333329589f, 0.13325406f,
+                                  -0.0533444307f, 0.0195829084f, -0.00471625688f};
+    float2 c[6];
+    float power = f;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      c[i] = both(tanh_over_x[i] * power);
+      power *= k2;
+    }
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      const float2 x = make_float2(s[j], s[j + 1]), q = mul2(x, x);
+      float2 r = fma2(c[5], q, c[4]);
+      r = fma2(r, q, c[3]);
+      r = fma2(r, q, c[2]);
+      r = fma2(r, q, c[1]);
+      r = fma2(r, q, c[0]);
+      r = mul2(r, x);
+      s[j] = r.x;
+      s[j + 1] = r.y;
+    }
+  } else {
+    const float c2 = 2.f * 1.4426950408889634f * k;
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = out * tanh_from(s[j] * c2);
+  }
+}
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
