@@ -10,10 +10,13 @@
 // but no partial dq in memory and no atomics.
 //
 // An owned row is a lane of tensor memory. Streamed tiles are 64 wide, and
-// two groups of 128 threads take them in turn: each reads its S and dP, and
-// writes P and dS (16 bits) over them, from where the second products take
-// them as their A operand. Warp 8 copies, warp 9 issues products, so one
-// group's arithmetic runs beside the other group's products.
+// two groups of 256 threads take them in turn, two threads a row with 32
+// columns each: a thread reads its S and dP, and writes P and dS (16 bits)
+// over them, from where the second products take them as their A operand.
+// Warp 16 copies, warp 17 issues products, so one group's arithmetic runs
+// beside the other group's products. (With one thread a row a tile's
+// arithmetic took twice its products' time, and the code of the biased modes
+// did not stay in the instruction cache.)
 //
 // Bound: the score products, whose 128 x 64 x 16 steps read 6 KB of shared
 // memory for 32 cycles of arithmetic (the tensor unit takes 128 bytes a cycle).
@@ -26,8 +29,10 @@ namespace bwd {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kGroup = 256;
 constexpr int kCols = 64;      // rows of a streamed tile
+constexpr int kColumns = kCols / 2;  // a thread's share
 constexpr int kDiagPad = 192;  // room beside the bias gradient for a tile's diagonals
 constexpr int kChains = 4, kChainEntries = 48;
 // f16 operands: P is kept 2^15 larger (weights are at most 1), and dS times a
@@ -56,17 +61,17 @@ struct Smem {
   static size_t bytes(int max_distance, bool bias, bool grad) {
     size_t n = 1024 + kBias;
     if (bias) n += sizeof(float) * (KEYS ? 2 : 1) * bias_floats(max_distance);
-    if (grad) n += sizeof(float) * (2 * diag_floats(max_distance) + 8 * kChains * kChainEntries + 512);
+    if (grad) n += sizeof(float) * (2 * diag_floats(max_distance) + 8 * kChains * kChainEntries + 1024);
     return n;
   }
 };
 enum { kFull = 0, kEmpty = 8, kOwnFull = 16, kSFull = 17, kPReady = 19, kDone = 21 };
 
-// a barrier of a group's 128 threads that also tells whether all are well
+// a barrier of a group's 256 threads that also tells whether all are well
 __device__ __forceinline__ bool group_ok(int group, bool ok) {
   int r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, %2, 256, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"((int)ok), "r"(group + 1)
       : "memory");
@@ -115,8 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   float* bias_mem = (float*)(mem + L::kBias);
   float* diag_mem = bias_mem + (has_bias ? (KEYS ? 2 : 1) * nbias : 0);  // [2][ndiag]
   const int ndiag = L::diag_floats(D);
-  float* chain_mem = diag_mem + 2 * ndiag;  // [8 warps][kChains][kChainEntries]
-  float* far_mem = chain_mem + 8 * kChains * kChainEntries;  // [2][256]
+  float* chain_mem = diag_mem + 2 * ndiag;  // [group][quarter of the rows][kChains][kChainEntries]
+  float* far_mem = chain_mem + 8 * kChains * kChainEntries;  // [2][512]
 
   const int b = blockIdx.z;
   const int r0 = (!KEYS && p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * kTile;
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   if (tid == 0) {
     for (int i = 0; i < L::kSlots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
     bar_init(bar(kOwnFull), 1);
-    for (int w = 0; w < 2; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 4);
+    for (int w = 0; w < 2; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 8);
     bar_init(bar(kDone), 1);
     fence_bar_init();
     dead = 0;
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     tma_prefetch(&t.vm);
     tma_prefetch(&t.gm);
   }
-  if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
   auto fill = [&](float* to, int h, int at, int step) {
     for (int i = at; i < nbias; i += step) to[i] = x.bias[(long long)h * (2 * D + 1) + min(max(i - kBiasPad, 0), 2 * D)];
   };
@@ -176,11 +181,13 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   const int per_head = max(se - sb, 0), n = per_head * (KEYS ? p.group : 1);
 
   constexpr uint32_t kAcc = 256;  // columns: S0 T0 S1 T1 (64 each), dv or nothing, dk or dq
-  if (warp < 8) {
-    take_registers<224>();
-    const int w = warp >> 2, lane_row = tid & 127;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t ts = tmem + lanes + w * 128, tt = ts + 64;
+  // registers: 5 groups of warps x 96 at the start; 4 x 104 + 64 = 480
+  if (warp < 16) {
+    take_registers<104>();
+    const int w = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, lane = tid & 31;
+    const int lane_row = quarter * 32 + lane, in_group = half * 128 + lane_row;
+    const uint32_t lanes = (uint32_t)quarter << 21;
+    const uint32_t ts = tmem + lanes + w * 128 + half * kColumns, tt = ts + 64;
     const int row = r0 + lane_row;  // the key or the query
     const float c = p.scale * kLog2e;
     const float sigma = BF16 ? 1.f : ds_scale(x, b * p.kv_heads + hk, p.batch * p.kv_heads);
@@ -207,27 +214,30 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     float* bias = bias_mem + (KEYS ? w * nbias : 0);
     float* diag = diag_mem + w * ndiag;
     float far_lo = 0.f, far_hi = 0.f;
-    int head = -1;
+    int head = -1, hh = 0, tile = sb + w;  // the streamed tile, and the head of the group it is of
     bool ok = true;
-    for (int it = w; it < n; it += 2) {
-      const int hh = KEYS ? it / per_head : 0, c0 = (sb + (it - hh * per_head)) * kCols, h = h0 + hh;
+    for (int it = w; it < n; it += 2, tile += 2) {
+      if (KEYS) {
+        while (tile >= se) tile -= per_head, ++hh;
+      }
+      const int first = tile * kCols, c0 = first + half * kColumns, h = h0 + hh;
       const int slot = it % L::kSlots;
       if (KEYS && has_bias && h != head) {
         // every thread of the group is done with the head before
         if (!group_ok(w, ok)) break;
-        fill(bias, h, lane_row, 128);
+        fill(bias, h, in_group, kGroup);
         if (!group_ok(w, ok)) break;
       }
       head = h;
       const float slope2 = MODE == 2 && p.slopes ? p.slopes[h] * kLog2e : 0.f;
-      // columns [lo, hi) of the tile are seen by length and causality
-      int lo = 0, hi = kCols;
-      bool masked = false, clean = false;
+      // columns [lo, hi) of this half are seen by length and causality
+      int lo = 0, hi = kColumns;
+      bool masked = false, clean = false, docs = false;
       if (KEYS) {
         if (row >= info.len) hi = 0;
         if (p.causal && row >= info.prefix) lo = row - info.start - c0;
         masked = r0 + kTile > info.len;
-        if (p.causal && r0 + kTile > info.prefix) masked |= r0 + kTile - 1 - info.start > c0;
+        if (p.causal && r0 + kTile > info.prefix) masked |= r0 + kTile - 1 - info.start > first;
       } else {
         int end = info.len, all = info.len;
         if (p.causal) {
@@ -235,131 +245,57 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
           all = min(all, max(info.start + r0 + 1, info.prefix));
         }
         hi = end - c0;
-        masked = c0 + kCols > all;
-        clean = c0 + kCols > info.len && info.len < p.k_len;
+        masked = first + kCols > all;
+        clean = first + kCols > info.len && info.len < p.k_len;
       }
-      const int32_t* sd = nullptr;
       if (kdocs) {
-        const int4 o = KEYS ? t.q_ranges[b * t.q_tiles + c0 / kTile] : t.k_ranges[b * t.k_tiles + c0 / kTile];
-        if (!(o.z && own_range.z && o.x == own_range.x)) sd = sdocs + c0, masked = true;
+        const int4 o = KEYS ? t.q_ranges[b * t.q_tiles + first / kTile] : t.k_ranges[b * t.k_tiles + first / kTile];
+        if (!(o.z && own_range.z && o.x == own_range.x)) docs = masked = true;
         if (!o.z) clean = true;
       }
-      const int there = (KEYS ? p.q_len : p.k_len) - c0;  // columns that exist
-      const int o0 = KEYS ? row - (info.start + c0) : c0 - (info.start + row);  // offset of column 0
+      const int s_len = KEYS ? p.q_len : p.k_len;
 
       ok = bar_wait(bar(kSFull + w), (it >> 1) & 1, &dead, t.err);
+      fence_after();
+      if (clean || KEYS) ok = bar_wait(bar(kFull + slot), (it / L::kSlots) & 1, &dead, t.err) && ok;
       if (joined) {
         if (!group_ok(w, ok)) break;
       } else if (!__all_sync(0xffffffffu, ok)) {
         break;
       }
-      fence_after();
-      if (clean || KEYS) {
-        ok = bar_wait(bar(kFull + slot), (it / L::kSlots) & 1, &dead, t.err);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;  // a joined group leaves at its next barrier
-          if (!joined) break;
-        }
-      }
       unsigned char* smem_slot = mem + L::kRing + slot * L::kSlot;
       if (clean) {
         // streamed frames that nothing may use become zeros before the second
         // products read them: q and dout, or k
-        const int r = lane_row & 63;
-        const bool unused = r < there && ((!KEYS && c0 + r >= info.len) || (kdocs && sdocs[c0 + r] < 0));
-        if (unused && (KEYS || lane_row < 64)) {
-          unsigned char* to = smem_slot + (lane_row >> 6) * L::kHalf + r * 128;
+        const int r = in_group & 63, op = (in_group >> 6) & 1, piece = in_group >> 7, frame = first + r;
+        const bool unused = frame < s_len && ((!KEYS && frame >= info.len) || (kdocs && sdocs[frame] < 0));
+        if (unused && (KEYS || op == 0)) {
+          unsigned char* to = smem_slot + op * L::kHalf + r * 128;
           for (int e = 0; e < L::kBoxes; ++e)
-            for (int f = 0; f < 8; ++f) *(uint4*)(to + e * L::kBox + 16 * f) = make_uint4(0, 0, 0, 0);
+            for (int f = 4 * piece; f < 4 * piece + 4; ++f) *(uint4*)(to + e * L::kBox + 16 * f) = make_uint4(0, 0, 0, 0);
         }
         fence_async();
       }
-      const float* lse = (const float*)(smem_slot + L::kStats);
+      const float* lse = (const float*)(smem_slot + L::kStats) + half * kColumns;
       const float* delta = lse + kCols;
 
-      float s[64];
-      float slope[MODE == 2 ? 64 : 1];
+      float s[kColumns], slope[MODE == 2 ? kColumns : 1];
+      uint32_t dp[kColumns];
       uint32_t* u = (uint32_t*)s;
       tmem_ld32(ts, u);
-      tmem_ld32(ts + 32, u + 32);
+      if (MODE != 2) tmem_ld32(tt, dp);
       wait_ld();
       tie32(u);
-      tie32(u + 32);
-      float cc = c;
-      if (MODE == 2) {
-        if (p.cap > 0.f) {
-          cap_scores(s, p.scale, p.cap);
-          const float2 in = both(1.f / (p.cap * kLog2e));
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const float2 th = mul2(make_float2(s[j], s[j + 1]), in), f = fma2(make_float2(-th.x, -th.y), th, both(1.f));
-            slope[j] = f.x;
-            slope[j + 1] = f.y;
-          }
-          cc = 1.f;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) slope[j] = 1.f;
-        }
-      }
-      if (has_bias) {
-        // one choice for a warp's rows, as in the forward pass
-        const bool above = __all_sync(0xffffffffu, (KEYS ? o0 - 63 : o0) >= D);
-        const bool below = __all_sync(0xffffffffu, (KEYS ? o0 : o0 + 63) <= -D);
-        if (above || below) {
-          const float2 v = both(bias[above ? 2 * (D + kBiasPad) : 0]);
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const float2 z = fma2(make_float2(s[j], s[j + 1]), both(cc), v);
-            s[j] = z.x;
-            s[j + 1] = z.y;
-          }
-        } else {
-          const float* at = bias + (o0 + D + kBiasPad);
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const float2 v = KEYS ? make_float2(at[-j], at[-j - 1]) : make_float2(at[j], at[j + 1]);
-            const float2 z = fma2(make_float2(s[j], s[j + 1]), both(cc), v);
-            s[j] = z.x;
-            s[j + 1] = z.y;
-          }
-        }
-      } else if (MODE == 2 && !(p.cap > 0.f)) {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) s[j] *= cc;
-      }
-      if (MODE == 2 && p.slopes) {
-        const int far_end = KEYS ? o0 - 63 : o0 + 63;
-        if (__all_sync(0xffffffffu, o0 >= 0 && far_end >= 0) || __all_sync(0xffffffffu, o0 <= 0 && far_end <= 0)) {
-          // one sign: |o| slope is linear in the column
-          const float g = o0 > 0 || far_end > 0 ? -slope2 : slope2, base_z = g * (float)o0, step = KEYS ? -g : g;
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const float2 z = add2(make_float2(s[j], s[j + 1]),
-                                  fma2(both(step), make_float2((float)j, (float)(j + 1)), both(base_z)));
-            s[j] = z.x;
-            s[j + 1] = z.y;
-          }
-        } else {
-          const float f0 = (float)o0;
-#pragma unroll
-          for (int j = 0; j < 64; ++j) s[j] = fmaf(-slope2, fabsf(KEYS ? f0 - (float)j : f0 + (float)j), s[j]);
-        }
-      }
-      uint64_t seen = ~0ull;  // bit j: column j is seen
+      if (MODE != 2) tie32(dp);
+      tile_scores<kColumns, MODE, KEYS, MODE == 2>(s, slope, p, c, bias, slope2,
+                                                   KEYS ? row - (info.start + c0) : c0 - (info.start + row));
+      uint32_t seen = ~0u;  // bit j: column j is seen
       if (masked) {
-        const int first = max(lo, 0), last = min(hi, min(kCols, there));
-        seen = first < last ? (~0ull >> (64 - (last - first))) << first : 0ull;
-        if (sd) {
-          uint64_t same = 0;
-#pragma unroll 8
-          for (int j = 0; j < 64; ++j) same |= (uint64_t)(j < there && __ldg(sd + j) == rd) << j;
-          seen &= same;
-        }
+        seen = (uint32_t)column_range<kColumns>(lo, min(hi, s_len - c0));
+        if (docs) seen &= (uint32_t)same_document<kColumns>(sdocs + c0, s_len - c0, rd);
       }
-      uint32_t pk[32];
 #pragma unroll
-      for (int j = 0; j < 64; j += 4) {
+      for (int j = 0; j < kColumns; j += 4) {
         float4 q = make_float4(row_lse, row_lse, row_lse, row_lse);
         if (KEYS) q = *(const float4*)(lse + j);
 #pragma unroll
@@ -372,72 +308,69 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       }
       if (masked) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) s[j] = (seen >> j & 1) ? s[j] : 0.f;
+        for (int j = 0; j < kColumns; ++j) s[j] = (seen >> j & 1) ? s[j] : 0.f;
       }
+      uint32_t pk[kColumns / 2];
       if (KEYS) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) pk[j] = pack2<BF16>(s[2 * j], s[2 * j + 1]);
-        tmem_st32(ts, pk);
+        for (int j = 0; j < kColumns / 2; ++j) pk[j] = pack2<BF16>(s[2 * j], s[2 * j + 1]);
+        tmem_st16(ts, pk);
+      }
+      if (MODE == 2) {  // beside the cap's derivatives there were no registers for it
+        tmem_ld32(tt, dp);
+        wait_ld();
+        tie32(dp);
       }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t d[32];
-        tmem_ld32(tt + 32 * half, d);
-        wait_ld();
-        tie32(d);
+      for (int j = 0; j < kColumns; j += 4) {
+        float4 q = make_float4(row_delta, row_delta, row_delta, row_delta);
+        if (KEYS) q = *(const float4*)(delta + j);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float4 q = make_float4(row_delta, row_delta, row_delta, row_delta);
-          if (KEYS) q = *(const float4*)(delta + 32 * half + j);
-          float* a = s + 32 * half + j;
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float2 g = add2(make_float2(__uint_as_float(d[j + e]), __uint_as_float(d[j + e + 1])),
-                                  e ? make_float2(-q.z, -q.w) : make_float2(-q.x, -q.y));
-            const float2 r = mul2(make_float2(a[e], a[e + 1]), g);
-            a[e] = r.x;
-            a[e + 1] = r.y;
-          }
+        for (int e = 0; e < 4; e += 2) {
+          const float2 g = add2(make_float2(__uint_as_float(dp[j + e]), __uint_as_float(dp[j + e + 1])),
+                                e ? make_float2(-q.z, -q.w) : make_float2(-q.x, -q.y));
+          const float2 f = mul2(make_float2(s[j + e], s[j + e + 1]), g);
+          s[j + e] = f.x;
+          s[j + e + 1] = f.y;
         }
       }
       if (masked) {  // 0 times what an unused frame's dP holds
 #pragma unroll
-        for (int j = 0; j < 64; ++j) s[j] = (seen >> j & 1) ? s[j] : 0.f;
+        for (int j = 0; j < kColumns; ++j) s[j] = (seen >> j & 1) ? s[j] : 0.f;
       }
       // dS goes to the products in the inputs' type; the bias gradient below
       // sums it in 32 bits
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+      for (int j = 0; j < kColumns / 2; ++j) {
         float2 a = make_float2(s[2 * j], s[2 * j + 1]);
         if (!BF16) a = mul2(a, both(tau));
         if (MODE == 2) a = mul2(a, make_float2(slope[2 * j], slope[2 * j + 1]));
         pk[j] = pack2<BF16>(a.x, a.y);
       }
-      tmem_st32(tt, pk);
+      tmem_st16(tt, pk);
       wait_st();
       fence_before();
       __syncwarp();
-      if (tid % 32 == 0) bar_arrive(bar(kPReady + w));
+      if (lane == 0) bar_arrive(bar(kPReady + w));
 
       if (grad) {
-        // offsets of the tile: o = (c0 - start - r0) + column - row
-        const int t0 = c0 - info.start - r0;
+        // offsets of the tile: o = (first - start - r0) + column - row
+        const int t0 = first - info.start - r0;
         if (t0 - (kTile - 1) >= D || t0 + kCols - 1 <= -D) {
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
-          for (int j = 0; j < 64; ++j) sum[j & 3] += s[j];
-          const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          if (t0 > 0) far_hi += all;
-          else far_lo += all;
+          for (int j = 0; j < kColumns; j += 2) sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], make_float2(s[j], s[j + 1]));
+          sum[0] = add2(sum[0], sum[1]);
+          if (t0 > 0) far_hi += sum[0].x + sum[0].y;
+          else far_lo += sum[0].x + sum[0].y;
         } else {
-          // Diagonal sums of the warp's 32 x 64: in four chains of 16 columns,
+          // Diagonal sums of the warp's 32 x 32: in two chains of 16 columns,
           // each step hands a lane's sum to the next row's lane, which adds its
           // element of the next column. Lane 31 finishes one diagonal a step;
           // at the end lane r holds that of column 15 - row r.
-          const int lane = tid & 31;
-          float* mine = chain_mem + (warp * kChains) * kChainEntries;
+          float* mine = chain_mem + ((w * 4 + quarter) * kChains + 2 * half) * kChainEntries;
 #pragma unroll
-          for (int g = 0; g < kChains; ++g) {
+          for (int g = 0; g < 2; ++g) {
             float f[16];
             f[0] = s[16 * g];
 #pragma unroll
@@ -454,8 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
             }
           }
           ok = group_ok(w, ok);
-          // the group's four warps and their chains, diagonal by diagonal
-          for (int d = lane_row; d < kTile + kCols - 1; d += 128) {  // d = column - row + 127
+          // the rows' quarters and their chains, diagonal by diagonal
+          const int d = in_group;  // column - row + 127
+          if (d < kTile + kCols - 1) {
             float sum = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -469,8 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         }
       }
     }
-    if (grad) far_mem[tid] = far_lo, far_mem[256 + tid] = far_hi;
-    // ---- results: a group each for dv and dk, or half of dq's columns each
+    if (grad) far_mem[tid] = far_lo, far_mem[512 + tid] = far_hi;
+    // ---- results: a group each for dv and dk, or half of dq's columns each,
+    // and half of those a thread
     if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(bar(kDone), 0, &dead, t.err));
     if (ok) {
       fence_after();
@@ -480,28 +415,30 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
                       (KEYS ? hk : h0) * st.h;
       const uint32_t from = tmem + lanes + kAcc + (KEYS && is_dv ? 0 : DP);
       const float f = is_dv ? exp2f(-kLift<BF16>) : p.scale / sigma;
-      const int begin = KEYS ? 0 : w * (DP / 2), end = KEYS ? t.dim16 : min(t.dim16, begin + DP / 2);
+      constexpr int kShare = KEYS ? DP / 2 : DP / 4;
+      const int begin = (KEYS ? half : 2 * w + half) * kShare;
 #pragma unroll 1
-      for (int y = begin; y < end; y += 16) {
+      for (int y = begin; y < begin + kShare; y += 16) {
+        if (y >= t.dim16) break;
         uint32_t o[16];
         if (n > 0) tmem_ld16(from + y, o);
         wait_ld();
         tie16(o);
-        uint32_t r[8];
+        uint32_t v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          r[e] = n > 0 ? pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
+          v[e] = n > 0 ? pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
         if (lane_row < owned) {
-          *(uint4*)(out + y) = make_uint4(r[0], r[1], r[2], r[3]);
-          if (y + 8 < p.dim) *(uint4*)(out + y + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+          *(uint4*)(out + y) = make_uint4(v[0], v[1], v[2], v[3]);
+          if (y + 8 < p.dim) *(uint4*)(out + y + 8) = make_uint4(v[4], v[5], v[6], v[7]);
         }
       }
       fence_before();
     }
   } else {
-    give_registers<56>();
+    give_registers<64>();
     const uint32_t lead = elect();
-    if (warp == 8 && n > 0) {
+    if (warp == 16 && n > 0) {
       // ---- copies: the owned tile once, then streamed tiles
       if (lead) {
         const uint32_t own = bar(kOwnFull);
@@ -547,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         __syncwarp();
         if (++tile == se) tile = sb, ++h;
       }
-    } else if (warp == 9 && n > 0) {
+    } else if (warp == 17 && n > 0) {
       // ---- products
       const uint32_t id_s = instr_desc(kTile, kCols, BF16, false), id_a = instr_desc(kTile, t.dim16, BF16, true);
       const int ksteps = t.dim16 / 16;
@@ -566,6 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
                    desc_k(from + op * L::kHalf + (k / 4) * L::kBox + (k % 4) * 32), id_s, k > 0);
         mma_commit(lead, bar(kSFull + w));
       };
+      // each half's 16-bit weights start where its scores did
+      auto p_at = [](int k) { return (uint32_t)((k >> 1) * kColumns + (k & 1) * 8); };
       // the ring's slot and round two tiles ahead of the one being summed
       int ahead = 0, round = 0, slot = 0;
       bool ok = wait(kOwnFull, 0);
@@ -586,12 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         if (KEYS) {
 #pragma unroll
           for (int k = 0; k < kCols / 16; ++k)
-            mma_ts(lead, tmem + kAcc, tmem + w * 128 + k * 8, desc_mn(from + L::kHalf + k * 2048, L::kBox), id_a,
+            mma_ts(lead, tmem + kAcc, tmem + w * 128 + p_at(k), desc_mn(from + L::kHalf + k * 2048, L::kBox), id_a,
                    it > 0 || k > 0);
         }
 #pragma unroll
         for (int k = 0; k < kCols / 16; ++k)
-          mma_ts(lead, tmem + kAcc + DP, tmem + w * 128 + 64 + k * 8, desc_mn(from + k * 2048, L::kBox), id_a,
+          mma_ts(lead, tmem + kAcc + DP, tmem + w * 128 + 64 + p_at(k), desc_mn(from + k * 2048, L::kBox), id_a,
                  it > 0 || k > 0);
         mma_commit(lead, bar(kEmpty + slot));
         if (++slot == L::kSlots) slot = 0;
@@ -613,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     if (warp < 2) {
       float s = 0.f;
       const int lane = tid & 31;
-      for (int i = lane; i < 256; i += 32) s += far_mem[warp * 256 + i] * unit;
+      for (int i = lane; i < 512; i += 32) s += far_mem[warp * 512 + i] * unit;
       for (int i = lane; i <= kDiagPad; i += 32) s += both(warp ? 2 * D + kDiagPad + i : i);
       s = warp_sum(s);
       if (lane == 0) part[warp ? 2 * D : 0] = s;
@@ -624,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     __syncwarp();
     fence_after();
     tmem_free(tmem, 512);

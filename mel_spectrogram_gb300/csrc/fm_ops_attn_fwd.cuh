@@ -5,14 +5,16 @@
 // products with accumulators in tensor memory; one thread per query row reads
 // its scores, keeps the running maximum and sum in registers, and writes its
 // 16-bit weights P back over them, from where the second product takes them.
-// Warps: 0-3 and 4-7 do the softmax of one query tile each, warp 8 copies
-// tiles by TMA into a ring, warp 9 issues products. While one tile's softmax
-// runs, the products of the other do.
+// Warps: 0-7 and 8-15 do the softmax of one query tile each, two threads a row
+// with 64 columns each; warp 16 copies tiles by TMA into a ring, warp 17 issues
+// products. While one tile's softmax runs, the products of the other do.
 //
-// Bound: for head size 128 a key tile costs two 128 x 128 x 128 products a
-// query tile, 2 x 512 cycles of the tensor unit for both tiles' pairs, and
-// 2 x 16384 exponentials and about five times as many FP32 instructions, which
-// is what holds it below the tensor rate.
+// Bound: a key tile costs 2 x 2 products of 128 x 128 x dim (2048 cycles of the
+// tensor unit at dim 128) for 2 x 16384 exponentials. A tile's own chain
+// (scores, softmax, products) has to fit twice its products' time, which is
+// why a row has two threads: one thread a row took 1500 cycles for its
+// softmax, and with a tile's whole width unrolled the code of the biased modes
+// did not stay in the instruction cache.
 //
 // Rescaling O when the maximum rises is put off until it has risen by 2^8:
 // weights then stay below 2^8, exact in the sense that the same factor divides
@@ -27,7 +29,8 @@ namespace fwd {
 
 using namespace tc;
 
-constexpr int kThreads = 384;  // warps 10 and 11 only complete a group of four
+constexpr int kThreads = 640;  // warps 18 and 19 only complete a group of four
+constexpr int kColumns = kTile / 2;  // a thread's share of a tile
 constexpr float kRise = 8.f;
 // f16 weights are kept 2^7 larger, up to 2^15, so that small ones stay normal
 // numbers; the factor divides out with the sum. bf16 has the range.
@@ -49,77 +52,17 @@ struct Smem {
 };
 enum { kFull = 0, kEmpty = 8, kQFull = 16, kSFull = 17, kPReady = 19, kOFull = 21, kBarCount = 23 };
 
-// One row's scores of a tile, in registers: scaled, capped, biased (base 2).
-template <int MODE, bool MASKED>
-struct RowScores {
-  // s: raw products. o0: offset of column 0. lim: columns below are in length
-  // and causal range; qd / kd: this row's document and the columns'
-  static __device__ __forceinline__ void apply(float (&s)[128], const AttnParams& p, float c, const float* bias,
-                                               float slope2, int o0, int lim, int qd, const int32_t* kd) {
-    if (MODE == 2 && p.cap > 0.f) {
-      cap_scores(s, p.scale, p.cap);
-      c = 1.f;
-    }
-    const int D = p.max_distance;
-    if (MODE == 1 || (MODE == 2 && p.map)) {
-      // rows of a warp differ by 31 in o0: one choice for all of them (the
-      // array holds copies of its ends far enough)
-      const bool above = __all_sync(0xffffffffu, o0 >= D), below = __all_sync(0xffffffffu, o0 + 127 <= -D);
-      if (above || below) {
-        const float2 b = both(bias[above ? 2 * (D + kBiasPad) : 0]);
-#pragma unroll
-        for (int j = 0; j < 128; j += 2) {
-          const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c), b);
-          s[j] = z.x;
-          s[j + 1] = z.y;
-        }
-      } else {
-        const float* at = bias + (o0 + D + kBiasPad);
-#pragma unroll
-        for (int j = 0; j < 128; j += 2) {
-          const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c), make_float2(at[j], at[j + 1]));
-          s[j] = z.x;
-          s[j + 1] = z.y;
-        }
-      }
-    } else if (MODE == 2 && !(p.cap > 0.f)) {
-#pragma unroll
-      for (int j = 0; j < 128; j += 2) {
-        const float2 z = mul2(make_float2(s[j], s[j + 1]), both(c));
-        s[j] = z.x;
-        s[j + 1] = z.y;
-      }
-    }
-    if (MODE == 2 && p.slopes) {
-      if (__all_sync(0xffffffffu, o0 >= 0) || __all_sync(0xffffffffu, o0 + 127 <= 0)) {
-        // one sign: |o0 + j| slope is linear in j
-        const float g = o0 >= 0 ? -slope2 : slope2, base = g * (float)o0;
-#pragma unroll
-        for (int j = 0; j < 128; j += 2) {
-          const float2 z = add2(make_float2(s[j], s[j + 1]),
-                                fma2(both(g), make_float2((float)j, (float)(j + 1)), both(base)));
-          s[j] = z.x;
-          s[j + 1] = z.y;
-        }
-      } else {
-        const float f0 = (float)o0;
-#pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope2, fabsf(f0 + (float)j), s[j]);
-      }
-    }
-    if (MASKED) {
-#pragma unroll
-      for (int j = 0; j < 128; ++j) s[j] = j < lim ? s[j] : -INFINITY;
-      if (kd) {
-#pragma unroll
-        for (int j = 0; j < 128; ++j) {
-          const int d = j < lim ? __ldg(kd + j) : -1;
-          s[j] = d == qd ? s[j] : -INFINITY;
-        }
-      }
-    }
-  }
-};
+// a barrier of the two warps that share 32 rows, which also tells whether both
+// are well: they leave together
+__device__ __forceinline__ bool pair_ok(int pair, bool ok) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, %2, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((int)ok), "r"(pair + 1)
+      : "memory");
+  return r != 0;
+}
 
 template <int DP, bool BF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t) {
@@ -128,6 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int dead;
   __shared__ int range[2];
+  __shared__ float row_stat[2][2][2][kTile];  // [tile parity][query tile][half][row]
   const AttnParams& p = t.p;
   const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
   unsigned char* mem = raw + (base - smem_u32(raw));
@@ -146,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     bar_init(bar(kQFull), 1);
     for (int w = 0; w < 2; ++w) {
       bar_init(bar(kSFull + w), 1);
-      bar_init(bar(kPReady + w), 4);
+      bar_init(bar(kPReady + w), 8);
       bar_init(bar(kOFull + w), 1);
     }
     fence_bar_init();
@@ -157,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     tma_prefetch(&t.km);
     tma_prefetch(&t.vm);
   }
-  if (warp == 9) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
   if (MODE == 1 || (MODE == 2 && p.map)) fill_bias<BF16>(p, h, bias, tid, kThreads);
   fence_before();
   __syncthreads();
@@ -185,14 +129,15 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   const int n = max(te - tb, 0);
 
   constexpr uint32_t kO = 256;  // columns of O0; O1 follows at kO + DP
-  // registers: the block starts with 3 groups x 168; the softmax threads, which
-  // hold 128 scores each, take 224 and leave the others 56 (2 x 224 + 56 = 504)
-  if (warp < 8) {
-    take_registers<224>();
-    // ---- softmax: one query row a thread
-    const int w = warp >> 2, lane_row = tid & 127;
+  // registers: the block starts with 5 groups x 96; the softmax threads take
+  // 104 and leave the others 64 (4 x 104 + 64 = 480)
+  if (warp < 16) {
+    take_registers<104>();
+    // ---- softmax: a thread has 64 columns of one query row
+    const int w = warp >> 3, half = (warp >> 2) & 1, pair = (warp >> 3) * 4 + (warp & 3);
+    const int lane_row = (warp & 3) * 32 + (tid & 31);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 * (warp % 4) in bits 16 up
-    const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + kO + w * DP;
+    const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + kO + w * DP + half * (DP / 2);
     const int i = q0 + w * kTile + lane_row, place = info.start + i;
     const float c = p.scale * kLog2e;
     const float slope2 = MODE == 2 && p.slopes ? p.slopes[h] * kLog2e : 0.f;
@@ -213,48 +158,58 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     int all_end = info.len;
     if (p.causal) all_end = min(all_end, max(info.start + q0 + w * kTile + 1, info.prefix));
 
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;  // l: of this thread's columns
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const int k0 = (tb + j) * kTile;
-      bool masked = k0 + kTile > all_end, clean = k0 + kTile > info.len && info.len < p.k_len;
-      const int32_t* kd = nullptr;
+      const int k0 = (tb + j) * kTile, mine = k0 + half * kColumns;
+      bool masked = k0 + kTile > all_end, clean = k0 + kTile > info.len && info.len < p.k_len, docs = false;
       if (kdocs) {
         const int4 kr = t.k_ranges[b * t.k_tiles + tb + j];
-        if (!(qr.z && kr.z && qr.x == kr.x)) kd = kdocs + k0, masked = true;
+        if (!(qr.z && kr.z && qr.x == kr.x)) docs = masked = true;
         if (!kr.z) clean = true;
       }
       ok = bar_wait(bar(kSFull + w), j & 1, &dead, t.err);
-      if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
       if (clean) {
         // rows of V that nothing may use become zeros: 0 weights times
         // whatever memory holds would not be 0
         const int it = 2 * j + 1;
-        ok = bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        ok = bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err) && ok;
         const int key = k0 + lane_row;
-        if (key >= info.len || (kdocs && kdocs[key] < 0)) {
+        if (ok && (key >= info.len || (kdocs && kdocs[key] < 0))) {
           unsigned char* row = mem + L::kRing + (it % L::kSlots) * L::kOperand + lane_row * 128;
           for (int x = 0; x < L::kBoxes; ++x)
-            for (int e = 0; e < 8; ++e) *(uint4*)(row + x * L::kBox + 16 * e) = make_uint4(0, 0, 0, 0);
+            for (int e = 4 * half; e < 4 * half + 4; ++e) *(uint4*)(row + x * L::kBox + 16 * e) = make_uint4(0, 0, 0, 0);
         }
         fence_async();
       }
-      float s[128];
+      ok = __all_sync(0xffffffffu, ok);
+      float s[kColumns], unused[1];
       uint32_t* u = (uint32_t*)s;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, u + 32 * x);
+      tmem_ld32(ts + half * kColumns, u);
+      tmem_ld32(ts + half * kColumns + 32, u + 32);
       wait_ld();
+      tie32(u);
+      tie32(u + 32);
+      tile_scores<kColumns, MODE, false, false>(s, unused, p, c, bias, slope2, mine - place);
+      if (masked) {
+        uint64_t seen = column_range<kColumns>(0, seen_end - mine);
+        if (docs) seen &= same_document<kColumns>(kdocs + mine, p.k_len - mine, qd);
+        const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) tie32(u + 32 * x);
-      const int o0 = k0 - place;
-      if (masked) RowScores<MODE, true>::apply(s, p, c, bias, slope2, o0, seen_end - k0, qd, kd);
-      else RowScores<MODE, false>::apply(s, p, c, bias, slope2, o0, 128, 0, nullptr);
+        for (int e = 0; e < kColumns; ++e) s[e] = ((e < 32 ? lo : hi) >> (e & 31) & 1) ? s[e] : -INFINITY;
+      }
       float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int e = 4; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
+      for (int e = 4; e < kColumns; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
       float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      row_stat[j & 1][w][half][lane_row] = mx;
+      if (!pair_ok(pair, ok)) {
+        ok = false;
+        break;
+      }
+      // both warps have their scores in registers now: P may replace them
+      mx = fmaxf(mx, row_stat[j & 1][w][half ^ 1][lane_row]);
       if (MODE == 0) mx *= c;  // scale > 0 here
       if (__any_sync(0xffffffffu, mx > m + kRise || (m == -INFINITY && mx > m))) {
         const float top_m = fmaxf(m, mx), f = top_m == -INFINITY ? 1.f : ex2(m - top_m);
@@ -262,32 +217,32 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         l *= f;
         if (j > 0) {
 #pragma unroll 1
-          for (int x = 0; x < DP; x += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + x, o);
+          for (int x = 0; x < DP / 2; x += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + x, o);
             wait_ld();
-            tie32(o);
+            tie16(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(to + x, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(to + x, o);
           }
         }
       }
       const float m0 = (m == -INFINITY ? 0.f : m) - kLift<BF16>;
       float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
+      for (int part = 0; part < 2; ++part) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 z = make_float2(s[64 * half + 2 * e], s[64 * half + 2 * e + 1]);
+        for (int e = 0; e < 16; ++e) {
+          const float2 z = make_float2(s[32 * part + 2 * e], s[32 * part + 2 * e + 1]);
           const float2 a = MODE == 0 ? fma2(z, both(c), both(-m0)) : add2(z, both(-m0));
           const float2 q = make_float2(ex2(a.x), ex2(a.y));
           sum[e & 1] = add2(sum[e & 1], q);
           // weights go to the product in the inputs' type: the sum keeps 32 bits
           pk[e] = pack2<BF16>(q.x, q.y);
         }
-        tmem_st32(ts + 32 * half, pk);
+        tmem_st16(ts + 32 * half + 16 * part, pk);
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
@@ -296,67 +251,63 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       __syncwarp();
       if (tid % 32 == 0) bar_arrive(bar(kPReady + w));
     }
-    // ---- the row's result
-    if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(bar(kOFull + w), 0, &dead, t.err));
+    // ---- the row's result, half of its columns a thread
+    if (n > 0) ok = bar_wait(bar(kOFull + w), 0, &dead, t.err) && ok;
+    row_stat[n & 1][w][half][lane_row] = l;
+    ok = pair_ok(pair, ok);
     if (ok) {
       fence_after();
+      l += row_stat[n & 1][w][half ^ 1][lane_row];
       const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float lse2 = l == 0.f ? -INFINITY : m - kLift<BF16> + log2f(l);
       const long long row = ((long long)b * p.heads + h) * p.q_len + i;
+      const long long at = (long long)split * p.batch * p.heads * p.q_len + row;
+      const long long place_out = b * p.os.b + i * p.os.t + h * p.os.h;
       const bool store = i < p.q_len;
-      if (t.splits > 1) {
-        const long long at = (long long)split * p.batch * p.heads * p.q_len + row;
-        if (store) t.part_lse[at] = l == 0.f ? -INFINITY : m - kLift<BF16> + log2f(l);
+      if (store && half == 0) {
+        if (t.splits > 1) t.part_lse[at] = lse2;
+        else if (p.lse) p.lse[row] = lse2 * kLn2;
+      }
+      uint16_t* rest = t.splits == 1 && p.rest ? (uint16_t*)p.rest + place_out : nullptr;
 #pragma unroll 1
-        for (int x = 0; x < t.dim16; x += 16) {
-          uint32_t o[16];
-          if (n > 0) tmem_ld16(to + x, o);
-          wait_ld();
-          tie16(o);
-          if (store)
+      for (int y = 0; y < DP / 2; y += 16) {
+        const int x = half * (DP / 2) + y;
+        if (x >= t.dim16) break;
+        uint32_t o[16];
+        if (n > 0) tmem_ld16(to + y, o);
+        wait_ld();
+        tie16(o);
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = n > 0 ? __uint_as_float(o[e]) * f : 0.f;
+        if (t.splits > 1) {
+          if (store) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
               if (x + e < p.dim)
-                *(float4*)(t.part_o + at * p.dim + x + e) =
-                    n > 0 ? make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
-                                        __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      } else {
-        if (store && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m - kLift<BF16> + log2f(l)) * kLn2;
-        const long long place_out = b * p.os.b + i * p.os.t + h * p.os.h;
-        uint16_t* out = (uint16_t*)p.out + place_out;
-        uint16_t* rest = p.rest ? (uint16_t*)p.rest + place_out : nullptr;
-#pragma unroll 1
-        for (int x = 0; x < t.dim16; x += 16) {
-          uint32_t o[16];
-          if (n > 0) tmem_ld16(to + x, o);
-          wait_ld();
-          tie16(o);
+                *(float4*)(t.part_o + at * p.dim + x + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+        } else if (store) {
           uint32_t r[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            r[e] = n > 0 ? pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
-          if (store) {
-            *(uint4*)(out + x) = make_uint4(r[0], r[1], r[2], r[3]);
-            if (x + 8 < p.dim) *(uint4*)(out + x + 8) = make_uint4(r[4], r[5], r[6], r[7]);
-          }
+          for (int e = 0; e < 8; ++e) r[e] = pack2<BF16>(v[2 * e], v[2 * e + 1]);
+          uint16_t* out = (uint16_t*)p.out + place_out + x;
+          *(uint4*)out = make_uint4(r[0], r[1], r[2], r[3]);
+          if (x + 8 < p.dim) *(uint4*)(out + 8) = make_uint4(r[4], r[5], r[6], r[7]);
           if (rest) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              r[e] = n > 0 ? rest2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f, r[e]) : 0u;
-            if (store) {
-              *(uint4*)(rest + x) = make_uint4(r[0], r[1], r[2], r[3]);
-              if (x + 8 < p.dim) *(uint4*)(rest + x + 8) = make_uint4(r[4], r[5], r[6], r[7]);
-            }
+            for (int e = 0; e < 8; ++e) r[e] = rest2<BF16>(v[2 * e], v[2 * e + 1], r[e]);
+            *(uint4*)(rest + x) = make_uint4(r[0], r[1], r[2], r[3]);
+            if (x + 8 < p.dim) *(uint4*)(rest + x + 8) = make_uint4(r[4], r[5], r[6], r[7]);
           }
         }
       }
       fence_before();
     }
   } else {
-    give_registers<56>();
+    give_registers<64>();
     const uint32_t lead = elect();
-    if (warp == 8 && n > 0) {
+    if (warp == 16 && n > 0) {
       // ---- copies: q once, then K and V tiles in turn through the ring
       if (lead) {
         bar_expect(bar(kQFull), 2 * L::kOperand);
@@ -381,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         }
         __syncwarp();
       }
-    } else if (warp == 9 && n > 0) {
+    } else if (warp == 17 && n > 0) {
       // ---- products
       const uint32_t id_s = instr_desc(kTile, kTile, BF16, false), id_o = instr_desc(kTile, t.dim16, BF16, true);
       const int ksteps = t.dim16 / 16;
@@ -445,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     __syncwarp();
     fence_after();
     tmem_free(tmem, 512);

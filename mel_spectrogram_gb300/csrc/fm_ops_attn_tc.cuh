@@ -8,7 +8,8 @@
 namespace fm {
 
 constexpr int kTile = 128;      // rows of a tile: the lanes of tensor memory
-constexpr int kBiasPad = 256;   // copies of the end values beside the bias by offset
+constexpr int kBiasPad = 128;   // copies of the end values beside the bias by offset: a warp's rows and a
+                                // thread's columns reach 94 past an end when one of them is inside
 
 // Which documents the 128 frames of a tile hold: lowest and highest id, and
 // whether all its frames carry that one id. No documents: every tile is {0, 0, 1}.
@@ -78,6 +79,134 @@ __device__ __forceinline__ void fill_bias(const AttnParams& p, int h, float* bia
     const int at = min(max(i - kBiasPad, 0), 2 * D);
     bias[i] = kLog2e * table_value(p, (long long)p.map[at] * p.heads + h, BF16);
   }
+}
+
+// A row's N raw products of one tile, to scores in base 2: scaled or capped,
+// and biased. MODE 0 leaves them raw (the weights' exponent scales them), 1 is
+// scale and bucket bias, 2 anything. Column j has offset o0 + j, or o0 - j
+// where REV. CAP_SLOPE: also 1 - tanh^2, the cap's derivative, into slope.
+//
+// tanh: where every score of the warp's rows is small against the cap
+// (|x| <= 0.4, the usual case) tanh(x) / x is a polynomial of degree 3 in x^2,
+// fitted for the least relative error there (1e-7): three multiply-adds
+// instead of two trips to the special-function unit, which the weights' 2^z
+// needs.
+template <int N, int MODE, bool REV, bool CAP_SLOPE>
+__device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SLOPE ? N : 1], const AttnParams& p,
+                                            float c, const float* bias, float slope2, int o0) {
+  using namespace tc;
+  if (MODE == 0) return;
+  const int D = p.max_distance, last = REV ? o0 - (N - 1) : o0 + (N - 1);
+  if (MODE == 2) {
+    // a slope's share is linear in the column where all offsets have one sign
+    const bool ahead = __all_sync(0xffffffffu, min(o0, last) >= 0), back = __all_sync(0xffffffffu, max(o0, last) <= 0);
+    const bool linear = p.slopes && (ahead || back);
+    const float g = !linear ? 0.f : ahead ? -slope2 : slope2;
+    const float2 g2 = both(REV ? -g : g), base = both(linear ? g * (float)o0 : 0.f);
+    if (p.cap > 0.f) {
+      const float k = p.scale / p.cap, out = p.cap * kLog2e;
+      const float2 in = both(1.f / out);
+      float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < N; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(s[j]));
+      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      const bool small = __all_sync(0xffffffffu, most * fabsf(k) <= 0.4f);
+      const float tanh_over_x[4] = {0.999999902f, -0.333313625f, 0.132709768f, -0.0475536036f};
+      const float k2 = k * k;
+      float2 a[4];
+      float power = out * k;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = both(tanh_over_x[i] * power);
+        power *= k2;
+      }
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        const float2 x = make_float2(s[j], s[j + 1]);
+        float2 t;
+        if (small) {
+          const float2 q = mul2(x, x);
+          t = mul2(fma2(fma2(fma2(a[3], q, a[2]), q, a[1]), q, a[0]), x);
+        } else {
+          const float c2 = 2.f * kLog2e * k;
+          t = make_float2(out * tanh_from(x.x * c2), out * tanh_from(x.y * c2));
+        }
+        if (CAP_SLOPE) {
+          const float2 th = mul2(t, in), f = fma2(make_float2(-th.x, -th.y), th, both(1.f));
+          slope[j] = f.x;
+          slope[j + 1] = f.y;
+        }
+        const float2 z = add2(t, fma2(g2, make_float2((float)j, (float)(j + 1)), base));
+        s[j] = z.x;
+        s[j + 1] = z.y;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c),
+                              fma2(g2, make_float2((float)j, (float)(j + 1)), base));
+        s[j] = z.x;
+        s[j + 1] = z.y;
+        if (CAP_SLOPE) slope[j] = slope[j + 1] = 1.f;
+      }
+    }
+    if (p.slopes && !linear) {
+      const float f0 = (float)o0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[j] = fmaf(-slope2, fabsf(REV ? f0 - (float)j : f0 + (float)j), s[j]);
+    }
+    c = 1.f;
+  }
+  if (MODE == 1 || p.map) {
+    // rows of a warp differ by 31 in o0: one choice for all of them (the array
+    // holds copies of its ends far enough)
+    const bool above = __all_sync(0xffffffffu, min(o0, last) >= D), below = __all_sync(0xffffffffu, max(o0, last) <= -D);
+    if (above || below) {
+      const float2 b = both(bias[above ? 2 * (D + kBiasPad) : 0]);
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c), b);
+        s[j] = z.x;
+        s[j + 1] = z.y;
+      }
+    } else {
+      const float* at = bias + (o0 + D + kBiasPad);
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        const float2 b = REV ? make_float2(at[-j], at[-j - 1]) : make_float2(at[j], at[j + 1]);
+        const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c), b);
+        s[j] = z.x;
+        s[j + 1] = z.y;
+      }
+    }
+  }
+}
+
+// Bits of the N columns whose document is this row's. ids: the columns'
+// documents, `there` of them exist; own: the row's (-2: none matches). A warp
+// goes through the distinct ids of the tile, usually one or two.
+template <int N>
+__device__ __forceinline__ uint64_t same_document(const int32_t* ids, int there, int own) {
+  const int lane = threadIdx.x & 31;
+  const int v0 = lane < there ? __ldg(ids + lane) : -1;
+  const int v1 = N > 32 && lane + 32 < there ? __ldg(ids + lane + 32) : -1;
+  uint64_t left = (uint64_t)__ballot_sync(0xffffffffu, v0 >= 0) | (uint64_t)__ballot_sync(0xffffffffu, v1 >= 0) << 32;
+  uint64_t same = 0;
+  while (left != 0) {
+    const int j = __ffsll((long long)left) - 1;
+    const int id = __shfl_sync(0xffffffffu, j < 32 ? v0 : v1, j & 31);
+    const uint64_t m = (uint64_t)__ballot_sync(0xffffffffu, v0 == id) | (uint64_t)__ballot_sync(0xffffffffu, v1 == id) << 32;
+    if (own == id) same = m;
+    left &= ~m;
+  }
+  return same;
+}
+// bits [lo, hi) of N columns
+template <int N>
+__device__ __forceinline__ uint64_t column_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, N);
+  return lo < hi ? (~0ull >> (64 - (hi - lo))) << lo : 0ull;
 }
 #endif
 

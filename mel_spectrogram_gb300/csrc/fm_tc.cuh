@@ -236,48 +236,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// Scores capped and brought to base 2: z = cap log2(e) tanh(s scale / cap).
-// Where every score of a warp's tile is small against the cap (|x| <= 3/4,
-// the usual case) tanh(x) / x is a polynomial of degree 5 in x^2, fitted for
-// the least relative error there (2.9e-8): five packed multiply-adds instead of
-// two trips to the special-function unit, which the weights' 2^z needs.
-template <int N>
-__device__ __forceinline__ void cap_scores(float (&s)[N], float scale, float cap) {
-  const float k = scale / cap, out = cap * 1.4426950408889634f;
-  float top[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < N; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(s[j]));
-  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  if (__all_sync(0xffffffffu, most * fabsf(k) <= 0.75f)) {
-    const float k2 = k * k, f = out * k;
-    const float tanh_over_x[6] = {0.999999971f,   -0.333329589f, 0.13325406f,
-                                  -0.0533444307f, 0.0195829084f, -0.00471625688f};
-    float2 c[6];
-    float power = f;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      c[i] = both(tanh_over_x[i] * power);
-      power *= k2;
-    }
-#pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      const float2 x = make_float2(s[j], s[j + 1]), q = mul2(x, x);
-      float2 r = fma2(c[5], q, c[4]);
-      r = fma2(r, q, c[3]);
-      r = fma2(r, q, c[2]);
-      r = fma2(r, q, c[1]);
-      r = fma2(r, q, c[0]);
-      r = mul2(r, x);
-      s[j] = r.x;
-      s[j + 1] = r.y;
-    }
-  } else {
-    const float c2 = 2.f * 1.4426950408889634f * k;
-#pragma unroll
-    for (int j = 0; j < N; ++j) s[j] = out * tanh_from(s[j] * c2);
-  }
-}
-
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
