@@ -65,7 +65,12 @@ struct Smem {
     return n;
   }
 };
-enum { kFull = 0, kEmpty = 8, kOwnFull = 16, kSFull = 17, kPReady = 19, kDone = 21 };
+enum { kFull = 0, kEmpty = 8, kOwnFull = 16, kSFull = 17, kPReady = 20, kDone = 23 };
+// Buffers of 128 columns for a streamed tile's scores and dP, taken in turn:
+// with three, a tile's scores are there before the group that will take it has
+// finished its last one. Beside dk and dv of 128 columns only two fit.
+template <int DP, bool KEYS>
+constexpr int kBuffers = DP == 128 && KEYS ? 2 : 3;
 
 // a barrier of a group's 256 threads that also tells whether all are well
 __device__ __forceinline__ bool group_ok(int group, bool ok) {
@@ -87,7 +92,6 @@ __device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_
 struct Extra {
   const float* lse2;   // [batch * heads][q_pad]: base-2 lse, +inf for rows that see nothing or are not there
   const float* delta;  // [batch * heads][q_pad]
-  const float* bias;   // [heads][2 * max_distance + 1], base 2
   int q_pad;           // q_len rounded up to 64
   // [batch * kv_heads] largest squared norms of a row of dout, then of v (f16)
   const float* peak;
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   if (tid == 0) {
     for (int i = 0; i < L::kSlots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
     bar_init(bar(kOwnFull), 1);
-    for (int w = 0; w < 2; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 8);
+    for (int w = 0; w < 3; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 8);
     bar_init(bar(kDone), 1);
     fence_bar_init();
     dead = 0;
@@ -145,10 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     tma_prefetch(&t.gm);
   }
   if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
-  auto fill = [&](float* to, int h, int at, int step) {
-    for (int i = at; i < nbias; i += step) to[i] = x.bias[(long long)h * (2 * D + 1) + min(max(i - kBiasPad, 0), 2 * D)];
-  };
-  if (has_bias && !KEYS) fill(bias_mem, h0, tid, kThreads);
+  if (has_bias && !KEYS) fill_bias(t, h0, bias_mem, tid, kThreads);
   if (grad)
     for (int i = tid; i < 2 * ndiag; i += kThreads) diag_mem[i] = 0.f;
   fence_before();
@@ -180,14 +181,15 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   }
   const int per_head = max(se - sb, 0), n = per_head * (KEYS ? p.group : 1);
 
-  constexpr uint32_t kAcc = 256;  // columns: S0 T0 S1 T1 (64 each), dv or nothing, dk or dq
+  constexpr int NB = kBuffers<DP, KEYS>;
+  // columns: buffers of S and dP (64 each), then dv and dk, or dq
+  constexpr uint32_t kAcc = NB * 128, kAcc2 = kAcc + (KEYS ? DP : 0);
   // registers: 5 groups of warps x 96 at the start; 4 x 104 + 64 = 480
   if (warp < 16) {
     take_registers<104>();
     const int w = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, lane = tid & 31;
     const int lane_row = quarter * 32 + lane, in_group = half * 128 + lane_row;
     const uint32_t lanes = (uint32_t)quarter << 21;
-    const uint32_t ts = tmem + lanes + w * 128 + half * kColumns, tt = ts + 64;
     const int row = r0 + lane_row;  // the key or the query
     const float c = p.scale * kLog2e;
     const float sigma = BF16 ? 1.f : ds_scale(x, b * p.kv_heads + hk, p.batch * p.kv_heads);
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     float* bias = bias_mem + (KEYS ? w * nbias : 0);
     float* diag = diag_mem + w * ndiag;
     float far_lo = 0.f, far_hi = 0.f;
+    int buffer = w, turn = 0;
     int head = -1, hh = 0, tile = sb + w;  // the streamed tile, and the head of the group it is of
     bool ok = true;
     for (int it = w; it < n; it += 2, tile += 2) {
@@ -222,10 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       }
       const int first = tile * kCols, c0 = first + half * kColumns, h = h0 + hh;
       const int slot = it % L::kSlots;
+      const uint32_t ts = tmem + lanes + buffer * 128 + half * kColumns, tt = ts + 64;
       if (KEYS && has_bias && h != head) {
         // every thread of the group is done with the head before
         if (!group_ok(w, ok)) break;
-        fill(bias, h, in_group, kGroup);
+        fill_bias(t, h, bias, in_group, kGroup);
         if (!group_ok(w, ok)) break;
       }
       head = h;
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       }
       const int s_len = KEYS ? p.q_len : p.k_len;
 
-      ok = bar_wait(bar(kSFull + w), (it >> 1) & 1, &dead, t.err);
+      ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err);
       fence_after();
       if (clean || KEYS) ok = bar_wait(bar(kFull + slot), (it / L::kSlots) & 1, &dead, t.err) && ok;
       if (joined) {
@@ -351,7 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       wait_st();
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(bar(kPReady + w));
+      if (lane == 0) bar_arrive(bar(kPReady + buffer));
+      buffer += 2;
+      if (buffer >= NB) buffer -= NB, turn ^= 1;
 
       if (grad) {
         // offsets of the tile: o = (first - start - r0) + column - row
@@ -411,28 +417,31 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       fence_after();
       const bool is_dv = KEYS && w == 0;
       const Strides st = KEYS ? (is_dv ? p.dvs : p.dks) : p.dqs;
-      uint16_t* out = (uint16_t*)(KEYS ? (is_dv ? p.dv : p.dk) : p.dq) + b * st.b + row * st.t +
+      uint16_t* out = (uint16_t*)(KEYS ? (is_dv ? p.dv : p.dk) : p.dq) + b * st.b + (row - lane) * st.t +
                       (KEYS ? hk : h0) * st.h;
-      const uint32_t from = tmem + lanes + kAcc + (KEYS && is_dv ? 0 : DP);
+      const uint32_t from = tmem + lanes + (is_dv ? kAcc : kAcc2);
       const float f = is_dv ? exp2f(-kLift<BF16>) : p.scale / sigma;
       constexpr int kShare = KEYS ? DP / 2 : DP / 4;
       const int begin = (KEYS ? half : 2 * w + half) * kShare;
-#pragma unroll 1
-      for (int y = begin; y < begin + kShare; y += 16) {
-        if (y >= t.dim16) break;
+      // through shared memory (rows of the owned tile, which no product reads any
+      // more), to be written by lines
+      constexpr int kPieces = kShare / 8;
+      unsigned char* stage = mem + warp * 32 * 128;
+#pragma unroll
+      for (int y = 0; y < kShare; y += 16) {
         uint32_t o[16];
-        if (n > 0) tmem_ld16(from + y, o);
+        if (n > 0) tmem_ld16(from + begin + y, o);
         wait_ld();
         tie16(o);
         uint32_t v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           v[e] = n > 0 ? pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
-        if (lane_row < owned) {
-          *(uint4*)(out + y) = make_uint4(v[0], v[1], v[2], v[3]);
-          if (y + 8 < p.dim) *(uint4*)(out + y + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-        }
+        stage_piece(stage, lane, y / 8, make_uint4(v[0], v[1], v[2], v[3]));
+        stage_piece(stage, lane, y / 8 + 1, make_uint4(v[4], v[5], v[6], v[7]));
       }
+      __syncwarp();
+      write_rows<kPieces>(stage, 0, out + begin, st.t, owned - quarter * 32, min(kPieces, (p.dim - begin) / 8));
       fence_before();
     }
   } else {
@@ -492,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         const bool ok = bar_wait(bar(n_bar), parity, &dead, t.err);
         return __all_sync(0xffffffffu, ok) != 0;
       };
-      auto scores = [&](int w, int slot) {
-        const uint32_t d = tmem + w * 128, from = base + L::kRing + slot * L::kSlot;
+      auto scores = [&](int buffer, int slot) {
+        const uint32_t d = tmem + buffer * 128, from = base + L::kRing + slot * L::kSlot;
 #pragma unroll
         for (int op = 0; op < 2; ++op)
 #pragma unroll
@@ -501,42 +510,44 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
             mma_ss(k < ksteps ? lead : 0u, d + op * 64,
                    desc_k(base + op * L::kOwn + (k / 4) * L::kOwnBox + (k % 4) * 32),
                    desc_k(from + op * L::kHalf + (k / 4) * L::kBox + (k % 4) * 32), id_s, k > 0);
-        mma_commit(lead, bar(kSFull + w));
+        mma_commit(lead, bar(kSFull + buffer));
       };
       // each half's 16-bit weights start where its scores did
       auto p_at = [](int k) { return (uint32_t)((k >> 1) * kColumns + (k & 1) * 8); };
-      // the ring's slot and round two tiles ahead of the one being summed
-      int ahead = 0, round = 0, slot = 0;
+      // slot, round and buffer of the next tile to get scores, and of the one
+      // being summed
+      int ahead = 0, ahead_slot = 0, ahead_round = 0, fill = 0;
+      int slot = 0, buffer = 0, turn = 0;
       bool ok = wait(kOwnFull, 0);
-      auto next_scores = [&](int w) {
-        ok = ok && wait(kFull + ahead, round);
+      auto next_scores = [&]() {
+        ok = ok && wait(kFull + ahead_slot, ahead_round);
         if (!ok) return;
-        scores(w, ahead);
-        if (++ahead == L::kSlots) ahead = 0, round ^= 1;
+        scores(fill, ahead_slot);
+        ++ahead;
+        if (++ahead_slot == L::kSlots) ahead_slot = 0, ahead_round ^= 1;
+        if (++fill == NB) fill = 0;
       };
-      next_scores(0);
-      if (n > 1) next_scores(1);
+      for (int i = 0; i < NB && i < n; ++i) next_scores();
       for (int it = 0; ok && it < n; ++it) {
-        const int w = it & 1;
-        ok = wait(kPReady + w, (it >> 1) & 1);
+        ok = wait(kPReady + buffer, turn);
         if (!ok) break;
         fence_after();
-        const uint32_t from = base + L::kRing + slot * L::kSlot;
+        const uint32_t from = base + L::kRing + slot * L::kSlot, p_from = tmem + buffer * 128;
         if (KEYS) {
 #pragma unroll
           for (int k = 0; k < kCols / 16; ++k)
-            mma_ts(lead, tmem + kAcc, tmem + w * 128 + p_at(k), desc_mn(from + L::kHalf + k * 2048, L::kBox), id_a,
+            mma_ts(lead, tmem + kAcc, p_from + p_at(k), desc_mn(from + L::kHalf + k * 2048, L::kBox), id_a,
                    it > 0 || k > 0);
         }
 #pragma unroll
         for (int k = 0; k < kCols / 16; ++k)
-          mma_ts(lead, tmem + kAcc + DP, tmem + w * 128 + 64 + p_at(k), desc_mn(from + k * 2048, L::kBox), id_a,
-                 it > 0 || k > 0);
+          mma_ts(lead, tmem + kAcc2, p_from + 64 + p_at(k), desc_mn(from + k * 2048, L::kBox), id_a, it > 0 || k > 0);
         mma_commit(lead, bar(kEmpty + slot));
         if (++slot == L::kSlots) slot = 0;
+        if (++buffer == NB) buffer = 0, turn ^= 1;
         // in order of issue: these scores replace P and dS only after the
         // products above have read them
-        if (it + 2 < n) next_scores(w);
+        if (ahead < n) next_scores();
       }
       if (ok) mma_commit(lead, bar(kDone));
     }

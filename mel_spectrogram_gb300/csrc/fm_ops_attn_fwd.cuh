@@ -50,7 +50,13 @@ struct Smem {
     return 1024 + kBias + (bias ? sizeof(float) * (2 * (max_distance + kBiasPad) + 1) : 0);
   }
 };
-enum { kFull = 0, kEmpty = 8, kQFull = 16, kSFull = 17, kPReady = 19, kOFull = 21, kBarCount = 23 };
+enum { kFull = 0, kEmpty = 8, kQFull = 16, kSFull = 17, kPReady = 20, kOFull = 23, kOReady = 25, kBarCount = 27 };
+// Score buffers of 128 columns. The tiles (key tile j, query tile w) are taken
+// in the order i = 2 j + w, buffer i % kBuffers. With three of them the scores
+// of a tile's successor are there before its softmax ends; beside two outputs
+// of 128 columns only two fit.
+template <int DP>
+constexpr int kBuffers = DP == 64 ? 3 : 2;
 
 // a barrier of the two warps that share 32 rows, which also tells whether both
 // are well: they leave together
@@ -88,11 +94,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   if (tid == 0) {
     for (int i = 0; i < L::kSlots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
     bar_init(bar(kQFull), 1);
-    for (int w = 0; w < 2; ++w) {
-      bar_init(bar(kSFull + w), 1);
-      bar_init(bar(kPReady + w), 8);
-      bar_init(bar(kOFull + w), 1);
-    }
+    for (int w = 0; w < 3; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 8);
+    for (int w = 0; w < 2; ++w) bar_init(bar(kOFull + w), 1), bar_init(bar(kOReady + w), 1);
     fence_bar_init();
     dead = 0;
     range[0] = 0x7fffffff;
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     tma_prefetch(&t.vm);
   }
   if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
-  if (MODE == 1 || (MODE == 2 && p.map)) fill_bias<BF16>(p, h, bias, tid, kThreads);
+  if (MODE == 1 || (MODE == 2 && p.map)) fill_bias(t, h, bias, tid, kThreads);
   fence_before();
   __syncthreads();
   fence_after();
@@ -128,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   }
   const int n = max(te - tb, 0);
 
-  constexpr uint32_t kO = 256;  // columns of O0; O1 follows at kO + DP
+  constexpr int NB = kBuffers<DP>;
+  constexpr uint32_t kO = NB * kTile;  // columns of O0; O1 follows at kO + DP
   // registers: the block starts with 5 groups x 96; the softmax threads take
   // 104 and leave the others 64 (4 x 104 + 64 = 480)
   if (warp < 16) {
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     const int w = warp >> 3, half = (warp >> 2) & 1, pair = (warp >> 3) * 4 + (warp & 3);
     const int lane_row = (warp & 3) * 32 + (tid & 31);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane 32 * (warp % 4) in bits 16 up
-    const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + kO + w * DP + half * (DP / 2);
+    const uint32_t to = tmem + lanes + kO + w * DP + half * (DP / 2);
     const int i = q0 + w * kTile + lane_row, place = info.start + i;
     const float c = p.scale * kLog2e;
     const float slope2 = MODE == 2 && p.slopes ? p.slopes[h] * kLog2e : 0.f;
@@ -160,7 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
 
     float m = -INFINITY, l = 0.f;  // l: of this thread's columns
     bool ok = true;
+    int buffer = w, turn = 0;  // of this tile's scores
     for (int j = 0; j < n; ++j) {
+      const uint32_t ts = tmem + lanes + buffer * kTile;
       const int k0 = (tb + j) * kTile, mine = k0 + half * kColumns;
       bool masked = k0 + kTile > all_end, clean = k0 + kTile > info.len && info.len < p.k_len, docs = false;
       if (kdocs) {
@@ -168,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         if (!(qr.z && kr.z && qr.x == kr.x)) docs = masked = true;
         if (!kr.z) clean = true;
       }
-      ok = bar_wait(bar(kSFull + w), j & 1, &dead, t.err);
+      ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err);
       fence_after();
       if (clean) {
         // rows of V that nothing may use become zeros: 0 weights times
@@ -216,6 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         m = top_m;
         l *= f;
         if (j > 0) {
+          // O has to hold all earlier products: two buffers' scores follow them
+          // in the tensor unit's order, of three they may not
+          if (NB == 3) {
+            ok = bar_wait(bar(kOReady + w), (j - 1) & 1, &dead, t.err);
+            fence_after();
+          }
 #pragma unroll 1
           for (int x = 0; x < DP / 2; x += 16) {
             uint32_t o[16];
@@ -249,7 +261,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       wait_st();
       fence_before();
       __syncwarp();
-      if (tid % 32 == 0) bar_arrive(bar(kPReady + w));
+      if (tid % 32 == 0) bar_arrive(bar(kPReady + buffer));
+      buffer += 2;
+      if (buffer >= NB) buffer -= NB, turn ^= 1;
     }
     // ---- the row's result, half of its columns a thread
     if (n > 0) ok = bar_wait(bar(kOFull + w), 0, &dead, t.err) && ok;
@@ -268,38 +282,55 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         if (t.splits > 1) t.part_lse[at] = lse2;
         else if (p.lse) p.lse[row] = lse2 * kLn2;
       }
-      uint16_t* rest = t.splits == 1 && p.rest ? (uint16_t*)p.rest + place_out : nullptr;
-#pragma unroll 1
-      for (int y = 0; y < DP / 2; y += 16) {
-        const int x = half * (DP / 2) + y;
-        if (x >= t.dim16) break;
+      // 16-bit results go through shared memory (this warp's rows and columns of
+      // the query tile, which no product reads any more) to be written by lines
+      constexpr int kPieces = DP / 16;  // of this thread's half row
+      unsigned char* stage = mem + w * L::kOperand + (DP == 128 ? half * L::kBox : 0) + (warp & 3) * 32 * 128;
+      const int first = DP == 128 ? 0 : half * kPieces, lane = tid & 31;
+      const int rows_left = p.q_len - (i - lane), pieces = min(kPieces, p.dim / 8 - half * kPieces);
+      auto result = [&](int y, float (&v)[16]) {
         uint32_t o[16];
         if (n > 0) tmem_ld16(to + y, o);
         wait_ld();
         tie16(o);
-        float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = n > 0 ? __uint_as_float(o[e]) * f : 0.f;
-        if (t.splits > 1) {
+      };
+      if (t.splits > 1) {
+#pragma unroll 1
+        for (int y = 0; y < DP / 2; y += 16) {
+          const int x = half * (DP / 2) + y;
+          float v[16];
+          result(y, v);
           if (store) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
               if (x + e < p.dim)
                 *(float4*)(t.part_o + at * p.dim + x + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
-        } else if (store) {
-          uint32_t r[8];
+        }
+      } else {
+        uint16_t* to_out = (uint16_t*)p.out + place_out - lane * p.os.t + half * (DP / 2);
+        uint16_t* to_rest = (uint16_t*)p.rest + place_out - lane * p.os.t + half * (DP / 2);
+#pragma unroll 1
+        for (int what = 0; what < (p.rest ? 2 : 1); ++what) {
+#pragma unroll 1
+          for (int y = 0; y < DP / 2; y += 16) {
+            float v[16];
+            result(y, v);
+            uint32_t r[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[e] = pack2<BF16>(v[2 * e], v[2 * e + 1]);
-          uint16_t* out = (uint16_t*)p.out + place_out + x;
-          *(uint4*)out = make_uint4(r[0], r[1], r[2], r[3]);
-          if (x + 8 < p.dim) *(uint4*)(out + 8) = make_uint4(r[4], r[5], r[6], r[7]);
-          if (rest) {
+            for (int e = 0; e < 8; ++e) r[e] = pack2<BF16>(v[2 * e], v[2 * e + 1]);
+            if (what) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = rest2<BF16>(v[2 * e], v[2 * e + 1], r[e]);
-            *(uint4*)(rest + x) = make_uint4(r[0], r[1], r[2], r[3]);
-            if (x + 8 < p.dim) *(uint4*)(rest + x + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+              for (int e = 0; e < 8; ++e) r[e] = rest2<BF16>(v[2 * e], v[2 * e + 1], r[e]);
+            }
+            stage_piece(stage, lane, first + y / 8, make_uint4(r[0], r[1], r[2], r[3]));
+            stage_piece(stage, lane, first + y / 8 + 1, make_uint4(r[4], r[5], r[6], r[7]));
           }
+          __syncwarp();
+          write_rows<kPieces>(stage, first, what ? to_rest : to_out, p.os.t, rows_left, pieces);
+          __syncwarp();
         }
       }
       fence_before();
@@ -336,57 +367,61 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       // ---- products
       const uint32_t id_s = instr_desc(kTile, kTile, BF16, false), id_o = instr_desc(kTile, t.dim16, BF16, true);
       const int ksteps = t.dim16 / 16;
-      auto scores = [&](int w, int slot) {
+      auto scores = [&](int w, int buffer, int slot) {
         const uint32_t a = base + w * L::kOperand, from = base + L::kRing + slot * L::kOperand;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t at = (k / 4) * L::kBox + (k % 4) * 32;
-          mma_ss(k < ksteps ? lead : 0u, tmem + w * kTile, desc_k(a + at), desc_k(from + at), id_s, k > 0);
+          mma_ss(k < ksteps ? lead : 0u, tmem + buffer * kTile, desc_k(a + at), desc_k(from + at), id_s, k > 0);
         }
-        mma_commit(lead, bar(kSFull + w));
+        mma_commit(lead, bar(kSFull + buffer));
       };
       auto wait = [&](int n_bar, uint32_t parity) {
         const bool ok = bar_wait(bar(n_bar), parity, &dead, t.err);
         return __all_sync(0xffffffffu, ok) != 0;
       };
-      // slot and round of the ring's next entries: V of this tile, K of the next
-      int sv = 1, rv = 0, sk = 2, rk = 0;
+      // slot and round of the ring's next K and next V
+      int sk = 0, rk = 0, sv = 1, rv = 0;
       auto advance = [&](int& s, int& r) {
         s += 2;
         if (s >= L::kSlots) s -= L::kSlots, r ^= 1;
       };
-      bool ok = wait(kQFull, 0) && wait(kFull, 0);
-      if (ok) {
-        scores(0, 0);
-        scores(1, 0);
-        mma_commit(lead, bar(kEmpty));
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        const bool more = j + 1 < n;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          ok = ok && (w || wait(kFull + sv, rv)) && wait(kPReady + w, j & 1);
-          if (!ok) break;
-          fence_after();
-          const uint32_t from = base + L::kRing + sv * L::kOperand;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(lead, tmem + kO + w * DP, tmem + w * kTile + k * 8, desc_mn(from + k * 2048, L::kBox), id_o,
-                   j > 0 || k > 0);
-          if (w) mma_commit(lead, bar(kEmpty + sv));
-          if (more) {
-            // the tensor unit runs products in the order of issue: these
-            // scores replace P only after the product above has read it
-            ok = w || wait(kFull + sk, rk);
-            if (!ok) break;
-            scores(w, sk);
-            if (w) mma_commit(lead, bar(kEmpty + sk));
-          } else {
-            mma_commit(lead, bar(kOFull + w));
-          }
+      bool ok = wait(kQFull, 0);
+      int ahead = 0, fill = 0;  // the next tile to get scores, and its buffer
+      auto next_scores = [&]() {
+        const int w = ahead & 1;
+        if (w == 0) ok = ok && wait(kFull + sk, rk);
+        if (!ok) return;
+        scores(w, fill, sk);
+        if (w) {
+          mma_commit(lead, bar(kEmpty + sk));
+          advance(sk, rk);
         }
-        advance(sv, rv);
-        advance(sk, rk);
+        ++ahead;
+        if (++fill == NB) fill = 0;
+      };
+      for (int i = 0; i < NB && i < 2 * n; ++i) next_scores();
+      int buffer = 0, turn = 0;
+      for (int i = 0; ok && i < 2 * n; ++i) {
+        const int w = i & 1;
+        ok = (w || wait(kFull + sv, rv)) && wait(kPReady + buffer, turn);
+        if (!ok) break;
+        fence_after();
+        const uint32_t from = base + L::kRing + sv * L::kOperand;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts(lead, tmem + kO + w * DP, tmem + buffer * kTile + k * 8, desc_mn(from + k * 2048, L::kBox), id_o,
+                 i > 1 || k > 0);
+        if (w) {
+          mma_commit(lead, bar(kEmpty + sv));
+          advance(sv, rv);
+        }
+        if (NB == 3) mma_commit(lead, bar(kOReady + w));
+        if (i + 2 >= 2 * n) mma_commit(lead, bar(kOFull + w));
+        if (++buffer == NB) buffer = 0, turn ^= 1;
+        // the tensor unit runs products in the order of issue: scores replace P
+        // only after the product above has read it
+        if (ahead < 2 * n) next_scores();
       }
     }
   }

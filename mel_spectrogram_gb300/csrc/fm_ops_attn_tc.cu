@@ -74,16 +74,25 @@ bool encode(CUtensorMap* m, const void* base, const Strides& s, int batch, int l
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Ids of each tile of 128 frames: {lowest, highest, all one id}; padding
-// frames count only against the last.
-__global__ void __launch_bounds__(kTile) doc_ranges(const int32_t* q_docs, const int32_t* k_docs, int q_len, int k_len,
-                                                    int q_tiles, int k_tiles, int4* out) {
+// Before the tiles' kernels, in one launch: the documents of each tile of 128
+// frames ({lowest, highest, all one id}; padding frames count only against the
+// last), by blocks x < tiles of row y = batch entry; and the bias by offset in
+// base 2, by the blocks after them with y = head.
+__global__ void __launch_bounds__(kTile) prepare(const AttnParams p, int q_tiles, int k_tiles, int4* ranges, int bf16,
+                                                 float* bias) {
   __shared__ int lo, hi, valid;
-  const int x = blockIdx.x, b = blockIdx.y;
+  const int tiles = ranges ? q_tiles + k_tiles : 0, x = blockIdx.x;
+  if (x >= tiles) {
+    const int W = 2 * p.max_distance + 1, i = (x - tiles) * kTile + threadIdx.x, h = blockIdx.y;
+    if (i < W && h < p.heads) bias[(long long)h * W + i] = kLog2e * table_value(p, (long long)p.map[i] * p.heads + h, bf16);
+    return;
+  }
+  const int b = blockIdx.y;
+  if (b >= p.batch) return;
   const bool keys = x >= q_tiles;
-  const int tile = keys ? x - q_tiles : x, len = keys ? k_len : q_len;
+  const int tile = keys ? x - q_tiles : x, len = keys ? p.k_len : p.q_len;
   const int at = tile * kTile + threadIdx.x;
-  const int id = at < len ? (keys ? k_docs : q_docs)[(long long)b * len + at] : -1;
+  const int id = at < len ? (keys ? p.k_docs : p.q_docs)[(long long)b * len + at] : -1;
   if (threadIdx.x == 0) lo = 0x7fffffff, hi = -1, valid = 0;
   __syncthreads();
   if (id >= 0) {
@@ -93,7 +102,7 @@ __global__ void __launch_bounds__(kTile) doc_ranges(const int32_t* q_docs, const
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    int4* to = keys ? out + (long long)gridDim.y * q_tiles + (long long)b * k_tiles : out + (long long)b * q_tiles;
+    int4* to = keys ? ranges + (long long)p.batch * q_tiles + (long long)b * k_tiles : ranges + (long long)b * q_tiles;
     to[tile] = make_int4(lo, hi, valid == kTile && lo == hi, 0);
   }
 }
@@ -172,40 +181,42 @@ __device__ __forceinline__ void block_peak(float v, float* to) {
 
 // Statistics of the backward pass by query, padded to whole tiles of 64:
 // base-2 lse (+inf where a query sees nothing or is padding: every weight
-// 2^(z - inf) is 0) less `lift`, and delta = dout . out. 16 lanes a row, 8
-// elements each; a block's 16 rows are of one head. peak: the largest squared
-// norm of a row of dout, by key head.
-template <typename T>
+// 2^(z - inf) is 0) less `lift`, and delta = dout . out. LANES threads a row, 8
+// elements each; block (x, head, batch entry). peak: the largest squared norm
+// of a row of dout, by key head.
+template <typename T, int LANES>
 __global__ void __launch_bounds__(256) bwd_stats(const AttnParams p, int q_pad, float lift, float* lse2, float* delta,
                                                  float* peak) {
-  const long long rows = (long long)p.batch * p.heads * q_pad, row = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int lane = threadIdx.x & 15;
-  const int i = (int)(row % q_pad), h = (int)(row / q_pad % p.heads), b = (int)(row / q_pad / p.heads);
+  const int lane = threadIdx.x % LANES, i = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int h = blockIdx.y, b = blockIdx.z;
   const bool there = i < p.q_len && (p.q_docs == nullptr || p.q_docs[(long long)b * p.q_len + i] >= 0);
-  float s = 0.f, norm = 0.f;
-  if (there && lane * 8 < p.dim) {
-    const Pack<T, 8> g = *(const Pack<T, 8>*)((const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h + lane * 8);
-    const long long at = b * p.os.b + i * p.os.t + h * p.os.h + lane * 8;
-    const Pack<T, 8> o = *(const Pack<T, 8>*)((const T*)p.out_in + at);
-    Pack<T, 8> rest{};
-    if (p.rest) rest = *(const Pack<T, 8>*)((const T*)p.rest + at);
+  const long long row = (long long)b * p.heads + h;
+  float s = 0.f, norm = 0.f, l = -INFINITY;
+  if (there) {
+    l = p.lse[row * p.q_len + i];
+    if (lane * 8 < p.dim) {
+      const Pack<T, 8> g = *(const Pack<T, 8>*)((const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h + lane * 8);
+      const long long at = b * p.os.b + i * p.os.t + h * p.os.h + lane * 8;
+      const Pack<T, 8> o = *(const Pack<T, 8>*)((const T*)p.out_in + at);
+      Pack<T, 8> rest{};
+      if (p.rest) rest = *(const Pack<T, 8>*)((const T*)p.rest + at);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float d = to_f(g.v[k]);
-      s = fmaf(d, to_f(o.v[k]) + to_f(rest.v[k]), s);
-      norm = fmaf(d, d, norm);
+      for (int k = 0; k < 8; ++k) {
+        const float d = to_f(g.v[k]);
+        s = fmaf(d, to_f(o.v[k]) + to_f(rest.v[k]), s);
+        norm = fmaf(d, d, norm);
+      }
     }
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o, 16);
-    norm += __shfl_xor_sync(0xffffffffu, norm, o, 16);
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o, LANES);
+    norm += __shfl_xor_sync(0xffffffffu, norm, o, LANES);
   }
   if (peak) block_peak(norm, peak + b * p.kv_heads + h / p.group);
-  if (lane == 0) {
-    const float l = there ? p.lse[((long long)b * p.heads + h) * p.q_len + i] : -INFINITY;
-    lse2[row] = l == -INFINITY ? INFINITY : l * kLog2e - lift;
-    delta[row] = s;
+  if (lane == 0 && i < q_pad) {
+    lse2[row * q_pad + i] = l == -INFINITY ? INFINITY : l * kLog2e - lift;
+    delta[row * q_pad + i] = s;
   }
 }
 
@@ -229,12 +240,6 @@ __global__ void __launch_bounds__(256) bwd_v_peak(const AttnParams p, float* pea
     top = fmaxf(top, norm);
   }
   block_peak(top, peak + b * p.kv_heads + h);
-}
-
-// bias[h][o + max_distance] in base 2
-__global__ void __launch_bounds__(256) bwd_bias(const AttnParams p, int bf16, float* bias) {
-  const int W = 2 * p.max_distance + 1, i = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y;
-  if (i < W) bias[(long long)h * W + i] = kLog2e * table_value(p, (long long)p.map[i] * p.heads + h, bf16);
 }
 
 // Rows (queries x heads that share a key head) up to which the few-query
@@ -295,7 +300,7 @@ TcPlan tc_plan(const AttnParams& p, bool backward) {
   w.peak = at;
   if (backward) at += align256((int64_t)sizeof(float) * 2 * p.batch * p.kv_heads);
   w.bias = at;
-  if (backward && p.map) at += align256((int64_t)sizeof(float) * p.heads * (2 * (int64_t)p.max_distance + 1));
+  if (p.map && w.step.splits == 0) at += align256((int64_t)sizeof(float) * p.heads * (2 * (int64_t)p.max_distance + 1));
   w.total = at;
   return w;
 }
@@ -321,12 +326,15 @@ fm_status tc_setup(TcParams& t, const AttnParams& p, int64_t dtype, const TcPlan
     return FM_ERR_CUDA;
   if (p.dout && !encode(&t.gm, p.dout, p.dos, p.batch, p.q_len, p.heads, p.dim, q_rows, bf16, &t.g_mh, &t.g_mb))
     return FM_ERR_CUDA;
-  if (p.q_docs) {
-    int4* r = (int4*)(ws + w.ranges);
-    doc_ranges<<<dim3(w.q_tiles + w.k_tiles, p.batch), kTile, 0, st>>>(p.q_docs, p.k_docs, p.q_len, p.k_len,
-                                                                       w.q_tiles, w.k_tiles, r);
+  if (p.q_docs || p.map) {
+    int4* r = p.q_docs ? (int4*)(ws + w.ranges) : nullptr;
+    float* bias = p.map ? (float*)(ws + w.bias) : nullptr;
+    const int tiles = r ? w.q_tiles + w.k_tiles : 0, spans = bias ? (2 * p.max_distance + kTile) / kTile : 0;
+    const int rows = r && bias ? (p.batch > p.heads ? p.batch : p.heads) : r ? p.batch : p.heads;
+    prepare<<<dim3(tiles + spans, rows), kTile, 0, st>>>(p, w.q_tiles, w.k_tiles, r, bf16, bias);
     t.q_ranges = r;
-    t.k_ranges = r + (int64_t)p.batch * w.q_tiles;
+    t.k_ranges = r ? r + (int64_t)p.batch * w.q_tiles : nullptr;
+    t.bias = bias;
   }
   return FM_OK;
 }
@@ -367,23 +375,23 @@ fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cu
   float* lse2 = (float*)(ws + w.stats);
   x.lse2 = lse2;
   x.delta = lse2 + rows;
-  const unsigned blocks = (unsigned)(rows / 16);  // q_pad is a multiple of 64
-  if (bf16) {
-    bwd_stats<__nv_bfloat16><<<blocks, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, lse2 + rows, nullptr);
-  } else {
-    float* peak = (float*)(ws + w.peak);
-    x.peak = peak;
-    const int count = p.batch * p.kv_heads;
+  const bool narrow = p.dim <= 64;
+  const int per_block = narrow ? 32 : 16;
+  const dim3 grid((x.q_pad + per_block - 1) / per_block, p.heads, p.batch);
+  float* peak = nullptr;
+  const int count = p.batch * p.kv_heads;
+  if (!bf16) {
+    peak = (float*)(ws + w.peak);
     if (cudaMemsetAsync(peak, 0, sizeof(float) * 2 * count, st) != cudaSuccess) return FM_ERR_CUDA;
-    bwd_stats<__half><<<blocks, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, lse2 + rows, peak);
     const int rows16 = (p.k_len + 15) / 16;
     bwd_v_peak<__half><<<dim3(rows16 < 16 ? rows16 : 16, p.kv_heads, p.batch), 256, 0, st>>>(p, peak + count);
+    x.peak = peak;
   }
-  if (p.map) {
-    float* bias = (float*)(ws + w.bias);
-    bwd_bias<<<dim3((2 * p.max_distance + 256) / 256, p.heads), 256, 0, st>>>(p, bf16, bias);
-    x.bias = bias;
-  }
+  float* delta = lse2 + rows;
+  if (bf16 && narrow) bwd_stats<__nv_bfloat16, 8><<<grid, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, delta, peak);
+  else if (bf16) bwd_stats<__nv_bfloat16, 16><<<grid, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, delta, peak);
+  else if (narrow) bwd_stats<__half, 8><<<grid, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, delta, peak);
+  else bwd_stats<__half, 16><<<grid, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, delta, peak);
   const int mode = mode_of(p);
   using Fn = fm_status (*)(const TcParams&, const bwd::Extra&, int, cudaStream_t);
   const bool small = p.dim <= 64;

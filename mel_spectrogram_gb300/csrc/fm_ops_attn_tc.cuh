@@ -27,6 +27,7 @@ struct TcParams {
   int q_tiles, k_tiles;  // of 128
   int dim16;             // dim rounded up to 16
   int splits, split_tiles;  // the key tiles of one split; splits > 1: partial results
+  const float* bias;     // [heads][2 * max_distance + 1]: the bias by offset, base 2
   float* part_o;         // [splits][batch][heads][q_len][dim]
   float* part_lse;       // [splits][batch][heads][q_len], base 2
   unsigned* err;
@@ -72,13 +73,28 @@ __device__ __forceinline__ int key_end(const AttnParams& p, const RowInfo& r, in
 
 // The head's bias by offset, in units of log2, padded by copies of its ends:
 // bias[o + max_distance + kBiasPad] for |o| <= max_distance + kBiasPad.
-template <bool BF16>
-__device__ __forceinline__ void fill_bias(const AttnParams& p, int h, float* bias, int tid, int threads) {
-  const int D = p.max_distance;
-  for (int i = tid; i < 2 * (D + kBiasPad) + 1; i += threads) {
-    const int at = min(max(i - kBiasPad, 0), 2 * D);
-    bias[i] = kLog2e * table_value(p, (long long)p.map[at] * p.heads + h, BF16);
-  }
+__device__ __forceinline__ void fill_bias(const TcParams& t, int h, float* bias, int tid, int threads) {
+  const int D = t.p.max_distance;
+  const float* from = t.bias + (long long)h * (2 * D + 1);
+  for (int i = tid; i < 2 * (D + kBiasPad) + 1; i += threads) bias[i] = from[min(max(i - kBiasPad, 0), 2 * D)];
+}
+
+// 16 bits x 16 columns of this thread's row, staged so that a warp writes whole
+// lines: rows of `stage` are 128 bytes, their 16-byte pieces in an order that
+// keeps eight rows' same pieces on different banks.
+__device__ __forceinline__ void stage_piece(unsigned char* stage, int row, int piece, uint4 v) {
+  *(uint4*)(stage + row * 128 + ((piece ^ (row & 7)) << 4)) = v;
+}
+// The warp's 32 rows of PIECES 16-byte pieces each, from `first` on, to rows of
+// `stride` elements at `to`; `rows` of them exist, and `pieces` of their pieces.
+template <int PIECES>
+__device__ __forceinline__ void write_rows(const unsigned char* stage, int first, uint16_t* to, long long stride,
+                                           int rows, int pieces) {
+  const int lane = threadIdx.x & 31, piece = lane % PIECES;
+#pragma unroll
+  for (int r = lane / PIECES; r < 32; r += 32 / PIECES)
+    if (r < rows && piece < pieces)
+      *(uint4*)(to + r * stride + 8 * piece) = *(const uint4*)(stage + r * 128 + (((first + piece) ^ (r & 7)) << 4));
 }
 
 // A row's N raw products of one tile, to scores in base 2: scaled or capped,
@@ -120,17 +136,7 @@ __device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SL
         a[i] = both(tanh_over_x[i] * power);
         power *= k2;
       }
-#pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        const float2 x = make_float2(s[j], s[j + 1]);
-        float2 t;
-        if (small) {
-          const float2 q = mul2(x, x);
-          t = mul2(fma2(fma2(fma2(a[3], q, a[2]), q, a[1]), q, a[0]), x);
-        } else {
-          const float c2 = 2.f * kLog2e * k;
-          t = make_float2(out * tanh_from(x.x * c2), out * tanh_from(x.y * c2));
-        }
+      auto finish = [&](int j, float2 t) {
         if (CAP_SLOPE) {
           const float2 th = mul2(t, in), f = fma2(make_float2(-th.x, -th.y), th, both(1.f));
           slope[j] = f.x;
@@ -139,6 +145,20 @@ __device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SL
         const float2 z = add2(t, fma2(g2, make_float2((float)j, (float)(j + 1)), base));
         s[j] = z.x;
         s[j + 1] = z.y;
+      };
+      // two loops: with the choice inside one, its branches kept the columns'
+      // chains of multiply-adds from overlapping (four times slower)
+      if (small) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          const float2 x = make_float2(s[j], s[j + 1]), q = mul2(x, x);
+          finish(j, mul2(fma2(fma2(fma2(a[3], q, a[2]), q, a[1]), q, a[0]), x));
+        }
+      } else {
+        const float c2 = 2.f * kLog2e * k;
+#pragma unroll
+        for (int j = 0; j < N; j += 2)
+          finish(j, make_float2(out * tanh_from(s[j] * c2), out * tanh_from(s[j + 1] * c2)));
       }
     } else {
 #pragma unroll
