@@ -23,15 +23,27 @@ __host__ __device__ inline int pitch_of(int dim) {
   return 4 * (d4 | 1);
 }
 
-template <typename T>
-__device__ __forceinline__ void stage(float* to, const T* from, long long stride, int n, int rows, int dim, int pitch,
+// Stages ROWS rows of up to 64 G elements: 16 threads a row, and every thread
+// has all its loads of 16 rows under way before it writes the first (one load
+// at a time, each waiting for the last, took most of a small problem's time).
+template <typename T, int G, int ROWS>
+__device__ __forceinline__ void stage(float* to, const T* from, long long stride, int n, int dim, int pitch,
                                       const int32_t* docs) {
   // rows at or past n, and padding frames, arrive as zeros whatever memory holds
-  for (int e = threadIdx.x; e < rows * pitch; e += kThreads) {
-    const int r = e / pitch, d = e - r * pitch;
-    float v = 0.f;
-    if (r < n && d < dim && (docs == nullptr || docs[r] >= 0)) v = to_f(from[r * stride + d]);
-    to[e] = v;
+  const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
+#pragma unroll
+  for (int r0 = 0; r0 < ROWS; r0 += kThreads / 16) {
+    const int r = r0 + sub;
+    const bool real = r < n && (docs == nullptr || docs[r] >= 0);
+    const T* row = from + r * stride;
+    float v[4 * G];
+#pragma unroll
+    for (int k = 0; k < 4 * G; ++k) v[k] = real && lane + 16 * k < dim ? to_f(row[lane + 16 * k]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4 * G; ++k)
+      if (lane + 16 * k < pitch) to[r * pitch + lane + 16 * k] = v[k];
+    // a pitch one float4 past 64 G: its last four
+    if (pitch > 64 * G && lane < pitch - 64 * G) to[r * pitch + 64 * G + lane] = 0.f;
   }
 }
 
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
   const T* k = (const T*)p.k + b * p.ks.b + hk * p.ks.h;
   const T* v = (const T*)p.v + b * p.vs.b + hk * p.vs.h;
   const int nq = min(kRows, p.q_len - i0);
-  stage(Q, q, p.qs.t, nq, kRows, p.dim, pitch, score.qd ? score.qd + i0 : nullptr);
+  stage<T, G, kRows>(Q, q, p.qs.t, nq, p.dim, pitch, score.qd ? score.qd + i0 : nullptr);
   float4 acc[4][G];
   clear(acc);
   float m[4], l[4];
@@ -200,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
   for (int j0 = 0; j0 < end; j0 += kFwdKeys) {
     const int n = min(kFwdKeys, score.r.len - j0);
     __syncthreads();
-    stage(K, k + j0 * p.ks.t, p.ks.t, n, kFwdKeys, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
-    stage(V, v + j0 * p.vs.t, p.vs.t, n, kFwdKeys, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
+    stage<T, G, kFwdKeys>(K, k + j0 * p.ks.t, p.ks.t, n, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
+    stage<T, G, kFwdKeys>(V, v + j0 * p.vs.t, p.vs.t, n, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
     __syncthreads();
     float s[4][4];
     products<4>(Q, K, p.dim, pitch, tx, ty, s);
@@ -267,8 +279,8 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
   const int owned = min(kRows, (OF_KEYS ? p.k_len : p.q_len) - r0);
   if (OF_KEYS) {
     const int n = min(owned, info.len - r0);
-    stage(R1, k + r0 * p.ks.t, p.ks.t, n, kRows, p.dim, pitch, kd ? kd + r0 : nullptr);
-    stage(R2, v + r0 * p.vs.t, p.vs.t, n, kRows, p.dim, pitch, kd ? kd + r0 : nullptr);
+    stage<T, G, kRows>(R1, k + r0 * p.ks.t, p.ks.t, n, p.dim, pitch, kd ? kd + r0 : nullptr);
+    stage<T, G, kRows>(R2, v + r0 * p.vs.t, p.vs.t, n, p.dim, pitch, kd ? kd + r0 : nullptr);
   }
   float4 a1[4][G], a2[4][G];
   clear(a1);
@@ -286,8 +298,8 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
     const float* lse = p.lse + ((long long)b * p.heads + h) * p.q_len;
     const float* delta = p.delta + ((long long)b * p.heads + h) * p.q_len;
     if (!OF_KEYS) {
-      stage(R1, q + r0 * p.qs.t, p.qs.t, owned, kRows, p.dim, pitch, qd ? qd + r0 : nullptr);
-      stage(R2, g + r0 * p.dos.t, p.dos.t, owned, kRows, p.dim, pitch, qd ? qd + r0 : nullptr);
+      stage<T, G, kRows>(R1, q + r0 * p.qs.t, p.qs.t, owned, p.dim, pitch, qd ? qd + r0 : nullptr);
+      stage<T, G, kRows>(R2, g + r0 * p.dos.t, p.dos.t, owned, p.dim, pitch, qd ? qd + r0 : nullptr);
     }
     int begin = 0, end = OF_KEYS ? p.q_len : info.len;
     if (p.causal && !OF_KEYS) end = min(end, max(info.start + r0 + owned, info.prefix));
@@ -296,11 +308,11 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
       const int n = min(kBwdCols, end - c0);
       __syncthreads();
       if (OF_KEYS) {
-        stage(C1, q + c0 * p.qs.t, p.qs.t, n, kBwdCols, p.dim, pitch, qd ? qd + c0 : nullptr);
-        stage(C2, g + c0 * p.dos.t, p.dos.t, n, kBwdCols, p.dim, pitch, qd ? qd + c0 : nullptr);
+        stage<T, G, kBwdCols>(C1, q + c0 * p.qs.t, p.qs.t, n, p.dim, pitch, qd ? qd + c0 : nullptr);
+        stage<T, G, kBwdCols>(C2, g + c0 * p.dos.t, p.dos.t, n, p.dim, pitch, qd ? qd + c0 : nullptr);
       } else {
-        stage(C1, k + c0 * p.ks.t, p.ks.t, n, kBwdCols, p.dim, pitch, kd ? kd + c0 : nullptr);
-        stage(C2, v + c0 * p.vs.t, p.vs.t, n, kBwdCols, p.dim, pitch, kd ? kd + c0 : nullptr);
+        stage<T, G, kBwdCols>(C1, k + c0 * p.ks.t, p.ks.t, n, p.dim, pitch, kd ? kd + c0 : nullptr);
+        stage<T, G, kBwdCols>(C2, v + c0 * p.vs.t, p.vs.t, n, p.dim, pitch, kd ? kd + c0 : nullptr);
       }
       __syncthreads();
       float s[4][2], dp[4][2];

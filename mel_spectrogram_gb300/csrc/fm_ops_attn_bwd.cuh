@@ -51,18 +51,31 @@ struct Smem {
   static constexpr int kHalf = kBoxes * kBox;  // one streamed operand
   static constexpr int kStats = 2 * kHalf;     // lse and delta of the slot's queries
   static constexpr int kSlot = 2 * kHalf + 1024;
-  static constexpr int kSlots = DP == 64 ? 6 : KEYS ? 4 : 3;
-  static constexpr int kRing = 2 * kOwn;
-  static constexpr int kBars = kRing + kSlots * kSlot;
-  static constexpr int kBias = kBars + 256;
+  static constexpr int kMaxSlots = 6;
+  static constexpr int kBars = 2 * kOwn;
+  static constexpr int kRing = kBars + 1024;
   // floats, whole 16-byte units: the bias by offset, the bias gradient by offset
   __host__ __device__ static int bias_floats(int max_distance) { return (2 * (max_distance + kBiasPad) + 4) & ~3; }
   __host__ __device__ static int diag_floats(int max_distance) { return (2 * (max_distance + kDiagPad) + 4) & ~3; }
-  static size_t bytes(int max_distance, bool bias, bool grad) {
-    size_t n = 1024 + kBias;
+  // what follows the ring: the bias (a copy for each group where heads change
+  // on the way), the bias gradient by offset for each group, the chains'
+  // results (and at the end the far sums, in their place)
+  static size_t tail(int max_distance, bool bias, bool grad) {
+    size_t n = 0;
     if (bias) n += sizeof(float) * (KEYS ? 2 : 1) * bias_floats(max_distance);
-    if (grad) n += sizeof(float) * (2 * diag_floats(max_distance) + 8 * kChains * kChainEntries + 1024);
+    if (grad) n += sizeof(float) * (2 * diag_floats(max_distance) + 8 * kChains * kChainEntries);
     return n;
+  }
+  // streamed tiles the ring holds: what shared memory (227 KB, less a little
+  // for static variables and the base's alignment) has room for. Three at least
+  // for any map; with three a tile's copy starts only when the tile three
+  // before it is summed.
+  static int slots(int max_distance, bool bias, bool grad) {
+    const int n = (int)((227 * 1024 - 256 - 1024 - kRing - tail(max_distance, bias, grad)) / kSlot);
+    return n < kMaxSlots ? n : kMaxSlots;
+  }
+  static size_t bytes(int max_distance, bool bias, bool grad) {
+    return 1024 + kRing + (size_t)slots(max_distance, bias, grad) * kSlot + tail(max_distance, bias, grad);
   }
 };
 enum { kFull = 0, kEmpty = 8, kOwnFull = 16, kSFull = 17, kPReady = 20, kDone = 23 };
@@ -95,6 +108,7 @@ struct Extra {
   int q_pad;           // q_len rounded up to 64
   // [batch * kv_heads] largest squared norms of a row of dout, then of v (f16)
   const float* peak;
+  int slots;  // tiles of the ring
 };
 // the power of two for dS
 __device__ __forceinline__ float ds_scale(const Extra& x, int at, int count) {
@@ -121,11 +135,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   const bool grad = !KEYS && p.part != nullptr;
   // the group's threads meet at barriers: then they also leave together
   const bool joined = grad || (KEYS && has_bias);
-  float* bias_mem = (float*)(mem + L::kBias);
+  float* bias_mem = (float*)(mem + L::kRing + x.slots * L::kSlot);
   float* diag_mem = bias_mem + (has_bias ? (KEYS ? 2 : 1) * nbias : 0);  // [2][ndiag]
   const int ndiag = L::diag_floats(D);
   float* chain_mem = diag_mem + 2 * ndiag;  // [group][quarter of the rows][kChains][kChainEntries]
-  float* far_mem = chain_mem + 8 * kChains * kChainEntries;  // [2][512]
+  float* far_mem = chain_mem;  // [2][512], after the last chain
 
   const int b = blockIdx.z;
   const int r0 = (!KEYS && p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * kTile;
@@ -135,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   const int owned = min(kTile, (KEYS ? p.k_len : p.q_len) - r0);
 
   if (tid == 0) {
-    for (int i = 0; i < L::kSlots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
+    for (int i = 0; i < x.slots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
     bar_init(bar(kOwnFull), 1);
     for (int w = 0; w < 3; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 8);
     bar_init(bar(kDone), 1);
@@ -182,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   const int per_head = max(se - sb, 0), n = per_head * (KEYS ? p.group : 1);
 
   constexpr int NB = kBuffers<DP, KEYS>;
+  float far_lo = 0.f, far_hi = 0.f;  // bias gradients beyond the map, of this thread's row
   // columns: buffers of S and dP (64 each), then dv and dk, or dq
   constexpr uint32_t kAcc = NB * 128, kAcc2 = kAcc + (KEYS ? DP : 0);
   // registers: 5 groups of warps x 96 at the start; 4 x 104 + 64 = 480
@@ -215,8 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     }
     float* bias = bias_mem + (KEYS ? w * nbias : 0);
     float* diag = diag_mem + w * ndiag;
-    float far_lo = 0.f, far_hi = 0.f;
-    int buffer = w, turn = 0;
+    int buffer = w, turn = 0, slot = w, round = 0;
     int head = -1, hh = 0, tile = sb + w;  // the streamed tile, and the head of the group it is of
     bool ok = true;
     for (int it = w; it < n; it += 2, tile += 2) {
@@ -224,7 +238,6 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         while (tile >= se) tile -= per_head, ++hh;
       }
       const int first = tile * kCols, c0 = first + half * kColumns, h = h0 + hh;
-      const int slot = it % L::kSlots;
       const uint32_t ts = tmem + lanes + buffer * 128 + half * kColumns, tt = ts + 64;
       if (KEYS && has_bias && h != head) {
         // every thread of the group is done with the head before
@@ -258,10 +271,15 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         if (!o.z) clean = true;
       }
       const int s_len = KEYS ? p.q_len : p.k_len;
+      uint32_t seen = ~0u;  // bit j: column j is seen
+      if (masked) {
+        seen = (uint32_t)column_range<kColumns>(lo, min(hi, s_len - c0));
+        if (docs) seen &= (uint32_t)same_document<kColumns>(sdocs + c0, s_len - c0, rd);
+      }
 
       ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err);
       fence_after();
-      if (clean || KEYS) ok = bar_wait(bar(kFull + slot), (it / L::kSlots) & 1, &dead, t.err) && ok;
+      if (clean || KEYS) ok = bar_wait(bar(kFull + slot), round, &dead, t.err) && ok;
       if (joined) {
         if (!group_ok(w, ok)) break;
       } else if (!__all_sync(0xffffffffu, ok)) {
@@ -293,11 +311,6 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       if (MODE != 2) tie32(dp);
       tile_scores<kColumns, MODE, KEYS, MODE == 2>(s, slope, p, c, bias, slope2,
                                                    KEYS ? row - (info.start + c0) : c0 - (info.start + row));
-      uint32_t seen = ~0u;  // bit j: column j is seen
-      if (masked) {
-        seen = (uint32_t)column_range<kColumns>(lo, min(hi, s_len - c0));
-        if (docs) seen &= (uint32_t)same_document<kColumns>(sdocs + c0, s_len - c0, rd);
-      }
 #pragma unroll
       for (int j = 0; j < kColumns; j += 4) {
         float4 q = make_float4(row_lse, row_lse, row_lse, row_lse);
@@ -358,6 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       if (lane == 0) bar_arrive(bar(kPReady + buffer));
       buffer += 2;
       if (buffer >= NB) buffer -= NB, turn ^= 1;
+      slot += 2;
+      if (slot >= x.slots) slot -= x.slots, round ^= 1;
 
       if (grad) {
         // offsets of the tile: o = (first - start - r0) + column - row
@@ -409,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         }
       }
     }
-    if (grad) far_mem[tid] = far_lo, far_mem[512 + tid] = far_hi;
     // ---- results: a group each for dv and dk, or half of dq's columns each,
     // and half of those a thread
     if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(bar(kDone), 0, &dead, t.err));
@@ -466,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
           }
       }
       int tile = sb, h = h0;
+      int s = 0, round = 1;
       for (int it = 0; it < n; ++it) {
-        const int s = it % L::kSlots, round = it / L::kSlots;
-        const bool ok = bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err);
+        const bool ok = bar_wait(bar(kEmpty + s), round, &dead, t.err);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (lead) {
           const uint32_t full = bar(kFull + s), to = base + L::kRing + s * L::kSlot;
@@ -492,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         }
         __syncwarp();
         if (++tile == se) tile = sb, ++h;
+        if (++s == x.slots) s = 0, round ^= 1;
       }
     } else if (warp == 17 && n > 0) {
       // ---- products
@@ -524,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         if (!ok) return;
         scores(fill, ahead_slot);
         ++ahead;
-        if (++ahead_slot == L::kSlots) ahead_slot = 0, ahead_round ^= 1;
+        if (++ahead_slot == x.slots) ahead_slot = 0, ahead_round ^= 1;
         if (++fill == NB) fill = 0;
       };
       for (int i = 0; i < NB && i < n; ++i) next_scores();
@@ -543,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         for (int k = 0; k < kCols / 16; ++k)
           mma_ts(lead, tmem + kAcc2, p_from + 64 + p_at(k), desc_mn(from + k * 2048, L::kBox), id_a, it > 0 || k > 0);
         mma_commit(lead, bar(kEmpty + slot));
-        if (++slot == L::kSlots) slot = 0;
+        if (++slot == x.slots) slot = 0;
         if (++buffer == NB) buffer = 0, turn ^= 1;
         // in order of issue: these scores replace P and dS only after the
         // products above have read them
@@ -554,6 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   }
   __syncthreads();
   if (grad) {
+    if (warp < 16) far_mem[tid] = far_lo, far_mem[512 + tid] = far_hi;
+    __syncthreads();
     // this tile's row of partial bias gradients: the two groups, and at the
     // ends of the map what lay beyond them
     float* part = p.part + (((long long)b * t.q_tiles + r0 / kTile) * p.heads + h0) * (2 * D + 1);
@@ -582,10 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
 }
 
 template <int DP, bool BF16, bool KEYS>
-fm_status launch(const TcParams& t, const Extra& x, int mode, cudaStream_t st) {
+fm_status launch(const TcParams& t, Extra x, int mode, cudaStream_t st) {
   const int rows = KEYS ? t.p.k_len : t.p.q_len;
   const dim3 grid((rows + kTile - 1) / kTile, KEYS ? t.p.kv_heads : t.p.heads, t.p.batch);
-  const size_t smem = Smem<DP, KEYS>::bytes(t.p.max_distance, t.p.map != nullptr, !KEYS && t.p.part != nullptr);
+  const bool bias = t.p.map != nullptr, grad = !KEYS && t.p.part != nullptr;
+  const size_t smem = Smem<DP, KEYS>::bytes(t.p.max_distance, bias, grad);
+  x.slots = Smem<DP, KEYS>::slots(t.p.max_distance, bias, grad);
+  if (x.slots < 3) return FM_ERR_UNSUPPORTED;
   auto k = mode == 0 ? kernel<DP, BF16, 0, KEYS> : mode == 1 ? kernel<DP, BF16, 1, KEYS> : kernel<DP, BF16, 2, KEYS>;
   if (!allow_smem(k, smem)) return FM_ERR_CUDA;
   k<<<grid, kThreads, smem, st>>>(t, x);

@@ -174,6 +174,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         if (!(qr.z && kr.z && qr.x == kr.x)) docs = masked = true;
         if (!kr.z) clean = true;
       }
+      uint64_t seen = ~0ull;  // bit e: column e of this thread's is seen
+      if (masked) {
+        seen = column_range<kColumns>(0, seen_end - mine);
+        if (docs) seen &= same_document<kColumns>(kdocs + mine, p.k_len - mine, qd);
+      }
       ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err);
       fence_after();
       if (clean) {
@@ -199,8 +204,6 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       tie32(u + 32);
       tile_scores<kColumns, MODE, false, false>(s, unused, p, c, bias, slope2, mine - place);
       if (masked) {
-        uint64_t seen = column_range<kColumns>(0, seen_end - mine);
-        if (docs) seen &= same_document<kColumns>(kdocs + mine, p.k_len - mine, qd);
         const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
         for (int e = 0; e < kColumns; ++e) s[e] = ((e < 32 ? lo : hi) >> (e & 31) & 1) ? s[e] : -INFINITY;

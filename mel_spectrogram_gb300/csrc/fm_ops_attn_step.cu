@@ -4,12 +4,13 @@
 // Bound by reading K and V once. The queries of all heads that share a key
 // head make the rows of one 16-row operand (row = query * group + head), so
 // that the cache crosses HBM once whatever the grouping; products run on
-// mma.sync (16 rows would leave 7/8 of a tcgen05 tile empty, and the products
-// take a tenth of the time that the loads do). The key axis is split over
-// blocks, and within a block over its warps, each with its own ring of tiles
-// of 16 keys filled by cp.async: no barrier in the loop, two tiles a warp and
-// 128 KB an SM in flight. Warps join through shared memory, blocks through the
-// join kernel.
+// mma.sync (16 rows would leave 7/8 of a tcgen05 tile empty). The key axis is
+// split over blocks, and within a block over its warps, each with a ring of two
+// tiles of 16 keys of its own that one lane fills by TMA: no barrier between
+// warps in the loop, and the copies cost no instructions of the other lanes
+// (with cp.async they took a third of 633 instructions a tile, which is what
+// bound the kernel, at 38 % of the bandwidth). Warps join through shared
+// memory, blocks through the join kernel.
 #include "fm_ops_attn_tc.cuh"
 
 namespace fm {
@@ -17,21 +18,18 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 4, kKeys = 16, kStages = 3;
+constexpr int kWarps = 4, kKeys = 16, kStages = 2;
 
+// a multiple of 1024 bytes, as TMA's swizzle wants
 template <int DP>
 constexpr int stage_bytes() { return 2 * kKeys * DP * 2; }
 template <int DP>
 constexpr size_t smem_bytes() {
-  const size_t ring = (size_t)kWarps * kStages * stage_bytes<DP>();
+  const size_t ring = (size_t)kWarps * kStages * stage_bytes<DP>() + 1024;  // and its alignment
   const size_t out = (size_t)kWarps * 16 * (DP + 2) * sizeof(float);  // warps' results, over the ring
   return ring > out ? ring : out;
 }
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
-  const int n = real ? 16 : 0;  // the rest of the 16 bytes becomes zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t at, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -60,19 +58,35 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+
 struct StepParams {
   AttnParams p;
+  CUtensorMap km, vm;  // {dim, token, head, batch}, boxes of 64 x 16
+  int k_mh, k_mb, v_mh, v_mb;
+  unsigned* err;
   int splits, split_keys;  // keys of one split, a multiple of kWarps * kKeys
   int row_tiles;
   float *part_o, *part_lse;
 };
 
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
-  extern __shared__ __align__(128) unsigned char raw[];
+__global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ StepParams t) {
+  extern __shared__ unsigned char raw[];
   __shared__ float stat[2][kWarps][16];
+  __shared__ uint64_t full[kWarps][kStages];
+  __shared__ volatile int dead;
+  unsigned char* mem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const AttnParams& p = t.p;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  constexpr int kBoxes = DP / 64, kBox = kKeys * 128, kOperand = kBoxes * kBox;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) bar_init(smem_u32(&full[warp][s]), 1);
+    fence_bar_init();
+    if (warp == 0) dead = 0;
+  }
+  __syncthreads();
   const int split = blockIdx.x / t.row_tiles, rt = blockIdx.x % t.row_tiles;
   const int hk = blockIdx.y, b = blockIdx.z;
   const RowInfo info = row_info(p, b);
@@ -123,55 +137,56 @@ __global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
   const int32_t* kdocs = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
 
   // ---- the warp's ring: tile n of the split's tiles warp, warp + 4, ...
-  const uint32_t ring = smem_u32(raw) + warp * kStages * stage_bytes<DP>();
-  const uint16_t* kbase = (const uint16_t*)p.k + b * p.ks.b + hk * p.ks.h;
-  const uint16_t* vbase = (const uint16_t*)p.v + b * p.vs.b + hk * p.vs.h;
+  const uint32_t ring = smem_u32(mem) + warp * kStages * stage_bytes<DP>();
   const int tiles = k_end > k_begin ? (k_end - k_begin + kKeys - 1) / kKeys : 0;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-  const int chunks = 2 * steps;  // 16-byte pieces of a row that are used
   auto load = [&](int n) {
-    if (n < mine) {
+    if (lane == 0 && n < mine) {
       const int k0 = k_begin + (warp + n * kWarps) * kKeys;
-      const uint32_t to = ring + (n % kStages) * stage_bytes<DP>();
-      // half a warp a row pair: 16 lanes cover up to 16 pieces of one row
+      const uint32_t to = ring + (n % kStages) * stage_bytes<DP>(), bar = smem_u32(&full[warp][n % kStages]);
+      bar_expect(bar, 2 * kOperand);
 #pragma unroll
-      for (int r = 0; r < kKeys; r += (DP == 128 ? 2 : 4)) {
-        const int row = r + lane / (DP / 8), piece = lane % (DP / 8);
-        const int key = k0 + row;
-        bool real = key < k_end;
-        if (kdocs) real = real && kdocs[key] >= 0;
-        const bool data = real && piece * 8 < p.dim;
-        const long long at = data ? key : 0;  // an address to leave unread
-        const int d = data ? piece * 8 : 0;
-        const uint32_t place = row * (DP * 2) + ((piece ^ (row & 7)) << 4);
-        if (piece < chunks) {
-          copy16(to + place, kbase + at * p.ks.t + d, data);
-          copy16(to + kKeys * DP * 2 + place, vbase + at * p.vs.t + d, data);
-        }
+      for (int x = 0; x < kBoxes; ++x) {
+        tma_load(to + x * kBox, &t.km, bar, 64 * x, k0, hk * t.k_mh, b * t.k_mb);
+        tma_load(to + kOperand + x * kBox, &t.vm, bar, 64 * x, k0, hk * t.v_mh, b * t.v_mb);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   float o[DP / 8][4];
 #pragma unroll
   for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-  for (int n = 0; n < kStages - 1; ++n) load(n);
+  bool ok = true;
+  const float cap_in = p.cap > 0.f ? 2.f * kLog2e * p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
+  // this lane's places in a tile: rows of 128 bytes with TMA's swizzle, whose
+  // pieces 2 st + x stand at (x ^ row % 8) ^ 2 st (64 columns further: next box)
+  const int k_row = (lane & 7) + ((lane & 16) >> 1), v_row = lane & 15;
+  const uint32_t k_place = k_row * 128 + ((((lane >> 3) & 1) ^ (k_row & 7)) << 4);
+  const uint32_t v_place = v_row * 128 + (((lane >> 4) ^ (v_row & 7)) << 4);
+  for (int n = 0; n < kStages; ++n) load(n);
   for (int n = 0; n < mine; ++n) {
-    load(n + kStages - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    __syncwarp();
+    ok = bar_wait(smem_u32(&full[warp][n % kStages]), (n / kStages) & 1, &dead, t.err);
+    if (!__all_sync(0xffffffffu, ok)) break;
     const int k0 = k_begin + (warp + n * kWarps) * kKeys;
-    const uint32_t K = ring + (n % kStages) * stage_bytes<DP>(), V = K + kKeys * DP * 2;
+    const uint32_t K = ring + (n % kStages) * stage_bytes<DP>(), V = K + kOperand;
+    if (k0 + kKeys > info.len || kdocs) {
+      // rows of V that nothing may use become zeros: 0 weights times whatever
+      // memory holds would not be 0
+      const int row = lane >> 1, key = k0 + row;
+      if (key >= info.len || (kdocs && kdocs[key] < 0)) {
+        unsigned char* to = mem + (V - smem_u32(mem)) + row * 128 + (lane & 1) * 64;
+        for (int x = 0; x < kBoxes; ++x)
+          for (int e = 0; e < 4; ++e) *(uint4*)(to + x * kBox + 16 * e) = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       if (st < steps) {
         // four 8 x 8 pieces: keys 0-7 and 8-15, dims 16 st and 16 st + 8
-        const int row = (lane & 7) + ((lane & 16) >> 1), piece = 2 * st + ((lane >> 3) & 1);
         uint32_t kf[4];
-        ldsm4(K + row * (DP * 2) + ((piece ^ (row & 7)) << 4), kf);
+        ldsm4(K + (st / 4) * kBox + (k_place ^ ((st % 4) << 5)), kf);
         mma16<BF16>(s[0], q[st], kf[0], kf[1]);
         mma16<BF16>(s[1], q[st], kf[2], kf[3]);
       }
@@ -187,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
       for (int e = 0; e < 4; ++e) {
         const int r = e >> 1, key = k0 + 8 * x + pair + (e & 1), off = key - info.start - qi[r];
         float z = s[x][e];
-        if (p.cap > 0.f) z = p.cap * kLog2e * tanh_from(z * (2.f * kLog2e * p.scale / p.cap));
+        if (p.cap > 0.f) z = cap_out * tanh_from(z * cap_in);
         else z *= c;
         if (p.map) {
           if (far) {
@@ -205,30 +220,24 @@ __global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
         }
         s[x][e] = z;
       }
-    float f[2];
+    // the running maximum follows only rises by 2^8, as in the tiled kernel
+    float top[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float top = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      top = fmaxf(top, m[r]);
-      const float zero = top == -INFINITY ? 0.f : top;
-      f[r] = ex2(m[r] - zero);
-      m[r] = top;
-      float sum = 0.f;
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          s[x][2 * r + e] = ex2(s[x][2 * r + e] - zero);
-          sum += s[x][2 * r + e];
-        }
-      l[r] = l[r] * f[r] + sum;  // this thread's columns; joined at the end
+      top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
     }
-    // weights go to the product in the cache's type
-    uint32_t pf[4] = {pack2<BF16>(s[0][0], s[0][1]), pack2<BF16>(s[0][2], s[0][3]), pack2<BF16>(s[1][0], s[1][1]),
-                      pack2<BF16>(s[1][2], s[1][3])};
-    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+    auto risen = [&](int r) { return top[r] > m[r] + 8.f || (m[r] == -INFINITY && top[r] > m[r]); };
+    if (__any_sync(0xffffffffu, risen(0) || risen(1))) {
+      float f[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float next = fmaxf(m[r], top[r]);
+        f[r] = next == -INFINITY ? 1.f : ex2(m[r] - next);
+        m[r] = next;
+        l[r] *= f[r];
+      }
 #pragma unroll
       for (int x = 0; x < DP / 8; ++x) {
         o[x][0] *= f[0];
@@ -238,18 +247,36 @@ __global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
       }
     }
 #pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      // f16 weights are kept 2^7 larger, so that small ones stay normal numbers
+      const float zero = (m[r] == -INFINITY ? 0.f : m[r]) - kLift<BF16>;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[x][2 * r + e] = ex2(s[x][2 * r + e] - zero);
+          l[r] += s[x][2 * r + e];  // this thread's columns; joined at the end
+        }
+    }
+    // weights go to the product in the cache's type
+    uint32_t pf[4] = {pack2<BF16>(s[0][0], s[0][1]), pack2<BF16>(s[0][2], s[0][3]), pack2<BF16>(s[1][0], s[1][1]),
+                      pack2<BF16>(s[1][2], s[1][3])};
+#pragma unroll
     for (int st = 0; st < kSteps; ++st) {
       if (st < steps) {
-        const int row = lane & 15, piece = 2 * st + (lane >> 4);
         uint32_t vf[4];
-        ldsm4_t(V + row * (DP * 2) + ((piece ^ (row & 7)) << 4), vf);
+        ldsm4_t(V + (st / 4) * kBox + (v_place ^ ((st % 4) << 5)), vf);
         mma16<BF16>(o[2 * st], pf, vf[0], vf[1]);
         mma16<BF16>(o[2 * st + 1], pf, vf[2], vf[3]);
       }
     }
     __syncwarp();
+    load(n + kStages);
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (!ok && lane == 0) {
+    // copies still in flight land in this block's memory: give them time
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
   // ---- the warps' results
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -258,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
     if ((lane & 3) == 0) stat[0][warp][quad + 8 * r] = m[r], stat[1][warp][quad + 8 * r] = l[r];
   }
   __syncthreads();
-  float* all = (float*)raw;  // [warps][16][DP + 2]
+  float* all = (float*)mem;  // [warps][16][DP + 2]
 #pragma unroll
   for (int x = 0; x < DP / 8; ++x)
 #pragma unroll
@@ -285,7 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32) step(const StepParams t) {
     const float f = total == 0.f ? 0.f : 1.f / total;
     const int at_row = rt * 16 + row, i = at_row / p.group, h = hk * p.group + at_row % p.group;
     const long long stat_row = ((long long)b * p.heads + h) * p.q_len + i;
-    const float lse = total == 0.f ? -INFINITY : top + log2f(total);
+    const float lse = total == 0.f ? -INFINITY : top - kLift<BF16> + log2f(total);
     if (t.splits > 1) {
       const long long at = (long long)split * p.batch * p.heads * p.q_len + stat_row;
       if (d == 0) t.part_lse[at] = lse;
@@ -320,9 +347,9 @@ fm_status launch(const StepParams& t, cudaStream_t st) {
 StepPlan step_plan(const AttnParams& p) {
   StepPlan w{};
   w.row_tiles = (p.q_len * p.group + 15) / 16;
-  // Splits of at least 256 keys, as many as fill the SMs' blocks (two of 96 KB
-  // with head size 128, four of 48 KB with 64) in whole waves.
-  const long long slots = (long long)num_sms() * (p.dim <= 64 ? 4 : 2);
+  // Splits of at least 256 keys, as many as fill the SMs' blocks (three with
+  // head size 128, four with 64: their registers) in whole waves.
+  const long long slots = (long long)num_sms() * (p.dim <= 64 ? 4 : 3);
   const long long blocks = (long long)p.batch * p.kv_heads * w.row_tiles;
   const long long most = p.k_len / 256 > 1 ? p.k_len / 256 : 1;
   long long best = 1;
@@ -345,8 +372,19 @@ StepPlan step_plan(const AttnParams& p) {
 
 fm_status attn_step(const AttnParams& p, int64_t dtype, const StepPlan& w, float* part_o, float* part_lse,
                     cudaStream_t st) {
-  StepParams t{p, w.splits, w.split_keys, w.row_tiles, part_o, part_lse};
+  StepParams t{};
   const bool bf16 = dtype == FM_BF16;
+  t.p = p;
+  t.splits = w.splits;
+  t.split_keys = w.split_keys;
+  t.row_tiles = w.row_tiles;
+  t.part_o = part_o;
+  t.part_lse = part_lse;
+  t.err = ops_error_word();
+  if (t.err == nullptr ||
+      !tc_encode(&t.km, p.k, p.ks, p.batch, p.k_len, p.kv_heads, p.dim, kKeys, bf16, &t.k_mh, &t.k_mb) ||
+      !tc_encode(&t.vm, p.v, p.vs, p.batch, p.k_len, p.kv_heads, p.dim, kKeys, bf16, &t.v_mh, &t.v_mb))
+    return FM_ERR_CUDA;
   return p.dim <= 64 ? (bf16 ? launch<64, true>(t, st) : launch<64, false>(t, st))
                      : (bf16 ? launch<128, true>(t, st) : launch<128, false>(t, st));
 }

@@ -58,22 +58,6 @@ bool rows_ok(const void* base, const Strides& s, int batch, int len, int heads) 
   return ((uintptr_t)base & 15) == 0 && ok(s.t, len, false) && ok(s.h, heads, true) && ok(s.b, batch, true);
 }
 
-bool encode(CUtensorMap* m, const void* base, const Strides& s, int batch, int len, int heads, int dim, int rows,
-            bool bf16, int* mh, int* mb) {
-  *mh = heads > 1 && s.h != 0;
-  *mb = batch > 1 && s.b != 0;
-  const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)len, (cuuint64_t)(*mh ? heads : 1),
-                              (cuuint64_t)(*mb ? batch : 1)};
-  auto bytes = [&](long long stride, bool used) { return (cuuint64_t)(used ? stride * 2 : 16); };
-  const cuuint64_t strides[3] = {bytes(s.t, len > 1), bytes(s.h, *mh), bytes(s.b, *mb)};
-  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
-  return encoder() != nullptr &&
-         encoder()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                   const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Before the tiles' kernels, in one launch: the documents of each tile of 128
 // frames ({lowest, highest, all one id}; padding frames count only against the
 // last), by blocks x < tiles of row y = batch entry; and the bias by offset in
@@ -128,7 +112,7 @@ __global__ void __launch_bounds__(256) join(const AttnParams p, int splits, cons
   float total = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // dim <= 128
   const bool mine = 4 * lane < p.dim;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = warp; s < splits; s += 8) {
     const float lse = part_lse[s * rows + row], w = lse == -INFINITY ? 0.f : exp2f(lse - base);
     total += w;
@@ -182,42 +166,48 @@ __device__ __forceinline__ void block_peak(float v, float* to) {
 // Statistics of the backward pass by query, padded to whole tiles of 64:
 // base-2 lse (+inf where a query sees nothing or is padding: every weight
 // 2^(z - inf) is 0) less `lift`, and delta = dout . out. LANES threads a row, 8
-// elements each; block (x, head, batch entry). peak: the largest squared norm
+// elements each, kStatsParts rows in turn; block (x, head, batch entry). peak: the largest squared norm
 // of a row of dout, by key head.
+constexpr int kStatsParts = 4;
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) bwd_stats(const AttnParams p, int q_pad, float lift, float* lse2, float* delta,
                                                  float* peak) {
-  const int lane = threadIdx.x % LANES, i = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const bool there = i < p.q_len && (p.q_docs == nullptr || p.q_docs[(long long)b * p.q_len + i] >= 0);
-  const long long row = (long long)b * p.heads + h;
-  float s = 0.f, norm = 0.f, l = -INFINITY;
-  if (there) {
-    l = p.lse[row * p.q_len + i];
-    if (lane * 8 < p.dim) {
-      const Pack<T, 8> g = *(const Pack<T, 8>*)((const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h + lane * 8);
-      const long long at = b * p.os.b + i * p.os.t + h * p.os.h + lane * 8;
-      const Pack<T, 8> o = *(const Pack<T, 8>*)((const T*)p.out_in + at);
-      Pack<T, 8> rest{};
-      if (p.rest) rest = *(const Pack<T, 8>*)((const T*)p.rest + at);
+  const int lane = threadIdx.x % LANES, h = blockIdx.y, b = blockIdx.z;
+  float top = 0.f;
+#pragma unroll 2
+  for (int part = 0; part < kStatsParts; ++part) {
+    const int i = (blockIdx.x * kStatsParts + part) * (256 / LANES) + threadIdx.x / LANES;
+    const bool there = i < p.q_len && (p.q_docs == nullptr || p.q_docs[(long long)b * p.q_len + i] >= 0);
+    const long long row = (long long)b * p.heads + h;
+    float s = 0.f, norm = 0.f, l = -INFINITY;
+    if (there) {
+      l = p.lse[row * p.q_len + i];
+      if (lane * 8 < p.dim) {
+        const Pack<T, 8> g = *(const Pack<T, 8>*)((const T*)p.dout + b * p.dos.b + i * p.dos.t + h * p.dos.h + lane * 8);
+        const long long at = b * p.os.b + i * p.os.t + h * p.os.h + lane * 8;
+        const Pack<T, 8> o = *(const Pack<T, 8>*)((const T*)p.out_in + at);
+        Pack<T, 8> rest{};
+        if (p.rest) rest = *(const Pack<T, 8>*)((const T*)p.rest + at);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float d = to_f(g.v[k]);
-        s = fmaf(d, to_f(o.v[k]) + to_f(rest.v[k]), s);
-        norm = fmaf(d, d, norm);
+        for (int k = 0; k < 8; ++k) {
+          const float d = to_f(g.v[k]);
+          s = fmaf(d, to_f(o.v[k]) + to_f(rest.v[k]), s);
+          norm = fmaf(d, d, norm);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o, LANES);
-    norm += __shfl_xor_sync(0xffffffffu, norm, o, LANES);
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o, LANES);
+      norm += __shfl_xor_sync(0xffffffffu, norm, o, LANES);
+    }
+    top = fmaxf(top, norm);
+    if (lane == 0 && i < q_pad) {
+      lse2[row * q_pad + i] = l == -INFINITY ? INFINITY : l * kLog2e - lift;
+      delta[row * q_pad + i] = s;
+    }
   }
-  if (peak) block_peak(norm, peak + b * p.kv_heads + h / p.group);
-  if (lane == 0 && i < q_pad) {
-    lse2[row * q_pad + i] = l == -INFINITY ? INFINITY : l * kLog2e - lift;
-    delta[row * q_pad + i] = s;
-  }
+  if (peak) block_peak(top, peak + b * p.kv_heads + h / p.group);
 }
 
 // The largest squared norm of a row of v that counts, by batch entry and key
@@ -252,6 +242,28 @@ int mode_of(const AttnParams& p) {
 }
 int64_t align256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 }  // namespace
+
+// The tensor [batch][len][heads][dim] to TMA as {dim, len, heads, batch}, boxes of
+// 64 x rows. The encoder is a driver call: it needs the device's context on
+// this thread, which a thread that only took cached memory so far does not
+// have.
+bool tc_encode(CUtensorMap* m, const void* base, const Strides& s, int batch, int len, int heads, int dim, int rows,
+               bool bf16, int* mh, int* mb) {
+  *mh = heads > 1 && s.h != 0;
+  *mb = batch > 1 && s.b != 0;
+  const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)len, (cuuint64_t)(*mh ? heads : 1),
+                              (cuuint64_t)(*mb ? batch : 1)};
+  auto bytes = [&](long long stride, bool used) { return (cuuint64_t)(used ? stride * 2 : 16); };
+  const cuuint64_t strides[3] = {bytes(s.t, len > 1), bytes(s.h, *mh), bytes(s.b, *mb)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, step[4] = {1, 1, 1, 1};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+  return encoder() != nullptr &&
+         encoder()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool tc_layout_ok(const AttnParams& p, int64_t dtype, bool backward) {
   if (dtype == FM_F32 || p.dim > 128 || p.dim % 8 || p.k_len == 0 || encoder() == nullptr) return false;
@@ -308,10 +320,6 @@ TcPlan tc_plan(const AttnParams& p, bool backward) {
 fm_status tc_setup(TcParams& t, const AttnParams& p, int64_t dtype, const TcPlan& w, char* ws, int q_rows, int k_rows,
                    cudaStream_t st) {
   const bool bf16 = dtype == FM_BF16;
-  // the encoder is a driver call: it needs the device's context on this
-  // thread, which a thread that only took cached memory so far does not have
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return FM_ERR_CUDA;
   t.p = p;
   t.err = ops_error_word();
   if (t.err == nullptr) return FM_ERR_CUDA;
@@ -320,11 +328,11 @@ fm_status tc_setup(TcParams& t, const AttnParams& p, int64_t dtype, const TcPlan
   t.dim16 = (p.dim + 15) / 16 * 16;
   t.splits = w.splits;
   t.split_tiles = w.split_tiles;
-  if (!encode(&t.qm, p.q, p.qs, p.batch, p.q_len, p.heads, p.dim, q_rows, bf16, &t.q_mh, &t.q_mb) ||
-      !encode(&t.km, p.k, p.ks, p.batch, p.k_len, p.kv_heads, p.dim, k_rows, bf16, &t.k_mh, &t.k_mb) ||
-      !encode(&t.vm, p.v, p.vs, p.batch, p.k_len, p.kv_heads, p.dim, k_rows, bf16, &t.v_mh, &t.v_mb))
+  if (!tc_encode(&t.qm, p.q, p.qs, p.batch, p.q_len, p.heads, p.dim, q_rows, bf16, &t.q_mh, &t.q_mb) ||
+      !tc_encode(&t.km, p.k, p.ks, p.batch, p.k_len, p.kv_heads, p.dim, k_rows, bf16, &t.k_mh, &t.k_mb) ||
+      !tc_encode(&t.vm, p.v, p.vs, p.batch, p.k_len, p.kv_heads, p.dim, k_rows, bf16, &t.v_mh, &t.v_mb))
     return FM_ERR_CUDA;
-  if (p.dout && !encode(&t.gm, p.dout, p.dos, p.batch, p.q_len, p.heads, p.dim, q_rows, bf16, &t.g_mh, &t.g_mb))
+  if (p.dout && !tc_encode(&t.gm, p.dout, p.dos, p.batch, p.q_len, p.heads, p.dim, q_rows, bf16, &t.g_mh, &t.g_mb))
     return FM_ERR_CUDA;
   if (p.q_docs || p.map) {
     int4* r = p.q_docs ? (int4*)(ws + w.ranges) : nullptr;
@@ -376,7 +384,7 @@ fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cu
   x.lse2 = lse2;
   x.delta = lse2 + rows;
   const bool narrow = p.dim <= 64;
-  const int per_block = narrow ? 32 : 16;
+  const int per_block = kStatsParts * (narrow ? 32 : 16);
   const dim3 grid((x.q_pad + per_block - 1) / per_block, p.heads, p.batch);
   float* peak = nullptr;
   const int count = p.batch * p.kv_heads;

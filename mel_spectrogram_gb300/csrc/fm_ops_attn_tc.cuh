@@ -43,6 +43,8 @@ unsigned* ops_error_word();
 struct StepPlan {
   int splits, split_keys, row_tiles;
 };
+bool tc_encode(CUtensorMap* m, const void* base, const Strides& s, int batch, int len, int heads, int dim, int rows,
+               bool bf16, int* mh, int* mb);
 StepPlan step_plan(const AttnParams& p);
 fm_status attn_step(const AttnParams& p, int64_t dtype, const StepPlan& w, float* part_o, float* part_lse,
                     cudaStream_t st);
