@@ -70,7 +70,8 @@ int64_t part_bytes(const fm_attention_args* a, int q_tiles) {
 }
 Workspace any_layout(const fm_attention_args* a) {
   Workspace w{};
-  w.q_tiles = (int)((a->q_len + kAnyTile - 1) / kAnyTile);
+  const int rows = any_rows(params(a));
+  w.q_tiles = (int)((a->q_len + rows - 1) / rows);
   w.part = align256(sizeof(float) * a->batch * a->heads * a->q_len);
   w.total = w.part + part_bytes(a, w.q_tiles) + 256;
   return w;

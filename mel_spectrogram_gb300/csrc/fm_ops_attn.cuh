@@ -52,6 +52,6 @@ __device__ __forceinline__ float table_value(const AttnParams& p, long long at, 
 // kernels for any type, head size and stride (fm_ops_attn_any.cu)
 fm_status attn_any_forward(const AttnParams& p, int64_t dtype, cudaStream_t st);
 fm_status attn_any_backward(const AttnParams& p, int64_t dtype, cudaStream_t st);
-constexpr int kAnyTile = 64;  // queries per row of AttnParams::part
+int any_rows(const AttnParams& p);  // queries a block takes, and per row of AttnParams::part
 
 }  // namespace fm

@@ -13,8 +13,7 @@
 namespace fm {
 namespace {
 
-constexpr int kRows = kAnyTile;  // rows a block owns
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // 16 x 16: a thread has R rows and columns 16 apart
 
 // Floats between rows of a staged tile: padded to whole float4, an odd number
 // of them, so that float4 reads down a column of rows hit distinct banks.
@@ -107,23 +106,23 @@ __device__ __forceinline__ float half_sum(float x) {
   return x;
 }
 
-// s[r][c] = A row (ty*4 + r) . B row (tx + 16 c)
-template <int C>
+// s[r][c] = A row (ty*R + r) . B row (tx + 16 c)
+template <int R, int C>
 __device__ __forceinline__ void products(const float* A, const float* B, int dim, int pitch, int tx, int ty,
-                                         float (&s)[4][C]) {
+                                         float (&s)[R][C]) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int c = 0; c < C; ++c) s[r][c] = 0.f;
   const int d4 = (dim + 3) / 4;
   for (int d = 0; d < d4; ++d) {
-    float4 a[4], b[C];
+    float4 a[R], b[C];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) a[r] = *(const float4*)(A + (ty * 4 + r) * pitch + 4 * d);
+    for (int r = 0; r < R; ++r) a[r] = *(const float4*)(A + (ty * R + r) * pitch + 4 * d);
 #pragma unroll
     for (int c = 0; c < C; ++c) b[c] = *(const float4*)(B + (tx + 16 * c) * pitch + 4 * d);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         s[r][c] = fmaf(a[r].x, b[c].x, s[r][c]);
@@ -134,21 +133,21 @@ __device__ __forceinline__ void products(const float* A, const float* B, int dim
   }
 }
 
-// acc[r][g] += sum_j W[(ty*4 + r)][j] * V[j][4 tx + 64 g ..]
-template <int G>
-__device__ __forceinline__ void accumulate(float4 (&acc)[4][G], const float* W, int wpitch, const float* V, int n,
+// acc[r][g] += sum_j W[(ty*R + r)][j] * V[j][4 tx + 64 g ..]
+template <int R, int G>
+__device__ __forceinline__ void accumulate(float4 (&acc)[R][G], const float* W, int wpitch, const float* V, int n,
                                            int dim, int pitch, int tx, int ty) {
   for (int j = 0; j < n; ++j) {
-    float w[4];
+    float w[R];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) w[r] = W[(ty * 4 + r) * wpitch + j];
+    for (int r = 0; r < R; ++r) w[r] = W[(ty * R + r) * wpitch + j];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int d = 4 * tx + 64 * g;
       if (d >= dim) continue;
       const float4 v = *(const float4*)(V + j * pitch + d);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < R; ++r) {
         acc[r][g].x = fmaf(w[r], v.x, acc[r][g].x);
         acc[r][g].y = fmaf(w[r], v.y, acc[r][g].y);
         acc[r][g].z = fmaf(w[r], v.z, acc[r][g].z);
@@ -157,19 +156,19 @@ __device__ __forceinline__ void accumulate(float4 (&acc)[4][G], const float* W, 
     }
   }
 }
-template <int G>
-__device__ __forceinline__ void clear(float4 (&acc)[4][G]) {
+template <int R, int G>
+__device__ __forceinline__ void clear(float4 (&acc)[R][G]) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int g = 0; g < G; ++g) acc[r][g] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
-template <typename T, int G>
-__device__ __forceinline__ void put(T* to, long long stride, int n, int dim, const float4 (&acc)[4][G],
-                                    const float (&f)[4], int tx, int ty, T* rest = nullptr) {
+template <typename T, int R, int G>
+__device__ __forceinline__ void put(T* to, long long stride, int n, int dim, const float4 (&acc)[R][G],
+                                    const float (&f)[R], int tx, int ty, T* rest = nullptr) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = ty * 4 + r;
+  for (int r = 0; r < R; ++r) {
+    const int row = ty * R + r;
     if (row >= n) continue;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -188,9 +187,10 @@ __device__ __forceinline__ void put(T* to, long long stride, int n, int dim, con
 
 constexpr int kFwdKeys = 64;
 
-template <typename T, int G>
+template <typename T, int G, int R>
 __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
   extern __shared__ float sm[];
+  constexpr int kRows = 16 * R;
   const int pitch = pitch_of(p.dim);
   float *Q = sm, *K = Q + kRows * pitch, *V = K + kFwdKeys * pitch, *P = V + kFwdKeys * pitch;
   constexpr int wp = kFwdKeys + 4;
@@ -202,11 +202,11 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
   const T* v = (const T*)p.v + b * p.vs.b + hk * p.vs.h;
   const int nq = min(kRows, p.q_len - i0);
   stage<T, G, kRows>(Q, q, p.qs.t, nq, p.dim, pitch, score.qd ? score.qd + i0 : nullptr);
-  float4 acc[4][G];
+  float4 acc[R][G];
   clear(acc);
-  float m[4], l[4];
+  float m[R], l[R];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.f;
+  for (int r = 0; r < R; ++r) m[r] = -INFINITY, l[r] = 0.f;
   int end = score.r.len;
   if (p.causal) end = min(end, max(score.r.start + i0 + nq, score.r.prefix));
   for (int j0 = 0; j0 < end; j0 += kFwdKeys) {
@@ -215,14 +215,14 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
     stage<T, G, kFwdKeys>(K, k + j0 * p.ks.t, p.ks.t, n, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
     stage<T, G, kFwdKeys>(V, v + j0 * p.vs.t, p.vs.t, n, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
     __syncthreads();
-    float s[4][4];
-    products<4>(Q, K, p.dim, pitch, tx, ty, s);
+    float s[R][4];
+    products<R, 4>(Q, K, p.dim, pitch, tx, ty, s);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
       float top = m[r];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        s[r][c] = score(s[r][c], i0 + ty * 4 + r, j0 + tx + 16 * c).z;
+        s[r][c] = score(s[r][c], i0 + ty * R + r, j0 + tx + 16 * c).z;
         top = fmaxf(top, s[r][c]);
       }
       top = half_max(top);
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
       for (int c = 0; c < 4; ++c) {
         const float e = expf(s[r][c] - base);
         sum += e;
-        P[(ty * 4 + r) * wp + tx + 16 * c] = e;
+        P[(ty * R + r) * wp + tx + 16 * c] = e;
       }
       l[r] = l[r] * f + half_sum(sum);
       m[r] = top;
@@ -241,13 +241,13 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
       for (int g = 0; g < G; ++g) acc[r][g].x *= f, acc[r][g].y *= f, acc[r][g].z *= f, acc[r][g].w *= f;
     }
     __syncwarp();  // a row's weights come from the 16 lanes of its half warp
-    accumulate<G>(acc, P, wp, V, n, p.dim, pitch, tx, ty);
+    accumulate<R, G>(acc, P, wp, V, n, p.dim, pitch, tx, ty);
   }
-  float f[4];
+  float f[R];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < R; ++r) {
     f[r] = l[r] == 0.f ? 0.f : 1.f / l[r];
-    const int i = i0 + ty * 4 + r;
+    const int i = i0 + ty * R + r;
     if (p.lse && tx == 0 && i < p.q_len)
       p.lse[((long long)b * p.heads + h) * p.q_len + i] = l[r] == 0.f ? -INFINITY : m[r] + logf(l[r]);
   }
@@ -259,9 +259,10 @@ constexpr int kBwdCols = 32;  // rows of the streamed tile
 
 // OF_KEYS: the block owns keys and streams queries (dk, dv); otherwise it
 // owns queries and streams keys (dq and the bias).
-template <typename T, int G, bool OF_KEYS>
+template <typename T, int G, int R, bool OF_KEYS>
 __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
   extern __shared__ float sm[];
+  constexpr int kRows = 16 * R;
   const int pitch = pitch_of(p.dim);
   float *R1 = sm, *R2 = R1 + kRows * pitch;              // owned: (K, V) or (Q, dout)
   float *C1 = R2 + kRows * pitch, *C2 = C1 + kBwdCols * pitch;  // streamed: (Q, dout) or (K, V)
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
     stage<T, G, kRows>(R1, k + r0 * p.ks.t, p.ks.t, n, p.dim, pitch, kd ? kd + r0 : nullptr);
     stage<T, G, kRows>(R2, v + r0 * p.vs.t, p.vs.t, n, p.dim, pitch, kd ? kd + r0 : nullptr);
   }
-  float4 a1[4][G], a2[4][G];
+  float4 a1[R][G], a2[R][G];
   clear(a1);
   clear(a2);
   float* part = nullptr;
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
     }
     int begin = 0, end = OF_KEYS ? p.q_len : info.len;
     if (p.causal && !OF_KEYS) end = min(end, max(info.start + r0 + owned, info.prefix));
+    if (OF_KEYS && p.causal && r0 >= info.prefix) begin = max(0, r0 - info.start) / kBwdCols * kBwdCols;
     if (OF_KEYS && r0 >= info.len) end = 0;
     for (int c0 = begin; c0 < end; c0 += kBwdCols) {
       const int n = min(kBwdCols, end - c0);
@@ -315,15 +317,15 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
         stage<T, G, kBwdCols>(C2, v + c0 * p.vs.t, p.vs.t, n, p.dim, pitch, kd ? kd + c0 : nullptr);
       }
       __syncthreads();
-      float s[4][2], dp[4][2];
-      products<2>(R1, C1, p.dim, pitch, tx, ty, s);
-      products<2>(R2, C2, p.dim, pitch, tx, ty, dp);
-      float bias_grad[4][2];
+      float s[R][2], dp[R][2];
+      products<R, 2>(R1, C1, p.dim, pitch, tx, ty, s);
+      products<R, 2>(R2, C2, p.dim, pitch, tx, ty, dp);
+      float bias_grad[R][2];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int row = r0 + ty * 4 + r, col = c0 + tx + 16 * c;
+          const int row = r0 + ty * R + r, col = c0 + tx + 16 * c;
           const int i = OF_KEYS ? col : row, j = OF_KEYS ? row : col;
           const Score z = score(s[r][c], i, j);
           float w = 0.f, d = 0.f;
@@ -332,18 +334,18 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
             d = w * (dp[r][c] - delta[i]);
           }
           bias_grad[r][c] = d;
-          W1[(ty * 4 + r) * wp + tx + 16 * c] = w;
-          W2[(ty * 4 + r) * wp + tx + 16 * c] = d * z.slope;
+          W1[(ty * R + r) * wp + tx + 16 * c] = w;
+          W2[(ty * R + r) * wp + tx + 16 * c] = d * z.slope;
         }
       __syncwarp();
-      if (OF_KEYS) accumulate<G>(a1, W1, wp, C2, n, p.dim, pitch, tx, ty);  // dv
-      accumulate<G>(a2, W2, wp, C1, n, p.dim, pitch, tx, ty);               // dk or dq
+      if (OF_KEYS) accumulate<R, G>(a1, W1, wp, C2, n, p.dim, pitch, tx, ty);  // dv
+      accumulate<R, G>(a2, W2, wp, C1, n, p.dim, pitch, tx, ty);               // dk or dq
       if (part) {
         // the tile's diagonals, one thread each; the clamped ends one each
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) W1[(ty * 4 + r) * wp + tx + 16 * c] = bias_grad[r][c];
+          for (int c = 0; c < 2; ++c) W1[(ty * R + r) * wp + tx + 16 * c] = bias_grad[r][c];
         __syncthreads();
         constexpr int kDiag = kRows + kBwdCols - 1;
         const int base = c0 - (info.start + r0) - (kRows - 1);  // offset of diagonal 0
@@ -369,7 +371,9 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
       }
     }
   }
-  const float one[4] = {1.f, 1.f, 1.f, 1.f}, sc[4] = {p.scale, p.scale, p.scale, p.scale};
+  float one[R], sc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) one[r] = 1.f, sc[r] = p.scale;
   if (OF_KEYS) {
     put((T*)p.dv + b * p.dvs.b + r0 * p.dvs.t + hk * p.dvs.h, p.dvs.t, owned, p.dim, a1, one, tx, ty);
     put((T*)p.dk + b * p.dks.b + r0 * p.dks.t + hk * p.dks.h, p.dks.t, owned, p.dim, a2, sc, tx, ty);
@@ -397,50 +401,65 @@ __global__ void __launch_bounds__(256) any_delta(const AttnParams p) {
   if ((threadIdx.x & 31) == 0) p.delta[row] = s;
 }
 
-size_t fwd_smem(int dim) {
-  return sizeof(float) * ((size_t)(kRows + 2 * kFwdKeys) * pitch_of(dim) + kRows * (kFwdKeys + 4));
+size_t fwd_smem(int dim, int rows) {
+  return sizeof(float) * ((size_t)(rows + 2 * kFwdKeys) * pitch_of(dim) + rows * (kFwdKeys + 4));
 }
-size_t bwd_smem(int dim) {
-  return sizeof(float) * ((size_t)(2 * kRows + 2 * kBwdCols) * pitch_of(dim) + 2 * kRows * (kBwdCols + 4));
+size_t bwd_smem(int dim, int rows) {
+  return sizeof(float) * ((size_t)(2 * rows + 2 * kBwdCols) * pitch_of(dim) + 2 * rows * (kBwdCols + 4));
 }
 
-template <typename T, int G>
+template <typename T, int G, int R>
 fm_status fwd(const AttnParams& p, cudaStream_t st) {
-  const dim3 grid((p.q_len + kRows - 1) / kRows, p.heads, p.batch);
-  const size_t smem = fwd_smem(p.dim);
-  if (!allow_smem(any_fwd<T, G>, smem)) return FM_ERR_CUDA;
-  any_fwd<T, G><<<grid, kThreads, smem, st>>>(p);
+  const dim3 grid((p.q_len + 16 * R - 1) / (16 * R), p.heads, p.batch);
+  const size_t smem = fwd_smem(p.dim, 16 * R);
+  if (!allow_smem(any_fwd<T, G, R>, smem)) return FM_ERR_CUDA;
+  any_fwd<T, G, R><<<grid, kThreads, smem, st>>>(p);
   return launch_status();
 }
-template <typename T, int G>
+template <typename T, int G, int R>
 fm_status bwd(const AttnParams& p, cudaStream_t st) {
-  const size_t smem = bwd_smem(p.dim);
-  if (!allow_smem(any_bwd<T, G, true>, smem) || !allow_smem(any_bwd<T, G, false>, smem)) return FM_ERR_CUDA;
+  const int tile = 16 * R;
+  const size_t smem = bwd_smem(p.dim, tile);
+  if (!allow_smem(any_bwd<T, G, R, true>, smem) || !allow_smem(any_bwd<T, G, R, false>, smem)) return FM_ERR_CUDA;
   if (p.q_len > 0) {
     const long long rows = (long long)p.batch * p.heads * p.q_len;
     any_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
-    any_bwd<T, G, false><<<dim3((p.q_len + kRows - 1) / kRows, p.heads, p.batch), kThreads, smem, st>>>(p);
+    any_bwd<T, G, R, false><<<dim3((p.q_len + tile - 1) / tile, p.heads, p.batch), kThreads, smem, st>>>(p);
   }
   if (p.k_len > 0)
-    any_bwd<T, G, true><<<dim3((p.k_len + kRows - 1) / kRows, p.kv_heads, p.batch), kThreads, smem, st>>>(p);
+    any_bwd<T, G, R, true><<<dim3((p.k_len + tile - 1) / tile, p.kv_heads, p.batch), kThreads, smem, st>>>(p);
   return launch_status();
 }
-template <typename T>
+template <typename T, int R>
 fm_status fwd_g(const AttnParams& p, cudaStream_t st) {
-  return p.dim <= 64 ? fwd<T, 1>(p, st) : p.dim <= 128 ? fwd<T, 2>(p, st) : fwd<T, 4>(p, st);
+  return p.dim <= 64 ? fwd<T, 1, R>(p, st) : p.dim <= 128 ? fwd<T, 2, R>(p, st) : fwd<T, 4, R>(p, st);
 }
-template <typename T>
+template <typename T, int R>
 fm_status bwd_g(const AttnParams& p, cudaStream_t st) {
-  return p.dim <= 64 ? bwd<T, 1>(p, st) : p.dim <= 128 ? bwd<T, 2>(p, st) : bwd<T, 4>(p, st);
+  return p.dim <= 64 ? bwd<T, 1, R>(p, st) : p.dim <= 128 ? bwd<T, 2, R>(p, st) : bwd<T, 4, R>(p, st);
 }
 }  // namespace
 
+int any_rows(const AttnParams& p) {
+  // 64 rows a block make four times the products of an operand read; 32 make
+  // twice the blocks, for problems that would leave SMs without one
+  const long long blocks = (long long)((p.q_len + 63) / 64) * p.heads * p.batch;
+  return blocks < num_sms() ? 32 : 64;
+}
+template <typename T>
+static fm_status any_forward(const AttnParams& p, cudaStream_t st) {
+  return any_rows(p) == 32 ? fwd_g<T, 2>(p, st) : fwd_g<T, 4>(p, st);
+}
+template <typename T>
+static fm_status any_backward(const AttnParams& p, cudaStream_t st) {
+  return any_rows(p) == 32 ? bwd_g<T, 2>(p, st) : bwd_g<T, 4>(p, st);
+}
 fm_status attn_any_forward(const AttnParams& p, int64_t dtype, cudaStream_t st) {
-  return dtype == FM_F32 ? fwd_g<float>(p, st)
-                         : dtype == FM_F16 ? fwd_g<__half>(p, st) : fwd_g<__nv_bfloat16>(p, st);
+  return dtype == FM_F32 ? any_forward<float>(p, st)
+                         : dtype == FM_F16 ? any_forward<__half>(p, st) : any_forward<__nv_bfloat16>(p, st);
 }
 fm_status attn_any_backward(const AttnParams& p, int64_t dtype, cudaStream_t st) {
-  return dtype == FM_F32 ? bwd_g<float>(p, st)
-                         : dtype == FM_F16 ? bwd_g<__half>(p, st) : bwd_g<__nv_bfloat16>(p, st);
+  return dtype == FM_F32 ? any_backward<float>(p, st)
+                         : dtype == FM_F16 ? any_backward<__half>(p, st) : any_backward<__nv_bfloat16>(p, st);
 }
 }  // namespace fm

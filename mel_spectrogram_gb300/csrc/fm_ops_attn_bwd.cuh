@@ -170,6 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_slot;
+  // The keys' kernel needs nothing of the queries' one: its blocks may start on
+  // SMs that have no more blocks of this one.
+  if (!KEYS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the streamed tiles [sb, se), in steps of 64, of each head
   int sb = 0, se;
@@ -596,6 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     fence_after();
     tmem_free(tmem, 512);
   }
+  // what follows in the stream waits for this kernel: one block of it waits
+  // for the queries' kernel
+  if (KEYS && blockIdx.x + blockIdx.y + blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int DP, bool BF16, bool KEYS>
@@ -608,8 +614,17 @@ fm_status launch(const TcParams& t, Extra x, int mode, cudaStream_t st) {
   if (x.slots < 3) return FM_ERR_UNSUPPORTED;
   auto k = mode == 0 ? kernel<DP, BF16, 0, KEYS> : mode == 1 ? kernel<DP, BF16, 1, KEYS> : kernel<DP, BF16, 2, KEYS>;
   if (!allow_smem(k, smem)) return FM_ERR_CUDA;
-  k<<<grid, kThreads, smem, st>>>(t, x);
-  return launch_status();
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = smem;
+  config.stream = st;
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &early;
+  config.numAttrs = KEYS ? 1 : 0;  // launched right after the queries' kernel
+  return cudaLaunchKernelEx(&config, k, t, (const Extra)x) == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 }  // namespace bwd
