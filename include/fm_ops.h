@@ -125,8 +125,10 @@ int64_t fm_relative_bias_workspace(const fm_relative_bias_args* args);
  * keys that nothing sees get zero gradients. Keys at or past k_lens[b], and
  * frames whose document id is negative, are never used: their memory may hold
  * anything, infinities and NaN included.
- * A key that one query may see and another may not is left out of the
- * latter's softmax whatever its score is (NaN too); its v has to be finite.
+ * A key that one query may see and another may not changes nothing of the
+ * latter, whatever its k and v hold (in the backward pass, whatever the
+ * query's q and dout hold). Near a mask's border a query that does see a key
+ * whose v is not finite returns NaN in all of its elements.
  *
  *   batch, q_len, k_len, heads, kv_heads, dim : heads a multiple of kv_heads
  *            (query head h reads key head h / (heads / kv_heads)); dim 1 .. 256.

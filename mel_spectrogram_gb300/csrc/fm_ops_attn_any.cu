@@ -25,9 +25,14 @@ __host__ __device__ inline int pitch_of(int dim) {
 // Stages ROWS rows of up to 64 G elements: 16 threads a row, and every thread
 // has all its loads of 16 rows under way before it writes the first (one load
 // at a time, each waiting for the last, took most of a small problem's time).
+//
+// bad: where not every query sees the same keys, a row that is not finite must
+// not reach the rows that do not see it, but a weight of 0 times it would; such
+// elements are staged as zeros and their row is marked, and a weight for it
+// becomes NaN. NULL: no matter.
 template <typename T, int G, int ROWS>
 __device__ __forceinline__ void stage(float* to, const T* from, long long stride, int n, int dim, int pitch,
-                                      const int32_t* docs) {
+                                      const int32_t* docs, int* bad = nullptr) {
   // rows at or past n, and padding frames, arrive as zeros whatever memory holds
   const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
 #pragma unroll
@@ -38,6 +43,16 @@ __device__ __forceinline__ void stage(float* to, const T* from, long long stride
     float v[4 * G];
 #pragma unroll
     for (int k = 0; k < 4 * G; ++k) v[k] = real && lane + 16 * k < dim ? to_f(row[lane + 16 * k]) : 0.f;
+    if (bad) {
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < 4 * G; ++k) {
+        const bool wrong = !(fabsf(v[k]) <= 3.402823466e38f);
+        v[k] = wrong ? 0.f : v[k];
+        any |= wrong;
+      }
+      if (any) bad[r] = 1;
+    }
 #pragma unroll
     for (int k = 0; k < 4 * G; ++k)
       if (lane + 16 * k < pitch) to[r * pitch + lane + 16 * k] = v[k];
@@ -196,6 +211,8 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
   constexpr int wp = kFwdKeys + 4;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int i0 = blockIdx.x * kRows, h = blockIdx.y, b = blockIdx.z, hk = h / p.group;
+  __shared__ int bad_rows[kFwdKeys];
+  int* bad = p.causal || p.k_docs ? bad_rows : nullptr;
   const ScoreOf<T> score(p, b, h);
   const T* q = (const T*)p.q + b * p.qs.b + i0 * p.qs.t + h * p.qs.h;
   const T* k = (const T*)p.k + b * p.ks.b + hk * p.ks.h;
@@ -212,8 +229,13 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
   for (int j0 = 0; j0 < end; j0 += kFwdKeys) {
     const int n = min(kFwdKeys, score.r.len - j0);
     __syncthreads();
+    if (bad) {
+      if (threadIdx.x < kFwdKeys) bad[threadIdx.x] = 0;
+      __syncthreads();
+    }
     stage<T, G, kFwdKeys>(K, k + j0 * p.ks.t, p.ks.t, n, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
-    stage<T, G, kFwdKeys>(V, v + j0 * p.vs.t, p.vs.t, n, p.dim, pitch, score.kd ? score.kd + j0 : nullptr);
+    stage<T, G, kFwdKeys>(V, v + j0 * p.vs.t, p.vs.t, n, p.dim, pitch, score.kd ? score.kd + j0 : nullptr,
+                          bad);
     __syncthreads();
     float s[R][4];
     products<R, 4>(Q, K, p.dim, pitch, tx, ty, s);
@@ -222,7 +244,8 @@ __global__ void __launch_bounds__(kThreads) any_fwd(const AttnParams p) {
       float top = m[r];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        s[r][c] = score(s[r][c], i0 + ty * R + r, j0 + tx + 16 * c).z;
+        const Score z = score(s[r][c], i0 + ty * R + r, j0 + tx + 16 * c);
+        s[r][c] = z.seen && bad && bad[tx + 16 * c] ? NAN : z.z;
         top = fmaxf(top, s[r][c]);
       }
       top = half_max(top);
@@ -274,6 +297,8 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
   const int h0 = OF_KEYS ? hk * p.group : blockIdx.y, h1 = OF_KEYS ? h0 + p.group : h0 + 1;
   const T* k = (const T*)p.k + b * p.ks.b + hk * p.ks.h;
   const T* v = (const T*)p.v + b * p.vs.b + hk * p.vs.h;
+  __shared__ int bad_rows[kBwdCols];
+  int* bad = p.causal || p.k_docs ? bad_rows : nullptr;
   const RowInfo info = row_info(p, b);
   const int32_t* kd = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
   const int32_t* qd = p.q_docs ? p.q_docs + (long long)b * p.q_len : nullptr;
@@ -309,11 +334,15 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
     for (int c0 = begin; c0 < end; c0 += kBwdCols) {
       const int n = min(kBwdCols, end - c0);
       __syncthreads();
+      if (bad) {
+        if (threadIdx.x < kBwdCols) bad[threadIdx.x] = 0;
+        __syncthreads();
+      }
       if (OF_KEYS) {
-        stage<T, G, kBwdCols>(C1, q + c0 * p.qs.t, p.qs.t, n, p.dim, pitch, qd ? qd + c0 : nullptr);
-        stage<T, G, kBwdCols>(C2, g + c0 * p.dos.t, p.dos.t, n, p.dim, pitch, qd ? qd + c0 : nullptr);
+        stage<T, G, kBwdCols>(C1, q + c0 * p.qs.t, p.qs.t, n, p.dim, pitch, qd ? qd + c0 : nullptr, bad);
+        stage<T, G, kBwdCols>(C2, g + c0 * p.dos.t, p.dos.t, n, p.dim, pitch, qd ? qd + c0 : nullptr, bad);
       } else {
-        stage<T, G, kBwdCols>(C1, k + c0 * p.ks.t, p.ks.t, n, p.dim, pitch, kd ? kd + c0 : nullptr);
+        stage<T, G, kBwdCols>(C1, k + c0 * p.ks.t, p.ks.t, n, p.dim, pitch, kd ? kd + c0 : nullptr, bad);
         stage<T, G, kBwdCols>(C2, v + c0 * p.vs.t, p.vs.t, n, p.dim, pitch, kd ? kd + c0 : nullptr);
       }
       __syncthreads();
@@ -330,7 +359,7 @@ __global__ void __launch_bounds__(kThreads) any_bwd(const AttnParams p) {
           const Score z = score(s[r][c], i, j);
           float w = 0.f, d = 0.f;
           if (z.seen) {
-            w = expf(z.z - lse[i]);
+            w = bad && bad[tx + 16 * c] ? NAN : expf(z.z - lse[i]);
             d = w * (dp[r][c] - delta[i]);
           }
           bias_grad[r][c] = d;

@@ -78,7 +78,7 @@ struct Smem {
     return 1024 + kRing + (size_t)slots(max_distance, bias, grad) * kSlot + tail(max_distance, bias, grad);
   }
 };
-enum { kFull = 0, kEmpty = 8, kOwnFull = 16, kSFull = 17, kPReady = 20, kDone = 23 };
+enum { kFull = 0, kEmpty = 8, kOwnFull = 16, kSFull = 17, kPReady = 20, kDone = 23, kScanned = 24, kBarCount = 26 };
 // Buffers of 128 columns for a streamed tile's scores and dP, taken in turn:
 // with three, a tile's scores are there before the group that will take it has
 // finished its last one. Beside dk and dv of 128 columns only two fit.
@@ -117,14 +117,16 @@ __device__ __forceinline__ float ds_scale(const Extra& x, int at, int count) {
   return fabsf(e) < 120.f ? exp2f(e) : 1.f;  // nothing, infinite or NaN: as it is
 }
 
-template <int DP, bool BF16, int MODE, bool KEYS>
-__global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t,
-                                                      const __grid_constant__ Extra x) {
+// One block's work; SCAN: of the second launch (TcParams::flags).
+template <int DP, bool BF16, int MODE, bool KEYS, bool SCAN>
+__device__ __forceinline__ void block(const TcParams& t, const Extra& x, const dim3 at, const int index) {
   using L = Smem<DP, KEYS>;
   extern __shared__ unsigned char raw[];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int dead;
   __shared__ int range[2];
+  __shared__ int tainted;                            // a result is not finite
+  __shared__ uint32_t bad_rows[SCAN ? 2 : 1][2][8];  // [parity][group][warp]: streamed rows that are not finite
   const AttnParams& p = t.p;
   const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
   unsigned char* mem = raw + (base - smem_u32(raw));
@@ -141,10 +143,10 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   float* chain_mem = diag_mem + 2 * ndiag;  // [group][quarter of the rows][kChains][kChainEntries]
   float* far_mem = chain_mem;  // [2][512], after the last chain
 
-  const int b = blockIdx.z;
-  const int r0 = (!KEYS && p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * kTile;
-  const int hk = KEYS ? blockIdx.y : blockIdx.y / p.group;
-  const int h0 = KEYS ? hk * p.group : blockIdx.y;
+  const int b = at.z;
+  const int r0 = (!KEYS && p.causal ? t.blocks[0] - 1 - (int)at.x : (int)at.x) * kTile;
+  const int hk = KEYS ? at.y : at.y / p.group;
+  const int h0 = KEYS ? hk * p.group : at.y;
   const RowInfo info = row_info(p, b);
   const int owned = min(kTile, (KEYS ? p.k_len : p.q_len) - r0);
 
@@ -152,9 +154,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     for (int i = 0; i < x.slots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
     bar_init(bar(kOwnFull), 1);
     for (int w = 0; w < 3; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 8);
+    for (int w = 0; w < 2; ++w) bar_init(bar(kScanned + w), 8);
     bar_init(bar(kDone), 1);
     fence_bar_init();
     dead = 0;
+    tainted = 0;
     range[0] = 0x7fffffff;
     range[1] = 0;
     tma_prefetch(&t.qm);
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   const uint32_t tmem = tmem_slot;
   // The keys' kernel needs nothing of the queries' one: its blocks may start on
   // SMs that have no more blocks of this one.
-  if (!KEYS) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!KEYS && !SCAN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // the streamed tiles [sb, se), in steps of 64, of each head
   int sb = 0, se;
@@ -204,12 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   constexpr uint32_t kAcc = NB * 128, kAcc2 = kAcc + (KEYS ? DP : 0);
   // registers: 5 groups of warps x 96 at the start; 4 x 104 + 64 = 480
   if (warp < 16) {
-    take_registers<104>();
+    if (!SCAN) take_registers<104>();
     const int w = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, lane = tid & 31;
     const int lane_row = quarter * 32 + lane, in_group = half * 128 + lane_row;
     const uint32_t lanes = (uint32_t)quarter << 21;
     const int row = r0 + lane_row;  // the key or the query
     const float c = p.scale * kLog2e;
+    const bool raw = MODE == 0 || (SCAN && t.raw);
     const float sigma = BF16 ? 1.f : ds_scale(x, b * p.kv_heads + hk, p.batch * p.kv_heads);
     const float tau = BF16 ? 1.f : sigma * exp2f(-kLift<BF16>);
     const int32_t* kdocs = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     }
     float* bias = bias_mem + (KEYS ? w * nbias : 0);
     float* diag = diag_mem + w * ndiag;
-    int buffer = w, turn = 0, slot = w, round = 0;
+    int buffer = w, turn = 0, slot = w, round = 0, scan = 0;
     int head = -1, hh = 0, tile = sb + w;  // the streamed tile, and the head of the group it is of
     bool ok = true;
     for (int it = w; it < n; it += 2, tile += 2) {
@@ -280,7 +285,34 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         if (docs) seen &= (uint32_t)same_document<kColumns>(sdocs + c0, s_len - c0, rd);
       }
 
-      ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err);
+      unsigned char* smem_slot = mem + L::kRing + slot * L::kSlot;
+      // this thread's half of a streamed row: of q or dout, or of k
+      const int s_op = (in_group >> 6) & 1, s_frame = first + (in_group & 63);
+      unsigned char* s_row = smem_slot + s_op * L::kHalf + (in_group & 63) * 128;
+      uint32_t bad_seen = 0;  // columns seen by this row that are not finite
+      bool well = true;
+      if constexpr (SCAN) {
+        if (masked) {
+          well = bar_wait(bar(kFull + slot), round, &dead, t.err);
+          bool bad = false;
+          if (well && (KEYS || s_op == 0))
+            bad = clean_row<BF16, L::kBoxes>(
+                s_row, L::kBox, 4 * half,
+                s_frame < s_len && ((!KEYS && s_frame >= info.len) || (kdocs && sdocs[s_frame] < 0)));
+          fence_async();
+          const uint32_t rows = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) {
+            bad_rows[scan][w][half * 4 + quarter] = rows;
+            bar_arrive(bar(kScanned + w));
+          }
+          well = bar_wait(bar(kScanned + w), scan, &dead, t.err) && well;
+          const uint32_t* all = bad_rows[scan][w] + half;  // rows 32 half ..: every second warp's
+          bad_seen = seen & (all[0] | all[2] | all[4] | all[6]);
+          scan ^= 1;
+        }
+        clean = false;
+      }
+      ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err) && well;
       fence_after();
       if (clean || KEYS) ok = bar_wait(bar(kFull + slot), round, &dead, t.err) && ok;
       if (joined) {
@@ -288,17 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       } else if (!__all_sync(0xffffffffu, ok)) {
         break;
       }
-      unsigned char* smem_slot = mem + L::kRing + slot * L::kSlot;
       if (clean) {
         // streamed frames that nothing may use become zeros before the second
         // products read them: q and dout, or k
-        const int r = in_group & 63, op = (in_group >> 6) & 1, piece = in_group >> 7, frame = first + r;
-        const bool unused = frame < s_len && ((!KEYS && frame >= info.len) || (kdocs && sdocs[frame] < 0));
-        if (unused && (KEYS || op == 0)) {
-          unsigned char* to = smem_slot + op * L::kHalf + r * 128;
-          for (int e = 0; e < L::kBoxes; ++e)
-            for (int f = 4 * piece; f < 4 * piece + 4; ++f) *(uint4*)(to + e * L::kBox + 16 * f) = make_uint4(0, 0, 0, 0);
-        }
+        const bool unused = s_frame < s_len && ((!KEYS && s_frame >= info.len) || (kdocs && sdocs[s_frame] < 0));
+        if (unused && (KEYS || s_op == 0)) clear_row<L::kBoxes>(s_row, L::kBox, 4 * half);
         fence_async();
       }
       const float* lse = (const float*)(smem_slot + L::kStats) + half * kColumns;
@@ -312,7 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       wait_ld();
       tie32(u);
       if (MODE != 2) tie32(dp);
-      tile_scores<kColumns, MODE, KEYS, MODE == 2>(s, slope, p, c, bias, slope2,
+      if (SCAN && raw) {
+#pragma unroll
+        for (int j = 0; j < (MODE == 2 ? kColumns : 1); ++j) slope[j] = 1.f;
+      }
+      if (!raw) tile_scores<kColumns, MODE, KEYS, MODE == 2>(s, slope, p, c, bias, slope2,
                                                    KEYS ? row - (info.start + c0) : c0 - (info.start + row));
 #pragma unroll
       for (int j = 0; j < kColumns; j += 4) {
@@ -321,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const float2 z = make_float2(s[j + e], s[j + e + 1]), n2 = e ? make_float2(-q.z, -q.w) : make_float2(-q.x, -q.y);
-          const float2 a = MODE == 0 ? fma2(z, both(c), n2) : add2(z, n2);
+          const float2 a = raw ? fma2(z, both(c), n2) : add2(z, n2);
           s[j + e] = ex2(a.x);
           s[j + e + 1] = ex2(a.y);
         }
@@ -329,6 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       if (masked) {
 #pragma unroll
         for (int j = 0; j < kColumns; ++j) s[j] = (seen >> j & 1) ? s[j] : 0.f;
+      }
+      if (SCAN) {
+#pragma unroll
+        for (int j = 0; j < kColumns; ++j) s[j] = (bad_seen >> j & 1) ? NAN : s[j];
       }
       uint32_t pk[kColumns / 2];
       if (KEYS) {
@@ -444,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       // more), to be written by lines
       constexpr int kPieces = kShare / 8;
       unsigned char* stage = mem + warp * 32 * 128;
+      float taints = 0.f;
 #pragma unroll
       for (int y = 0; y < kShare; y += 16) {
         uint32_t o[16];
@@ -451,6 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         wait_ld();
         tie16(o);
         uint32_t v[8];
+        if (n > 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) taints = taint(taints, __uint_as_float(o[e]));
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           v[e] = n > 0 ? pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
@@ -458,11 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         stage_piece(stage, lane, y / 8 + 1, make_uint4(v[4], v[5], v[6], v[7]));
       }
       __syncwarp();
+      if (lane_row < owned && taints != 0.f) tainted = 1;  // NaN
       write_rows<kPieces>(stage, 0, out + begin, st.t, owned - quarter * 32, min(kPieces, (p.dim - begin) / 8));
       fence_before();
     }
   } else {
-    give_registers<64>();
+    if (!SCAN) give_registers<64>();
     const uint32_t lead = elect();
     if (warp == 16 && n > 0) {
       // ---- copies: the owned tile once, then streamed tiles
@@ -571,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     }
   }
   __syncthreads();
+  if (!SCAN && t.flags && tid == 0) t.flags[index] = tainted;
   if (grad) {
     if (warp < 16) far_mem[tid] = far_lo, far_mem[512 + tid] = far_hi;
     __syncthreads();
@@ -601,17 +642,46 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   }
   // what follows in the stream waits for this kernel: one block of it waits
   // for the queries' kernel
-  if (KEYS && blockIdx.x + blockIdx.y + blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (KEYS && !SCAN && index == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (SCAN) {  // another block's work may follow
+    if (tid == 0) {
+      for (int i = 0; i < x.slots; ++i) bar_free(bar(kFull + i)), bar_free(bar(kEmpty + i));
+      for (int i = kOwnFull; i < kBarCount; ++i) bar_free(bar(i));
+    }
+    fence_async();
+    __syncthreads();
+  }
+}
+
+template <int DP, bool BF16, int MODE, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t,
+                                                      const __grid_constant__ Extra x) {
+  block<DP, BF16, MODE, KEYS, false>(t, x, blockIdx, (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
+}
+template <int DP, bool BF16, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1) scan_kernel(const __grid_constant__ TcParams t,
+                                                           const __grid_constant__ Extra x) {
+  for (int i = blockIdx.x; i < t.blocks[0] * t.blocks[1] * t.blocks[2]; i += gridDim.x)
+    if (t.flags[i])
+      block<DP, BF16, 2, KEYS, true>(
+          t, x, dim3(i % t.blocks[0], i / t.blocks[0] % t.blocks[1], i / t.blocks[0] / t.blocks[1]), i);
 }
 
 template <int DP, bool BF16, bool KEYS>
-fm_status launch(const TcParams& t, Extra x, int mode, cudaStream_t st) {
+fm_status launch(TcParams t, Extra x, int mode, cudaStream_t st) {
   const int rows = KEYS ? t.p.k_len : t.p.q_len;
   const dim3 grid((rows + kTile - 1) / kTile, KEYS ? t.p.kv_heads : t.p.heads, t.p.batch);
   const bool bias = t.p.map != nullptr, grad = !KEYS && t.p.part != nullptr;
   const size_t smem = Smem<DP, KEYS>::bytes(t.p.max_distance, bias, grad);
   x.slots = Smem<DP, KEYS>::slots(t.p.max_distance, bias, grad);
   if (x.slots < 3) return FM_ERR_UNSUPPORTED;
+  t.blocks[0] = grid.x, t.blocks[1] = grid.y, t.blocks[2] = grid.z;
+  if (mode == kScan) {
+    const long long blocks = (long long)grid.x * grid.y * grid.z;
+    if (!allow_smem(scan_kernel<DP, BF16, KEYS>, smem)) return FM_ERR_CUDA;
+    scan_kernel<DP, BF16, KEYS><<<(unsigned)(blocks < num_sms() ? blocks : num_sms()), kThreads, smem, st>>>(t, x);
+    return launch_status();
+  }
   auto k = mode == 0 ? kernel<DP, BF16, 0, KEYS> : mode == 1 ? kernel<DP, BF16, 1, KEYS> : kernel<DP, BF16, 2, KEYS>;
   if (!allow_smem(k, smem)) return FM_ERR_CUDA;
   cudaLaunchConfig_t config = {};

@@ -50,7 +50,7 @@ struct Smem {
     return 1024 + kBias + (bias ? sizeof(float) * (2 * (max_distance + kBiasPad) + 1) : 0);
   }
 };
-enum { kFull = 0, kEmpty = 8, kQFull = 16, kSFull = 17, kPReady = 20, kOFull = 23, kOReady = 25, kBarCount = 27 };
+enum { kFull = 0, kEmpty = 8, kQFull = 16, kSFull = 17, kPReady = 20, kOFull = 23, kOReady = 25, kScanned = 27, kBarCount = 29 };
 // Score buffers of 128 columns. The tiles (key tile j, query tile w) are taken
 // in the order i = 2 j + w, buffer i % kBuffers. With three of them the scores
 // of a tile's successor are there before its softmax ends; beside two outputs
@@ -70,14 +70,17 @@ __device__ __forceinline__ bool pair_ok(int pair, bool ok) {
   return r != 0;
 }
 
-template <int DP, bool BF16, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t) {
+// One block's work; SCAN: of the second launch (TcParams::flags).
+template <int DP, bool BF16, int MODE, bool SCAN>
+__device__ __forceinline__ void block(const TcParams& t, const dim3 at, const int index) {
   using L = Smem<DP>;
   extern __shared__ unsigned char raw[];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int dead;
   __shared__ int range[2];
   __shared__ float row_stat[2][2][2][kTile];  // [tile parity][query tile][half][row]
+  __shared__ int tainted;                      // a result is not finite
+  __shared__ uint32_t bad_rows[SCAN ? L::kSlots : 1][4];  // of the slot's V: rows that are not finite
   const AttnParams& p = t.p;
   const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
   unsigned char* mem = raw + (base - smem_u32(raw));
@@ -85,9 +88,9 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   auto bar = [&](int n) { return base + L::kBars + 8 * n; };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be one per warp
 
-  const int split = blockIdx.z % t.splits, b = blockIdx.z / t.splits, h = blockIdx.y, hk = h / p.group;
+  const int split = at.z % t.splits, b = at.z / t.splits, h = at.y, hk = h / p.group;
   // causal rows late in the sequence see the most keys: they go first
-  const int q0 = (p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * 2 * kTile;
+  const int q0 = (p.causal ? t.blocks[0] - 1 - (int)at.x : (int)at.x) * 2 * kTile;
   const RowInfo info = row_info(p, b);
   const int nq = min(2 * kTile, p.q_len - q0);
 
@@ -95,9 +98,10 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     for (int i = 0; i < L::kSlots; ++i) bar_init(bar(kFull + i), 1), bar_init(bar(kEmpty + i), 1);
     bar_init(bar(kQFull), 1);
     for (int w = 0; w < 3; ++w) bar_init(bar(kSFull + w), 1), bar_init(bar(kPReady + w), 8);
-    for (int w = 0; w < 2; ++w) bar_init(bar(kOFull + w), 1), bar_init(bar(kOReady + w), 1);
+    for (int w = 0; w < 2; ++w) bar_init(bar(kOFull + w), 1), bar_init(bar(kOReady + w), 1), bar_init(bar(kScanned + w), 8);
     fence_bar_init();
     dead = 0;
+    tainted = 0;
     range[0] = 0x7fffffff;
     range[1] = 0;
     tma_prefetch(&t.qm);
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
   // registers: the block starts with 5 groups x 96; the softmax threads take
   // 104 and leave the others 64 (4 x 104 + 64 = 480)
   if (warp < 16) {
-    take_registers<104>();
+    if (!SCAN) take_registers<104>();
     // ---- softmax: a thread has 64 columns of one query row
     const int w = warp >> 3, half = (warp >> 2) & 1, pair = (warp >> 3) * 4 + (warp & 3);
     const int lane_row = (warp & 3) * 32 + (tid & 31);
@@ -144,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     const uint32_t to = tmem + lanes + kO + w * DP + half * (DP / 2);
     const int i = q0 + w * kTile + lane_row, place = info.start + i;
     const float c = p.scale * kLog2e;
+    const bool raw = MODE == 0 || (SCAN && t.raw);
     const float slope2 = MODE == 2 && p.slopes ? p.slopes[h] * kLog2e : 0.f;
     int qd = -2;  // matches no document
     const int32_t* kdocs = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
@@ -165,6 +170,14 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     float m = -INFINITY, l = 0.f;  // l: of this thread's columns
     bool ok = true;
     int buffer = w, turn = 0;  // of this tile's scores
+    int scan = 0;              // scanned tiles so far, modulo 2
+    int first_end = info.len;  // all_end of the first query tile
+    int4 other_range = make_int4(0, 0, 1, 0);
+    if (SCAN && p.causal) first_end = min(first_end, max(info.start + q0 + 1, info.prefix));
+    if (SCAN && kdocs) {
+      const int o = q0 / kTile + (w ^ 1);
+      other_range = o < t.q_tiles ? t.q_ranges[b * t.q_tiles + o] : make_int4(0x7fffffff, -1, 0, 0);
+    }
     for (int j = 0; j < n; ++j) {
       const uint32_t ts = tmem + lanes + buffer * kTile;
       const int k0 = (tb + j) * kTile, mine = k0 + half * kColumns;
@@ -179,7 +192,34 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         seen = column_range<kColumns>(0, seen_end - mine);
         if (docs) seen &= same_document<kColumns>(kdocs + mine, p.k_len - mine, qd);
       }
-      ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err);
+      uint64_t bad_seen = 0;
+      if constexpr (SCAN) {
+        // V is shared: both query tiles scan it where either has masked pairs
+        bool scanned = masked || k0 + kTile > first_end;
+        const int v_slot = (2 * j + 1) % L::kSlots;
+        ok = true;
+        if (kdocs) {
+          const int4 kr = t.k_ranges[b * t.k_tiles + tb + j];
+          scanned |= !(other_range.z && kr.z && other_range.x == kr.x);
+        }
+        if (scanned) {
+          const int key = k0 + lane_row;
+          ok = bar_wait(bar(kFull + v_slot), ((2 * j + 1) / L::kSlots) & 1, &dead, t.err);
+          if (ok)
+            clean_row<BF16, L::kBoxes>(mem + L::kRing + v_slot * L::kOperand + lane_row * 128, L::kBox, 4 * half,
+                                       key >= info.len || (kdocs && kdocs[key] < 0), &bad_rows[v_slot][warp & 3],
+                                       1u << (tid & 31));
+          fence_async();
+          __syncwarp();
+          if (tid % 32 == 0) bar_arrive(bar(kScanned + w));
+          ok = bar_wait(bar(kScanned + w), scan, &dead, t.err) && ok;
+          const volatile uint32_t* rows = bad_rows[v_slot] + 2 * half;
+          bad_seen = seen & ((uint64_t)rows[1] << 32 | rows[0]);
+          scan ^= 1;
+        }
+        clean = false;
+      }
+      ok = bar_wait(bar(kSFull + buffer), turn, &dead, t.err) && (!SCAN || ok);
       fence_after();
       if (clean) {
         // rows of V that nothing may use become zeros: 0 weights times
@@ -187,11 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         const int it = 2 * j + 1;
         ok = bar_wait(bar(kFull + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err) && ok;
         const int key = k0 + lane_row;
-        if (ok && (key >= info.len || (kdocs && kdocs[key] < 0))) {
-          unsigned char* row = mem + L::kRing + (it % L::kSlots) * L::kOperand + lane_row * 128;
-          for (int x = 0; x < L::kBoxes; ++x)
-            for (int e = 4 * half; e < 4 * half + 4; ++e) *(uint4*)(row + x * L::kBox + 16 * e) = make_uint4(0, 0, 0, 0);
-        }
+        if (ok && (key >= info.len || (kdocs && kdocs[key] < 0)))
+          clear_row<L::kBoxes>(mem + L::kRing + (it % L::kSlots) * L::kOperand + lane_row * 128, L::kBox, 4 * half);
         fence_async();
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -202,11 +239,15 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       wait_ld();
       tie32(u);
       tie32(u + 32);
-      tile_scores<kColumns, MODE, false, false>(s, unused, p, c, bias, slope2, mine - place);
+      if (!raw) tile_scores<kColumns, MODE, false, false>(s, unused, p, c, bias, slope2, mine - place);
       if (masked) {
         const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
         for (int e = 0; e < kColumns; ++e) s[e] = ((e < 32 ? lo : hi) >> (e & 31) & 1) ? s[e] : -INFINITY;
+      }
+      if (SCAN) {
+#pragma unroll
+        for (int e = 0; e < kColumns; ++e) s[e] = (bad_seen >> e & 1) ? NAN : s[e];
       }
       float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -219,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       }
       // both warps have their scores in registers now: P may replace them
       mx = fmaxf(mx, row_stat[j & 1][w][half ^ 1][lane_row]);
-      if (MODE == 0) mx *= c;  // scale > 0 here
+      if (raw) mx *= c;  // scale > 0 here
       if (__any_sync(0xffffffffu, mx > m + kRise || (m == -INFINITY && mx > m))) {
         const float top_m = fmaxf(m, mx), f = top_m == -INFINITY ? 1.f : ex2(m - top_m);
         m = top_m;
@@ -251,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 z = make_float2(s[32 * part + 2 * e], s[32 * part + 2 * e + 1]);
-          const float2 a = MODE == 0 ? fma2(z, both(c), both(-m0)) : add2(z, both(-m0));
+          const float2 a = raw ? fma2(z, both(c), both(-m0)) : add2(z, both(-m0));
           const float2 q = make_float2(ex2(a.x), ex2(a.y));
           sum[e & 1] = add2(sum[e & 1], q);
           // weights go to the product in the inputs' type: the sum keeps 32 bits
@@ -291,13 +332,17 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
       unsigned char* stage = mem + w * L::kOperand + (DP == 128 ? half * L::kBox : 0) + (warp & 3) * 32 * 128;
       const int first = DP == 128 ? 0 : half * kPieces, lane = tid & 31;
       const int rows_left = p.q_len - (i - lane), pieces = min(kPieces, p.dim / 8 - half * kPieces);
+      float taints = 0.f;
       auto result = [&](int y, float (&v)[16]) {
         uint32_t o[16];
         if (n > 0) tmem_ld16(to + y, o);
         wait_ld();
         tie16(o);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = n > 0 ? __uint_as_float(o[e]) * f : 0.f;
+        for (int e = 0; e < 16; ++e) {
+          v[e] = n > 0 ? __uint_as_float(o[e]) * f : 0.f;
+          taints = taint(taints, v[e]);
+        }
       };
       if (t.splits > 1) {
 #pragma unroll 1
@@ -336,10 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
           __syncwarp();
         }
       }
+      if (store && taints != 0.f) tainted = 1;  // NaN
       fence_before();
     }
   } else {
-    give_registers<64>();
+    if (!SCAN) give_registers<64>();
     const uint32_t lead = elect();
     if (warp == 16 && n > 0) {
       // ---- copies: q once, then K and V tiles in turn through the ring
@@ -355,6 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
         const bool ok = bar_wait(bar(kEmpty + s), (round & 1) ^ 1, &dead, t.err);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (lead) {
+          if (SCAN && (it & 1)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad_rows[s][e] = 0;
+          }
           bar_expect(bar(kFull + s), L::kOperand);
           const int row = (tb + it / 2) * kTile;
           const uint32_t to = base + L::kRing + s * L::kOperand;
@@ -429,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     }
   }
   __syncthreads();
+  if (!SCAN && t.flags && tid == 0) t.flags[index] = tainted;
   if (dead && tid == 0) {
     // copies still in flight land in this block's memory: give them time
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
@@ -439,15 +490,40 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ Tc
     fence_after();
     tmem_free(tmem, 512);
   }
+  if (SCAN) {  // another block's work may follow
+    if (tid == 0) {
+      for (int i = 0; i < L::kSlots; ++i) bar_free(bar(kFull + i)), bar_free(bar(kEmpty + i));
+      for (int i = kQFull; i < kBarCount; ++i) bar_free(bar(i));
+    }
+    fence_async();
+    __syncthreads();
+  }
+}
+
+template <int DP, bool BF16, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t) {
+  block<DP, BF16, MODE, false>(t, blockIdx, (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
+}
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) scan_kernel(const __grid_constant__ TcParams t) {
+  for (int i = blockIdx.x; i < t.blocks[0] * t.blocks[1] * t.blocks[2]; i += gridDim.x)
+    if (t.flags[i])
+      block<DP, BF16, 2, true>(t, dim3(i % t.blocks[0], i / t.blocks[0] % t.blocks[1], i / t.blocks[0] / t.blocks[1]), i);
 }
 
 template <int DP, bool BF16>
-fm_status launch(const TcParams& t, int mode, cudaStream_t st) {
+fm_status launch(TcParams t, int mode, cudaStream_t st) {
   const dim3 grid((t.p.q_len + 2 * kTile - 1) / (2 * kTile), t.p.heads, t.p.batch * t.splits);
+  t.blocks[0] = grid.x, t.blocks[1] = grid.y, t.blocks[2] = grid.z;
   const size_t smem = Smem<DP>::bytes(t.p.max_distance, t.p.map != nullptr);
   auto k = mode == 0 ? kernel<DP, BF16, 0> : mode == 1 ? kernel<DP, BF16, 1> : kernel<DP, BF16, 2>;
   if (!allow_smem(k, smem)) return FM_ERR_CUDA;
   k<<<grid, kThreads, smem, st>>>(t);
+  if (t.flags) {
+    const long long blocks = (long long)grid.x * grid.y * grid.z;
+    if (!allow_smem(scan_kernel<DP, BF16>, smem)) return FM_ERR_CUDA;
+    scan_kernel<DP, BF16><<<(unsigned)(blocks < num_sms() ? blocks : num_sms()), kThreads, smem, st>>>(t);
+  }
   return launch_status();
 }
 

@@ -169,15 +169,16 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
     if (!__all_sync(0xffffffffu, ok)) break;
     const int k0 = k_begin + (warp + n * kWarps) * kKeys;
     const uint32_t K = ring + (n % kStages) * stage_bytes<DP>(), V = K + kOperand;
-    if (k0 + kKeys > info.len || kdocs) {
-      // rows of V that nothing may use become zeros: 0 weights times whatever
-      // memory holds would not be 0
+    bool masked = k0 + kKeys > k_end || kdocs;
+    if (p.causal) masked = masked || k0 + kKeys > max(info.start + 1, info.prefix);
+    uint32_t bad = 0;  // two bits a key: halves of its row of V that are not finite
+    if (masked) {
+      // rows of V that nothing may use, or that are not finite, become zeros: a
+      // weight of 0 times what memory holds would not be 0
       const int row = lane >> 1, key = k0 + row;
-      if (key >= info.len || (kdocs && kdocs[key] < 0)) {
-        unsigned char* to = mem + (V - smem_u32(mem)) + row * 128 + (lane & 1) * 64;
-        for (int x = 0; x < kBoxes; ++x)
-          for (int e = 0; e < 4; ++e) *(uint4*)(to + x * kBox + 16 * e) = make_uint4(0, 0, 0, 0);
-      }
+      const bool no_use = key >= info.len || (kdocs && kdocs[key] < 0);
+      bad = __ballot_sync(0xffffffffu, clean_row<BF16, kBoxes>(mem + (V - smem_u32(mem)) + row * 128, kBox,
+                                                              4 * (lane & 1), no_use));
       __syncwarp();
     }
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -193,8 +194,6 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
     }
     // element e of s[x]: row quad + 8 (e / 2), key k0 + 8 x + pair + e % 2
     const bool far = !p.map || (k0 - info.start - p.q_len + 1 >= D) || (k0 + kKeys - 1 - info.start <= -D);
-    bool masked = k0 + kKeys > k_end || kdocs;
-    if (p.causal) masked = masked || k0 + kKeys > max(info.start + 1, info.prefix);
     const bool is_above = k0 > info.start;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -217,6 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
           bool seen = key < k_end && !(p.causal && off > 0 && key >= info.prefix);
           if (kdocs && seen) seen = __ldg(kdocs + key) == qd[r];
           z = seen ? z : -INFINITY;
+          if (bad != 0 && seen && (bad >> (2 * (key - k0)) & 3)) z = NAN;
         }
         s[x][e] = z;
       }

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256) bwd_stats(const AttnParams p, int q_pad, 
       s += __shfl_xor_sync(0xffffffffu, s, o, LANES);
       norm += __shfl_xor_sync(0xffffffffu, norm, o, LANES);
     }
-    top = fmaxf(top, norm);
+    top = norm <= 3.402823466e38f ? fmaxf(top, norm) : top;  // what is not finite sets no scale
     if (lane == 0 && i < q_pad) {
       lse2[row * q_pad + i] = l == -INFINITY ? INFINITY : l * kLog2e - lift;
       delta[row * q_pad + i] = s;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256) bwd_v_peak(const AttnParams p, float* pea
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, o, 16);
-    top = fmaxf(top, norm);
+    top = norm <= 3.402823466e38f ? fmaxf(top, norm) : top;  // what is not finite sets no scale
   }
   block_peak(top, peak + b * p.kv_heads + h);
 }
@@ -319,6 +319,12 @@ TcPlan tc_plan(const AttnParams& p, bool backward) {
   if (backward) at += align256((int64_t)sizeof(float) * 2 * p.batch * p.kv_heads);
   w.bias = at;
   if (p.map && w.step.splits == 0) at += align256((int64_t)sizeof(float) * p.heads * (2 * (int64_t)p.max_distance + 1));
+  w.flags = at;
+  if (p.causal || p.q_docs) {
+    const int64_t q_blocks = backward ? w.q_tiles : (w.q_tiles + 1) / 2;
+    w.flags_keys = at + align256((int64_t)sizeof(int) * q_blocks * p.heads * p.batch * w.splits);
+    at = w.flags_keys + (backward ? align256((int64_t)sizeof(int) * w.k_tiles * p.kv_heads * p.batch) : 0);
+  }
   w.total = at;
   return w;
 }
@@ -329,6 +335,7 @@ fm_status tc_setup(TcParams& t, const AttnParams& p, int64_t dtype, const TcPlan
   t.p = p;
   t.err = ops_error_word();
   if (t.err == nullptr) return FM_ERR_CUDA;
+  t.raw = mode_of(p) == 0;
   t.q_tiles = w.q_tiles;
   t.k_tiles = w.k_tiles;
   t.dim16 = (p.dim + 15) / 16 * 16;
@@ -365,6 +372,7 @@ fm_status attn_tc_forward(const AttnParams& p, int64_t dtype, char* ws, cudaStre
   } else {
     s = tc_setup(t, p, dtype, w, ws, kTile, kTile, st);
     const int mode = mode_of(p);
+    if (p.causal || p.q_docs) t.flags = (int*)(ws + w.flags);
     if (s == FM_OK)
       s = p.dim <= 64 ? (bf16 ? attn_fwd_bf16_64(t, mode, st) : attn_fwd_f16_64(t, mode, st))
                       : (bf16 ? attn_fwd_bf16_128(t, mode, st) : attn_fwd_f16_128(t, mode, st));
@@ -413,8 +421,17 @@ fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cu
                            : (bf16 ? attn_bwd_queries_bf16_128 : attn_bwd_queries_f16_128);
   const Fn keys = small ? (bf16 ? attn_bwd_keys_bf16_64 : attn_bwd_keys_f16_64)
                         : (bf16 ? attn_bwd_keys_bf16_128 : attn_bwd_keys_f16_128);
-  if (fm_status s = queries(t, x, mode, st)) return s;
-  return keys(t, x, mode, st);
+  const bool masks = p.causal || p.q_docs;
+  // the second launches (kScan, see TcParams::flags) come after both first ones,
+  // which run beside one another
+  for (int m : {mode, kScan}) {
+    if (m == kScan && !masks) break;
+    t.flags = masks ? (int*)(ws + w.flags) : nullptr;
+    if (fm_status s = queries(t, x, m, st)) return s;
+    t.flags = masks ? (int*)(ws + w.flags_keys) : nullptr;
+    if (fm_status s = keys(t, x, m, st)) return s;
+  }
+  return FM_OK;
 }
 }  // namespace fm
 

@@ -31,7 +31,18 @@ struct TcParams {
   float* part_o;         // [splits][batch][heads][q_len][dim]
   float* part_lse;       // [splits][batch][heads][q_len], base 2
   unsigned* err;
+  // Where masks may hide a key from one query of a tile and not from another, a
+  // block notes here whether its results were all finite, and a second launch
+  // runs the others again, looking at every streamed row (clean_row): nearly
+  // always it has nothing to do. To look at the rows at once cost a sixth of the
+  // time of packed training; a second round inside the block cost as much in
+  // registers. NULL: no such masks.
+  int* flags;  // [blocks]
+  int blocks[3];  // of the first launch
+  int raw;        // it ran as MODE 0: the second has to round as it did
 };
+
+constexpr int kScan = 3;  // in place of a mode: the second launch
 
 // the device's error word for the operators, NULL if there is none
 unsigned* ops_error_word();
@@ -52,7 +63,7 @@ fm_status attn_step(const AttnParams& p, int64_t dtype, const StepPlan& w, float
 struct TcPlan {
   StepPlan step;  // step.splits > 0: the forward pass takes the few-query kernel
   int splits, split_tiles, q_tiles, k_tiles;
-  int64_t ranges, part_o, part_lse, stats, peak, bias, total;
+  int64_t ranges, part_o, part_lse, stats, peak, bias, flags, flags_keys, total;
 };
 bool tc_layout_ok(const AttnParams& p, int64_t dtype, bool backward);
 TcPlan tc_plan(const AttnParams& p, bool backward);  // backward needs heads, q_len, map and grad only
@@ -115,7 +126,17 @@ __device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SL
   using namespace tc;
   if (MODE == 0) return;
   const int D = p.max_distance, last = REV ? o0 - (N - 1) : o0 + (N - 1);
-  if (MODE == 2) {
+  if (MODE == 2 && !(p.cap > 0.f) && p.slopes == nullptr) {
+    // as MODE 1, or a scale alone
+    if (CAP_SLOPE) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) slope[j] = 1.f;
+    }
+    if (p.map == nullptr) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[j] *= c;
+    }
+  } else if (MODE == 2) {
     // a slope's share is linear in the column where all offsets have one sign
     const bool ahead = __all_sync(0xffffffffu, min(o0, last) >= 0), back = __all_sync(0xffffffffu, max(o0, last) <= 0);
     const bool linear = p.slopes && (ahead || back);
@@ -202,6 +223,49 @@ __device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SL
       }
     }
   }
+}
+
+// Whether any of eight 16-bit floats is infinite or NaN: an exponent of ones
+// overflows into the sign's place when one is added to it.
+template <bool BF16>
+__device__ __forceinline__ bool not_finite(uint4 v) {
+  constexpr uint32_t one = BF16 ? 0x00800080u : 0x04000400u, m = 0x7fff7fffu;
+  return ((((v.x & m) + one) | ((v.y & m) + one) | ((v.z & m) + one) | ((v.w & m) + one)) & 0x80008000u) != 0;
+}
+// adds 0, or NaN for a value that is not finite
+__device__ __forceinline__ float taint(float sum, float v) { return fmaf(v, 0.f, sum); }
+// zeros for four 16-byte pieces of a row in each of BOXES boxes
+template <int BOXES>
+__device__ __forceinline__ void clear_row(unsigned char* row, int box, int first) {
+#pragma unroll
+  for (int x = 0; x < BOXES; ++x)
+#pragma unroll
+    for (int e = first; e < first + 4; ++e) *(uint4*)(row + x * box + 16 * e) = make_uint4(0, 0, 0, 0);
+}
+// In a tile with masked pairs a streamed row must not reach the rows that do
+// not see it, but a weight of 0 times infinity or NaN would. Four 16-byte
+// pieces of a row in each of BOXES boxes: all zeros if the row is unused, and
+// pieces that are not finite become zeros; whether there were any. A row that
+// sees such a row gets a NaN as its weight, and so a result of NaN. mark: set
+// before a piece is cleared, for others who scan the same row.
+template <bool BF16, int BOXES>
+__device__ __forceinline__ bool clean_row(unsigned char* row, int box, int first, bool unused,
+                                          uint32_t* mark = nullptr, uint32_t bit = 0) {
+  bool bad = false;
+#pragma unroll
+  for (int x = 0; x < BOXES; ++x)
+#pragma unroll
+    for (int e = first; e < first + 4; ++e) {
+      uint4* at = (uint4*)(row + x * box + 16 * e);
+      const bool wrong = !unused && not_finite<BF16>(*at);
+      if (wrong && mark) {
+        atomicOr(mark, bit);
+        __threadfence_block();
+      }
+      if (unused || wrong) *at = make_uint4(0, 0, 0, 0);
+      bad |= wrong;
+    }
+  return bad;
 }
 
 // Bits of the N columns whose document is this row's. ids: the columns'

@@ -345,6 +345,42 @@ def test_attention_masked_scores(ops):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dim", [64, 128, 40])
+def test_attention_hidden_values(ops, dtype, bad, dim):
+    # recordings side by side, one of them broken: the other's results and
+    # gradients are those of the whole batch without the broken one's values
+    T = 200
+    ids = docs_of(T, [(0, 90), (1, 70), (2, 40)])
+    q, k, v, dy, g = make((1, T, T, 2, 1, dim), dtype)
+    for causal in (False, True):
+        clean = check_attention(ops, q, k, v, "clean", dy=dy, q_docs=ids, k_docs=ids, causal=causal)
+        broken = [t.clone() for t in (q, k, v, dy)]
+        for t in broken:
+            t[:, 90:160, :, 3] = bad
+        leaves = [t.detach().requires_grad_() for t in broken[:3]]
+        out = ops.attention(*leaves, q_docs=ids, k_docs=ids, causal=causal)
+        grads = torch.autograd.grad(out, leaves, broken[3])
+        assert torch.equal(out[:, :90], clean[0][:, :90]) and torch.equal(out[:, 160:], clean[0][:, 160:])
+        for got, want in zip((out, *grads), (clean[0], *clean[1])):
+            # f16's dS has another power of two as its scale without the broken
+            # recording: the smallest of them round otherwise
+            for part in (slice(0, 90), slice(160, T)):
+                room = 2 * ref.U[dtype] * want[:, part].abs().max()
+                assert ((got[:, part] - want[:, part]).abs() <= room).all()
+            assert not torch.isfinite(got[:, 90:160]).all()
+    # causal: what comes after a query, in few-query form and in tiles
+    for Tq in (T, 3):
+        k2, v2 = k.clone(), v.clone()
+        k2[:, 150:], v2[:, 150:] = bad, bad
+        out = ops.attention(q[:, :Tq], k2, v2, causal=True, q_start=149 - (Tq - 1) if Tq < T else 0)
+        want = ops.attention(q[:, :Tq], k, v, causal=True, q_start=149 - (Tq - 1) if Tq < T else 0)
+        n = 150 if Tq == T else Tq
+        assert torch.equal(out[:, :n], want[:, :n])
+        assert torch.isnan(out[:, n:]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_attention_layouts(ops, dtype):
     g = gen(11)
     B, T, H, D = 2, 150, 4, 64
