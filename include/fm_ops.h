@@ -186,8 +186,9 @@ int64_t fm_attention_workspace(const fm_attention_args* args, int backward);
 
 /* Takes and clears the current device's error word of these operators, after
  * waiting for the work queued on it: FM_ERR_KERNEL_TIMEOUT if a bounded wait
- * inside an attention kernel gave up (its results are then not valid), FM_OK
- * otherwise. Not allowed while a graph is being recorded. */
+ * inside an attention kernel gave up (its results are then not valid, and until
+ * the word is taken later calls may give up early too), FM_OK otherwise. Not
+ * allowed while a graph is being recorded. */
 fm_status fm_ops_poll_error(void);
 
 #ifdef __cplusplus

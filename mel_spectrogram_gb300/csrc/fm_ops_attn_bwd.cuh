@@ -18,8 +18,14 @@
 // arithmetic took twice its products' time, and the code of the biased modes
 // did not stay in the instruction cache.)
 //
-// Bound: the score products, whose 128 x 64 x 16 steps read 6 KB of shared
-// memory for 32 cycles of arithmetic (the tensor unit takes 128 bytes a cycle).
+// Bound: a group's chain on a tile. At head size 64 with a bias its arithmetic
+// takes about 2300 cycles (3300 where the bias gradient's diagonals are added
+// too), while the products of two tiles take 1000 to 1300; at 128 the score
+// products count as well: their 128 x 64 x 16 steps read 6 KB of shared memory
+// for 32 cycles of arithmetic (the tensor unit takes 128 bytes a cycle).
+// Measured: 8 packed rows of 3001 frames, 8 heads of 64, bf16, bias of 320
+// buckets up to 800: 204 us for the queries, 183 for the keys; 8 rows of 1292,
+// 16 heads of 128 on 4 key heads, f16, causal, capped: 170 and 235.
 #pragma once
 
 #include "fm_ops_attn_tc.cuh"

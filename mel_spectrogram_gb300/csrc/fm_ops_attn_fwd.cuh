@@ -2,24 +2,31 @@
 //
 // A block owns 256 queries of one head, as two tiles of 128, and streams the
 // keys in tiles of 128. Scores S = Q K^T and the output O += P V are tcgen05
-// products with accumulators in tensor memory; one thread per query row reads
-// its scores, keeps the running maximum and sum in registers, and writes its
+// products with accumulators in tensor memory; a thread reads its scores,
+// keeps its row's running maximum and its own sum in registers, and writes its
 // 16-bit weights P back over them, from where the second product takes them.
 // Warps: 0-7 and 8-15 do the softmax of one query tile each, two threads a row
 // with 64 columns each; warp 16 copies tiles by TMA into a ring, warp 17 issues
 // products. While one tile's softmax runs, the products of the other do.
 //
 // Bound: a key tile costs 2 x 2 products of 128 x 128 x dim (2048 cycles of the
-// tensor unit at dim 128) for 2 x 16384 exponentials. A tile's own chain
-// (scores, softmax, products) has to fit twice its products' time, which is
-// why a row has two threads: one thread a row took 1500 cycles for its
-// softmax, and with a tile's whole width unrolled the code of the biased modes
-// did not stay in the instruction cache.
+// tensor unit at dim 128) for 2 x 16384 exponentials, and takes about 3200: a
+// tile's own chain (scores, 1500 cycles of softmax, products) is longer than
+// its share of the tensor unit, and tensor memory has no room for a third score
+// buffer beside two outputs of 128 columns. Measured: 372 us for 8 rows of up
+// to 3001 frames, 16 heads of 128, bf16 (447 GFLOP: 1200 TFLOP/s, 0.61 of the
+// measured matrix rate). With a bias by distance at head size 64 the shared
+// reads of the bias, the exponentials and the products want about 1000 cycles
+// of a tile each, and a tile takes 3300.
+// What made it faster: products issued by a converged warp (472 to 363 us, see
+// mma_ss); two threads a row, for the biased modes, whose code with a row's 128
+// columns unrolled did not stay in the instruction cache (199 to 147 us of
+// packed training's forward pass); the third score buffer at head size 64 and
+// results written by lines (147 to 128).
 //
 // Rescaling O when the maximum rises is put off until it has risen by 2^8:
-// weights then stay below 2^8, exact in the sense that the same factor divides
-// out of sum and output, and O is touched a few times per row instead of once
-// per tile.
+// weights then stay below 2^8, the same factor divides out of sum and output,
+// and O is touched a few times per row instead of once per tile.
 #pragma once
 
 #include "fm_ops_attn_tc.cuh"

@@ -10,7 +10,9 @@
 // warps in the loop, and the copies cost no instructions of the other lanes
 // (with cp.async they took a third of 633 instructions a tile, which is what
 // bound the kernel, at 38 % of the bandwidth). Warps join through shared
-// memory, blocks through the join kernel.
+// memory, blocks through the join kernel. Measured, with the join: 293 MB of 64
+// caches of up to 3001 frames in 67 us (0.65 of the measured bandwidth), 184 MB
+// of an hour's 360001 frames in 46 (0.60), in 297 splits.
 #include "fm_ops_attn_tc.cuh"
 
 namespace fm {
@@ -169,18 +171,6 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
     if (!__all_sync(0xffffffffu, ok)) break;
     const int k0 = k_begin + (warp + n * kWarps) * kKeys;
     const uint32_t K = ring + (n % kStages) * stage_bytes<DP>(), V = K + kOperand;
-    bool masked = k0 + kKeys > k_end || kdocs;
-    if (p.causal) masked = masked || k0 + kKeys > max(info.start + 1, info.prefix);
-    uint32_t bad = 0;  // two bits a key: halves of its row of V that are not finite
-    if (masked) {
-      // rows of V that nothing may use, or that are not finite, become zeros: a
-      // weight of 0 times what memory holds would not be 0
-      const int row = lane >> 1, key = k0 + row;
-      const bool no_use = key >= info.len || (kdocs && kdocs[key] < 0);
-      bad = __ballot_sync(0xffffffffu, clean_row<BF16, kBoxes>(mem + (V - smem_u32(mem)) + row * 128, kBox,
-                                                              4 * (lane & 1), no_use));
-      __syncwarp();
-    }
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
@@ -191,6 +181,19 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
         mma16<BF16>(s[0], q[st], kf[0], kf[1]);
         mma16<BF16>(s[1], q[st], kf[2], kf[3]);
       }
+    }
+    bool masked = k0 + kKeys > k_end || kdocs;
+    if (p.causal) masked = masked || k0 + kKeys > max(info.start + 1, info.prefix);
+    uint32_t bad = 0;  // two bits a key: halves of its row of V that are not finite
+    if (__builtin_expect(masked, 0)) {
+      // rows of V that nothing may use, or that are not finite, become zeros: a
+      // weight of 0 times what memory holds would not be 0
+      const int row = lane >> 1, key = k0 + row;
+      const bool no_use = key >= info.len || (kdocs && kdocs[key] < 0);
+      bad = __ballot_sync(0xffffffffu, clean_row<BF16, kBoxes>(mem + (V - smem_u32(mem)) + row * 128, kBox,
+                                                              4 * (lane & 1), no_use));
+      fence_async();  // before the copy that fills this stage next
+      __syncwarp();
     }
     // element e of s[x]: row quad + 8 (e / 2), key k0 + 8 x + pair + e % 2
     const bool far = !p.map || (k0 - info.start - p.q_len + 1 >= D) || (k0 + kKeys - 1 - info.start <= -D);
@@ -216,10 +219,16 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
           bool seen = key < k_end && !(p.causal && off > 0 && key >= info.prefix);
           if (kdocs && seen) seen = __ldg(kdocs + key) == qd[r];
           z = seen ? z : -INFINITY;
-          if (bad != 0 && seen && (bad >> (2 * (key - k0)) & 3)) z = NAN;
         }
         s[x][e] = z;
       }
+    if (bad != 0) {  // a query that sees such a row (its score is not -inf) returns NaN
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (s[x][e] != -INFINITY && (bad >> (2 * (8 * x + pair + (e & 1))) & 3)) s[x][e] = NAN;
+    }
     // the running maximum follows only rises by 2^8, as in the tiled kernel
     float top[2];
 #pragma unroll

@@ -92,28 +92,29 @@ __global__ void __launch_bounds__(kTile) prepare(const AttnParams p, int q_tiles
 }
 
 // out = sum of the splits' results, weighted by 2^(lse - highest lse). A block
-// a row: its eight warps take every eighth split, four elements a lane, and
-// are added up in order.
-template <bool BF16>
-__global__ void __launch_bounds__(256) join(const AttnParams p, int splits, const float* part_o, const float* part_lse) {
-  __shared__ float tops[8], totals[8];
-  __shared__ float4 sums[8][32];
+// a row: its warps take splits in turn, four elements a lane, and are added up
+// in order. Eight warps for few splits; 32 for many, whose reads one after
+// another would otherwise be what takes the time.
+template <bool BF16, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) join(const AttnParams p, int splits, const float* part_o, const float* part_lse) {
+  __shared__ float tops[WARPS], totals[WARPS];
+  __shared__ float4 sums[WARPS][32];
   const long long rows = (long long)p.batch * p.heads * p.q_len, row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float top = -INFINITY;
-  for (int s = threadIdx.x; s < splits; s += 256) top = fmaxf(top, part_lse[s * rows + row]);
+  for (int s = threadIdx.x; s < splits; s += 32 * WARPS) top = fmaxf(top, part_lse[s * rows + row]);
   top = warp_max(top);
   if (lane == 0) tops[warp] = top;
   __syncthreads();
   top = tops[0];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) top = fmaxf(top, tops[w]);
+  for (int w = 1; w < WARPS; ++w) top = fmaxf(top, tops[w]);
   const float base = top == -INFINITY ? 0.f : top;
   float total = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // dim <= 128
   const bool mine = 4 * lane < p.dim;
 #pragma unroll 8
-  for (int s = warp; s < splits; s += 8) {
+  for (int s = warp; s < splits; s += WARPS) {
     const float lse = part_lse[s * rows + row], w = lse == -INFINITY ? 0.f : exp2f(lse - base);
     total += w;
     if (mine) {
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(256) join(const AttnParams p, int splits, cons
   __syncthreads();
   if (warp != 0) return;
 #pragma unroll
-  for (int w = 1; w < 8; ++w) {
+  for (int w = 1; w < WARPS; ++w) {
     const float4 o = sums[w][lane];
     acc.x += o.x;
     acc.y += o.y;
@@ -380,8 +381,9 @@ fm_status attn_tc_forward(const AttnParams& p, int64_t dtype, char* ws, cudaStre
   if (s != FM_OK || w.splits == 1) return s;
   const long long rows = (long long)p.batch * p.heads * p.q_len;
   const unsigned blocks = (unsigned)rows;
-  if (bf16) join<true><<<blocks, 256, 0, st>>>(p, w.splits, t.part_o, t.part_lse);
-  else join<false><<<blocks, 256, 0, st>>>(p, w.splits, t.part_o, t.part_lse);
+  const bool many = w.splits >= 64;
+  auto k = many ? (bf16 ? join<true, 32> : join<false, 32>) : (bf16 ? join<true, 8> : join<false, 8>);
+  k<<<blocks, many ? 1024 : 256, 0, st>>>(p, w.splits, t.part_o, t.part_lse);
   return launch_status();
 }
 

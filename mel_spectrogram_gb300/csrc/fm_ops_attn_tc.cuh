@@ -35,7 +35,7 @@ struct TcParams {
   // block notes here whether its results were all finite, and a second launch
   // runs the others again, looking at every streamed row (clean_row): nearly
   // always it has nothing to do. To look at the rows at once cost a sixth of the
-  // time of packed training; a second round inside the block cost as much in
+  // time of packed training; a second run inside the block cost as much in
   // registers. NULL: no such masks.
   int* flags;  // [blocks]
   int blocks[3];  // of the first launch

@@ -500,6 +500,36 @@ def test_attention_graph(ops):
         ref.close(out, *ref.attention(q, k, v, table=table, k_lens=lens)["out"], "replayed")
 
 
+def test_training_graph(ops):
+    # a training step recorded once, replayed on new values
+    q, k, v, dy, g = make((2, 200, 200, 4, 2, 64), BF16)
+    table = randn(g, 32, 4, dtype=BF16)
+    w = randn(g, 64, dtype=BF16)
+    leaves = [t.requires_grad_() for t in (q, k, v, table, w)]
+    ids = docs_of(200, [(0, 120), (1, 70)], [(3, 200)])
+
+    def step():
+        out = ops.attention(ops.layer_norm(q, w), k, v, table=table, causal=True, q_docs=ids, k_docs=ids)
+        return [out.detach(), *torch.autograd.grad(out, leaves, dy)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (1, 2):
+        with torch.no_grad():
+            for t in (q, k, v):
+                t.copy_(randn(gen(seed), *t.shape, dtype=BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in got]
+        assert all(torch.equal(a, b) for a, b in zip(replayed, step()))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_attention_on_new_threads(ops, dtype):
     # a thread whose first CUDA work is the operator, its memory from the cache
