@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
     }
   }
   constexpr int kSteps = DP / 16;
-  const int steps = (p.dim + 15) / 16;
   uint32_t q[kSteps][4];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s)
@@ -171,17 +170,22 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
     if (!__all_sync(0xffffffffu, ok)) break;
     const int k0 = k_begin + (warp + n * kWarps) * kKeys;
     const uint32_t K = ring + (n % kStages) * stage_bytes<DP>(), V = K + kOperand;
+    // columns beyond dim are zeros in q and, by the copies' fill, in K and V. Two
+    // sums of every other step: half the chain of dependent products
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    float s_odd[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
-      if (st < steps) {
-        // four 8 x 8 pieces: keys 0-7 and 8-15, dims 16 st and 16 st + 8
-        uint32_t kf[4];
-        ldsm4(K + (st / 4) * kBox + (k_place ^ ((st % 4) << 5)), kf);
-        mma16<BF16>(s[0], q[st], kf[0], kf[1]);
-        mma16<BF16>(s[1], q[st], kf[2], kf[3]);
-      }
+      // four 8 x 8 pieces: keys 0-7 and 8-15, dims 16 st and 16 st + 8
+      uint32_t kf[4];
+      ldsm4(K + (st / 4) * kBox + (k_place ^ ((st % 4) << 5)), kf);
+      mma16<BF16>(st & 1 ? s_odd[0] : s[0], q[st], kf[0], kf[1]);
+      mma16<BF16>(st & 1 ? s_odd[1] : s[1], q[st], kf[2], kf[3]);
     }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[x][e] += s_odd[x][e];
     bool masked = k0 + kKeys > k_end || kdocs;
     if (p.causal) masked = masked || k0 + kKeys > max(info.start + 1, info.prefix);
     uint32_t bad = 0;  // two bits a key: halves of its row of V that are not finite
@@ -197,31 +201,35 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
     }
     // element e of s[x]: row quad + 8 (e / 2), key k0 + 8 x + pair + e % 2
     const bool far = !p.map || (k0 - info.start - p.q_len + 1 >= D) || (k0 + kKeys - 1 - info.start <= -D);
-    const bool is_above = k0 > info.start;
+    // each choice outside its loop over the elements, so that they overlap
+    auto each = [&](auto f) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = e >> 1, key = k0 + 8 * x + pair + (e & 1), off = key - info.start - qi[r];
-        float z = s[x][e];
-        if (p.cap > 0.f) z = cap_out * tanh_from(z * cap_in);
-        else z *= c;
-        if (p.map) {
-          if (far) {
-            z += is_above ? above[r] : below[r];
-          } else {
-            const int at = __ldg(p.map + min(max(off, -D), D) + D);
-            z += kLog2e * table_value(p, (long long)at * p.heads + qh[r], BF16);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int r = e >> 1, key = k0 + 8 * x + pair + (e & 1);
+          f(s[x][e], r, key, key - info.start - qi[r]);
         }
-        if (p.slopes) z = fmaf(-slope[r], fabsf((float)off), z);
-        if (masked) {
-          bool seen = key < k_end && !(p.causal && off > 0 && key >= info.prefix);
-          if (kdocs && seen) seen = __ldg(kdocs + key) == qd[r];
-          z = seen ? z : -INFINITY;
-        }
-        s[x][e] = z;
-      }
+    };
+    if (p.cap > 0.f) each([&](float& z, int, int, int) { z = cap_out * tanh_from(z * cap_in); });
+    else each([&](float& z, int, int, int) { z *= c; });
+    if (p.map && far) {
+      const bool is_above = k0 > info.start;
+      const float add[2] = {is_above ? above[0] : below[0], is_above ? above[1] : below[1]};
+      each([&](float& z, int r, int, int) { z += add[r]; });
+    } else if (p.map) {
+      each([&](float& z, int r, int, int off) {
+        const int at = __ldg(p.map + min(max(off, -D), D) + D);
+        z += kLog2e * table_value(p, (long long)at * p.heads + qh[r], BF16);
+      });
+    }
+    if (p.slopes) each([&](float& z, int r, int, int off) { z = fmaf(-slope[r], fabsf((float)off), z); });
+    if (masked)
+      each([&](float& z, int r, int key, int off) {
+        bool seen = key < k_end && !(p.causal && off > 0 && key >= info.prefix);
+        if (kdocs && seen) seen = __ldg(kdocs + key) == qd[r];
+        z = seen ? z : -INFINITY;
+      });
     if (bad != 0) {  // a query that sees such a row (its score is not -inf) returns NaN
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -272,12 +280,10 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
                       pack2<BF16>(s[1][2], s[1][3])};
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) {
-      if (st < steps) {
-        uint32_t vf[4];
-        ldsm4_t(V + (st / 4) * kBox + (v_place ^ ((st % 4) << 5)), vf);
-        mma16<BF16>(o[2 * st], pf, vf[0], vf[1]);
-        mma16<BF16>(o[2 * st + 1], pf, vf[2], vf[3]);
-      }
+      uint32_t vf[4];
+      ldsm4_t(V + (st / 4) * kBox + (v_place ^ ((st % 4) << 5)), vf);
+      mma16<BF16>(o[2 * st], pf, vf[0], vf[1]);
+      mma16<BF16>(o[2 * st + 1], pf, vf[2], vf[3]);
     }
     __syncwarp();
     load(n + kStages);
