@@ -233,15 +233,15 @@ __global__ void __launch_bounds__(256) bwd_v_peak(const AttnParams p, float* pea
   block_peak(top, peak + b * p.kv_heads + h);
 }
 
-// Queries up to which the few-query kernel runs: one operand of 16 a head at
-// most. It takes time with its rows (queries x heads that share a key head),
-// the tiled kernel with its heads, each a tile of 256 however few queries fill
-// it. Measured, bf16, 32 rows of 3001 keys, 4 key heads of 8 heads each, head
-// size 128: 16 queries 212 us against 287, 8 queries 136 against 283, 1 query
-// 55 (at most) against 283; head size 64: 98, 54 and 33 against 233. At 16 rows
-// the few-query kernel takes 26 us a key head's tile, the tiled one 35 a head:
-// beyond about 20 queries a head it would lose.
-constexpr int kStepQueries = 16;
+// Whether the few-query kernel runs. It takes time with its rows (queries x
+// heads that share a key head, 16 an operand), the tiled kernel with its heads,
+// each a tile of 256 however few queries fill it. Measured, bf16, 32 rows of 3001
+// keys, 4 key heads of 8 heads each: head size 128, 16 queries 136 us against
+// 285, 32 queries 231 against 285; head size 64, 75 and 143 against 234. Where
+// no heads share keys, more than one operand reads the keys again, and either
+// kernel may win: 32 rows, 4 heads, 24 queries, 66 us against 46 at head size 128
+// and 43 against 37 at 64; 16 heads, 156 against 167 and 81 against 136.
+bool takes_step(const AttnParams& p) { return p.q_len <= (p.group >= 4 ? 32 : 16); }
 
 int mode_of(const AttnParams& p) {
   if (p.cap > 0.f || p.slopes || !(p.scale > 0.f)) return 2;
@@ -291,7 +291,7 @@ TcPlan tc_plan(const AttnParams& p, bool backward) {
   w.k_tiles = (p.k_len + kTile - 1) / kTile;
   w.splits = 1;
   w.split_tiles = w.k_tiles;
-  if (!backward && p.q_len <= kStepQueries) {
+  if (!backward && takes_step(p)) {
     w.step = step_plan(p);
     w.splits = w.step.splits;
   } else if (!backward) {

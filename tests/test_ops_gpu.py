@@ -295,6 +295,18 @@ def test_attention(ops, shape, option, dtype):
     check_attention(ops, q, k, v, f"{shape} {option} {dtype}", dy=dy, **kw)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("option", ["plain", "causal", "all"])
+@pytest.mark.parametrize("Tq", [15, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (3, 3)])
+def test_attention_few_queries(ops, heads, kv_heads, Tq, option, dtype):
+    # both sides of the limits of the kernel for few queries
+    shape = (2, Tq, 700, heads, kv_heads, 64)
+    q, k, v, _, g = make(shape, dtype, seed=Tq)
+    kw = dict(OPTIONS[option](shape, dtype, g), q_start=lengths(700 - Tq, 40))
+    check_attention(ops, q, k, v, f"{shape} {option} {dtype}", **kw)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("dim", [40, 64, 128])
 def test_attention_documents(ops, dtype, dim):
