@@ -14,7 +14,7 @@
 // caches of up to 3001 frames in 62 us (0.71 of the measured bandwidth), 184 MB
 // of an hour's 360001 frames in 43 (0.64), in 297 splits. What is left is the
 // chain from a tile's arrival over its two products to the next: twelve warps an
-// SM, as many as the registers hold, issue in 0.35 of the cycles.
+// SM, as many as the registers hold, issue in 0.32 of the cycles.
 #include "fm_ops_attn_tc.cuh"
 
 namespace fm {
