@@ -123,9 +123,11 @@ __device__ __forceinline__ float ds_scale(const Extra& x, int at, int count) {
   return fabsf(e) < 120.f ? exp2f(e) : 1.f;  // nothing, infinite or NaN: as it is
 }
 
-// One block's work; SCAN: of the second launch (TcParams::flags).
+// One block's work; SCAN: of the second launch, on tensor memory that its block
+// holds (held), as in the forward pass. False: a wait gave up.
 template <int DP, bool BF16, int MODE, bool KEYS, bool SCAN>
-__device__ __forceinline__ void block(const TcParams& t, const Extra& x, const dim3 at, const int index) {
+__device__ __forceinline__ bool block(const TcParams& t, const Extra& x, const dim3 at, const int index,
+                                      const uint32_t held) {
   using L = Smem<DP, KEYS>;
   extern __shared__ unsigned char raw[];
   __shared__ uint32_t tmem_slot;
@@ -172,14 +174,14 @@ __device__ __forceinline__ void block(const TcParams& t, const Extra& x, const d
     tma_prefetch(&t.vm);
     tma_prefetch(&t.gm);
   }
-  if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (!SCAN && warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
   if (has_bias && !KEYS) fill_bias(t, h0, bias_mem, tid, kThreads);
   if (grad)
     for (int i = tid; i < 2 * ndiag; i += kThreads) diag_mem[i] = 0.f;
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = SCAN ? held : tmem_slot;
   // The keys' kernel needs nothing of the queries' one: its blocks may start on
   // SMs that have no more blocks of this one.
   if (!KEYS && !SCAN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -557,6 +559,11 @@ __device__ __forceinline__ void block(const TcParams& t, const Extra& x, const d
         if (++tile == se) tile = sb, ++h;
         if (++s == x.slots) s = 0, round ^= 1;
       }
+      if (SCAN) {  // the last arrival on every slot's barrier, before their memory serves others
+        for (int it = max(n - x.slots, 0); it < n; ++it)
+          if (!bar_wait(bar(kEmpty + it % x.slots), (it / x.slots) & 1, &dead, t.err)) break;
+        __syncwarp();
+      }
     } else if (warp == 17 && n > 0) {
       // ---- products
       const uint32_t id_s = instr_desc(kTile, kCols, BF16, false), id_a = instr_desc(kTile, t.dim16, BF16, true);
@@ -641,7 +648,7 @@ __device__ __forceinline__ void block(const TcParams& t, const Extra& x, const d
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
   __syncthreads();
-  if (warp == 17) {
+  if (!SCAN && warp == 17) {
     __syncwarp();
     fence_after();
     tmem_free(tmem, 512);
@@ -649,7 +656,8 @@ __device__ __forceinline__ void block(const TcParams& t, const Extra& x, const d
   // what follows in the stream waits for this kernel: one block of it waits
   // for the queries' kernel
   if (KEYS && !SCAN && index == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (SCAN) {  // another block's work may follow
+  const bool well = !dead;
+  if (SCAN && well) {  // another block's work may follow
     if (tid == 0) {
       for (int i = 0; i < x.slots; ++i) bar_free(bar(kFull + i)), bar_free(bar(kEmpty + i));
       for (int i = kOwnFull; i < kBarCount; ++i) bar_free(bar(i));
@@ -657,20 +665,20 @@ __device__ __forceinline__ void block(const TcParams& t, const Extra& x, const d
     fence_async();
     __syncthreads();
   }
+  return well;
 }
 
 template <int DP, bool BF16, int MODE, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t,
                                                       const __grid_constant__ Extra x) {
-  block<DP, BF16, MODE, KEYS, false>(t, x, blockIdx, (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
+  block<DP, BF16, MODE, KEYS, false>(t, x, blockIdx, (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x, 0);
 }
 template <int DP, bool BF16, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1) scan_kernel(const __grid_constant__ TcParams t,
                                                            const __grid_constant__ Extra x) {
-  for (int i = blockIdx.x; i < t.blocks[0] * t.blocks[1] * t.blocks[2]; i += gridDim.x)
-    if (t.flags[i])
-      block<DP, BF16, 2, KEYS, true>(
-          t, x, dim3(i % t.blocks[0], i / t.blocks[0] % t.blocks[1], i / t.blocks[0] / t.blocks[1]), i);
+  scan_blocks(t, [&](const dim3 at, int index, uint32_t tmem) {
+    return block<DP, BF16, 2, KEYS, true>(t, x, at, index, tmem);
+  });
 }
 
 template <int DP, bool BF16, bool KEYS>

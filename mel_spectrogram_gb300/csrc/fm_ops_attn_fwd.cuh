@@ -77,9 +77,11 @@ __device__ __forceinline__ bool pair_ok(int pair, bool ok) {
   return r != 0;
 }
 
-// One block's work; SCAN: of the second launch (TcParams::flags).
+// One block's work; SCAN: of the second launch (TcParams::flags), whose blocks
+// run several of these one after another, on tensor memory that they hold from
+// the first to the last (held). False: a wait gave up.
 template <int DP, bool BF16, int MODE, bool SCAN>
-__device__ __forceinline__ void block(const TcParams& t, const dim3 at, const int index) {
+__device__ __forceinline__ bool block(const TcParams& t, const dim3 at, const int index, const uint32_t held) {
   using L = Smem<DP>;
   extern __shared__ unsigned char raw[];
   __shared__ uint32_t tmem_slot;
@@ -115,12 +117,12 @@ __device__ __forceinline__ void block(const TcParams& t, const dim3 at, const in
     tma_prefetch(&t.km);
     tma_prefetch(&t.vm);
   }
-  if (warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (!SCAN && warp == 17) tmem_alloc(smem_u32(&tmem_slot), 512);
   if (MODE == 1 || (MODE == 2 && p.map)) fill_bias(t, h, bias, tid, kThreads);
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = SCAN ? held : tmem_slot;
 
   // the key tiles this block visits
   int tb = split * t.split_tiles, te = (key_end(p, info, q0, nq) + kTile - 1) / kTile;
@@ -318,6 +320,8 @@ __device__ __forceinline__ void block(const TcParams& t, const dim3 at, const in
     }
     // ---- the row's result, half of its columns a thread
     if (n > 0) ok = bar_wait(bar(kOFull + w), 0, &dead, t.err) && ok;
+    // the last arrival on every barrier, before their memory serves others
+    if (SCAN && NB == 3 && n > 0) ok = bar_wait(bar(kOReady + w), (n - 1) & 1, &dead, t.err) && ok;
     row_stat[n & 1][w][half][lane_row] = l;
     ok = pair_ok(pair, ok);
     if (ok) {
@@ -423,6 +427,11 @@ __device__ __forceinline__ void block(const TcParams& t, const dim3 at, const in
         }
         __syncwarp();
       }
+      if (SCAN) {  // the last arrival on every slot's barrier
+        for (int it = max(2 * n - L::kSlots, 0); it < 2 * n; ++it)
+          if (!bar_wait(bar(kEmpty + it % L::kSlots), (it / L::kSlots) & 1, &dead, t.err)) break;
+        __syncwarp();
+      }
     } else if (warp == 17 && n > 0) {
       // ---- products
       const uint32_t id_s = instr_desc(kTile, kTile, BF16, false), id_o = instr_desc(kTile, t.dim16, BF16, true);
@@ -492,12 +501,13 @@ __device__ __forceinline__ void block(const TcParams& t, const dim3 at, const in
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   }
   __syncthreads();
-  if (warp == 17) {
+  if (!SCAN && warp == 17) {
     __syncwarp();
     fence_after();
     tmem_free(tmem, 512);
   }
-  if (SCAN) {  // another block's work may follow
+  const bool well = !dead;
+  if (SCAN && well) {  // another block's work may follow
     if (tid == 0) {
       for (int i = 0; i < L::kSlots; ++i) bar_free(bar(kFull + i)), bar_free(bar(kEmpty + i));
       for (int i = kQFull; i < kBarCount; ++i) bar_free(bar(i));
@@ -505,17 +515,18 @@ __device__ __forceinline__ void block(const TcParams& t, const dim3 at, const in
     fence_async();
     __syncthreads();
   }
+  return well;
 }
 
 template <int DP, bool BF16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) kernel(const __grid_constant__ TcParams t) {
-  block<DP, BF16, MODE, false>(t, blockIdx, (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
+  block<DP, BF16, MODE, false>(t, blockIdx, (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x, 0);
 }
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) scan_kernel(const __grid_constant__ TcParams t) {
-  for (int i = blockIdx.x; i < t.blocks[0] * t.blocks[1] * t.blocks[2]; i += gridDim.x)
-    if (t.flags[i])
-      block<DP, BF16, 2, true>(t, dim3(i % t.blocks[0], i / t.blocks[0] % t.blocks[1], i / t.blocks[0] / t.blocks[1]), i);
+  scan_blocks(t, [&](const dim3 at, int index, uint32_t tmem) {
+    return block<DP, BF16, 2, true>(t, at, index, tmem);
+  });
 }
 
 template <int DP, bool BF16>

@@ -268,6 +268,39 @@ __device__ __forceinline__ bool clean_row(unsigned char* row, int box, int first
   return bad;
 }
 
+// The second launch (TcParams::flags): this block's share of the flagged blocks'
+// work, one after another, work(place in the grid, index, tensor memory). A
+// block may allocate tensor memory only once, and nearly all have nothing to
+// do: the first flagged one allocates, after the last it is freed. Ends early
+// where a wait gave up, whose products and copies may still be under way.
+template <typename Work>
+__device__ __forceinline__ void scan_blocks(const TcParams& t, Work work) {
+  using namespace tc;
+  __shared__ uint32_t slot;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), x = t.blocks[0], y = t.blocks[1];
+  uint32_t tmem = 0;
+  bool held = false;
+  for (int i = blockIdx.x; i < x * y * t.blocks[2]; i += gridDim.x) {
+    if (!t.flags[i]) continue;  // the same for the whole block
+    if (!held) {
+      if (warp == 17) tmem_alloc(smem_u32(&slot), 512);
+      fence_before();
+      __syncthreads();
+      fence_after();
+      tmem = slot;
+      held = true;
+    }
+    if (!work(dim3(i % x, i / x % y, i / x / y), i, tmem)) break;
+  }
+  if (!held) return;
+  __syncthreads();
+  if (warp == 17) {
+    __syncwarp();
+    fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
 // Bits of the N columns whose document is this row's. ids: the columns'
 // documents, `there` of them exist; own: the row's (-2: none matches). A warp
 // goes through the distinct ids of the tile, usually one or two.

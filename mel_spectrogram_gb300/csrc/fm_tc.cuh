@@ -85,6 +85,7 @@ __device__ __forceinline__ void fence_bar_init() {
 }
 
 // ---- tensor memory ----------------------------------------------------------
+// once in a block's life: after giving the permit up it may allocate no more
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");

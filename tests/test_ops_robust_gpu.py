@@ -1,0 +1,72 @@
+"""The frame-encoder operators where calls are easily answered wrongly: many
+broken rows at once, large caps, inputs changed between the passes, second
+derivatives, first uses inside a recording, waits that give up."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from tests import ops_reference as ref
+from tests import test_ops_gpu as base
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = base.F32, base.F16, base.BF16
+TYPES = base.TYPES
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from mel_spectrogram_gb300 import ops
+
+    return ops
+
+
+def passes(ops, q, k, v, dy, **kw):
+    """The output and the gradients of q, k, v (and a table)."""
+    leaves = [t.detach().requires_grad_() for t in (q, k, v)]
+    if kw.get("table") is not None:
+        kw["table"] = kw["table"].detach().requires_grad_()
+        leaves.append(kw["table"])
+    out = ops.attention(*leaves[:3], **kw)
+    return [out.detach(), *torch.autograd.grad(out, leaves, dy)]
+
+
+# ---------------------------------------------------------------------------
+# more tiles with results that are not finite than there are SMs: a block of
+# the second launch works on several of them in turn
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_broken_tiles(ops, dtype, dim):
+    B, T = 80, 200  # 320 blocks forward, 640 and 320 backward
+    q, k, v, dy, _ = base.make((B, T, T, 4, 2, dim), dtype)
+    ids = base.docs_of(T, *[[(0, 90), (1, 70), (2, 40)]] * B)
+    clean = passes(ops, q, k, v, dy, q_docs=ids, k_docs=ids)
+    broken = [t.clone() for t in (q, k, v, dy)]
+    for t in broken:
+        t[:, 90:160, :, 3] = math.inf
+    again = []
+    for _ in range(2):
+        got = passes(ops, *broken, q_docs=ids, k_docs=ids)
+        again.append(got)
+        for g, want in zip(got, clean):
+            # f16's dS has another power of two without the broken recording
+            for part in (slice(0, 90), slice(160, T)):
+                room = 2 * ref.U[dtype] * want[:, part].abs().max()
+                assert ((g[:, part] - want[:, part]).abs() <= room).all()
+            assert not torch.isfinite(g[:, 90:160]).all()
+        assert torch.equal(got[0][:, :90], clean[0][:, :90]) and torch.equal(got[0][:, 160:], clean[0][:, 160:])
+    for a, b in zip(*again):
+        assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+    # causal: every row's last keys are broken
+    clean = passes(ops, q, k, v, dy, causal=True)
+    v2 = v.clone()
+    v2[:, 150:] = math.nan
+    got = passes(ops, q, k, v2, dy, causal=True)
+    assert torch.equal(got[0][:, :150], clean[0][:, :150]) and got[0][:, 150:].isnan().all()
+    room = 2 * ref.U[dtype] * clean[1][:, :150].abs().max()
+    assert ((got[1][:, :150] - clean[1][:, :150]).abs() <= room).all()
+    assert ops.poll_error() == 0
