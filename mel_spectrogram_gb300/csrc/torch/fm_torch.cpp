@@ -9,6 +9,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -73,13 +74,20 @@ Maybe maybe(const Tensor& t) { return t.defined() ? Maybe(t) : Maybe(); }
 Tensor or_none(const Maybe& t) { return t ? *t : Tensor(); }
 bool wants_grad(const Tensor& t) { return t.defined() && t.requires_grad(); }
 
-// what a backward pass returns where the caller asked for a graph of it: the
-// gradients, and an error in place of their own gradients
-variable_list once(variable_list out, const char* name) {
-  if (!at::GradMode::is_enabled()) return out;
-  auto err = std::make_shared<torch::autograd::DelayedError>(
-      std::string(name) + ": its gradient is differentiable once, no second gradient is built", out.size());
-  return (*err)(std::move(out));
+// What a backward pass returns where the caller asked for a graph of it: the
+// gradients, whose own history is an error that leads to everything they were
+// made `from`, so that whoever derives through them to one of those meets it.
+template <typename... From>
+variable_list once(variable_list out, const char* name, const From&... from) {
+  using namespace torch::autograd;
+  if (!compute_requires_grad(from...)) return out;  // also where no graph is wanted
+  const std::shared_ptr<Node> error(
+      new Error(std::string(name) + ": its gradient is differentiable once, no second gradient is built",
+                collect_next_edges(from...)),
+      deleteNode);
+  for (Tensor& t : out)
+    if (t.defined()) set_history(t, error);
+  return out;
 }
 
 // ---- layer norm ---------------------------------------------------------------
@@ -157,7 +165,7 @@ struct NormNode : torch::autograd::Function<NormNode> {
       }
       run(fm_layer_norm_backward(&a, on.stream), "fm_layer_norm_backward");
     }
-    return once({dx, dw, db, Tensor()}, "layer_norm");
+    return once({dx, dw, db, Tensor()}, "layer_norm", grads[0], x, weight);
   }
 };
 
@@ -246,7 +254,8 @@ struct BiasNode : torch::autograd::Function<BiasNode> {
       OnDevice on(dout);
       run(fm_relative_bias_backward(&a, on.stream), "fm_relative_bias_backward");
     }
-    return once({dtable, Tensor(), Tensor(), Tensor(), Tensor()}, "relative_bias");
+    // linear in the gradient that came in, whatever the table holds
+    return once({dtable, Tensor(), Tensor(), Tensor(), Tensor()}, "relative_bias", grads[0]);
   }
 };
 
@@ -370,7 +379,7 @@ struct AttentionNode : torch::autograd::Function<AttentionNode> {
       workspace_for(a, 1, q, work);
       run(fm_attention_backward(&a, on.stream), "fm_attention_backward");
     }
-    return once({dq, dk, dv, dtable, Tensor()}, "attention");
+    return once({dq, dk, dv, dtable, Tensor()}, "attention", grads[0], q, k, v, table);
   }
 };
 

@@ -70,3 +70,29 @@ def test_many_broken_tiles(ops, dtype, dim):
     room = 2 * ref.U[dtype] * clean[1][:, :150].abs().max()
     assert ((got[1][:, :150] - clean[1][:, :150]).abs() <= room).all()
     assert ops.poll_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# second derivatives are refused, not dropped
+
+def test_second_derivatives(ops):
+    q, k, v, _, g = base.make((1, 6, 6, 2, 1, 16), F32)
+    x, w = base.randn(g, 5, 16), base.randn(g, 16)
+    table = base.randn(g, 8, 2)
+    calls = [(lambda x, w: ops.layer_norm(x, w), (x, w)),
+             (lambda t: ops.relative_bias(t, 4, 5, max_distance=16), (table,)),
+             (lambda q, k, v, t: ops.attention(q, k, v, table=t, max_distance=16), (q, k, v, table))]
+    for call, inputs in calls:
+        leaves = [t.clone().requires_grad_() for t in inputs]
+        first = torch.autograd.grad(call(*leaves).square().sum(), leaves, create_graph=True)
+        for d in first:
+            assert d.requires_grad
+            # beside a term that has a derivative, as in a gradient penalty
+            with pytest.raises(RuntimeError, match="differentiable once"):
+                torch.autograd.grad(d.square().sum() + leaves[0].square().sum(), leaves, retain_graph=True,
+                                    allow_unused=True)
+    # the bias's gradient does not depend on the table: a constant where the gradient given is one
+    leaf = table.clone().requires_grad_()
+    (d,) = torch.autograd.grad(ops.relative_bias(leaf, 4, 5, max_distance=16).sum(), leaf, create_graph=True)
+    (second,) = torch.autograd.grad((d * leaf).sum(), leaf)
+    assert torch.equal(second, d)
