@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
   for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   bool ok = true;
-  const float cap_in = p.cap > 0.f ? 2.f * kLog2e * p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
+  const float cap_in = p.cap > 0.f ? p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
   // this lane's places in a tile: rows of 128 bytes with TMA's swizzle, whose
   // pieces 2 st + x stand at (x ^ row % 8) ^ 2 st (64 columns further: next box)
   const int k_row = (lane & 7) + ((lane & 16) >> 1), v_row = lane & 15;
@@ -213,8 +213,19 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
           f(s[x][e], r, key, key - info.start - qi[r]);
         }
     };
-    if (p.cap > 0.f) each([&](float& z, int, int, int) { z = cap_out * tanh_from(z * cap_in); });
-    else each([&](float& z, int, int, int) { z *= c; });
+    if (p.cap > 0.f) {
+      // each score takes the form of tanh that its own size asks for
+      float most = 0.f;
+      each([&](float& z, int, int, int) { most = fmaxf(most, fabsf(z)); });
+      const bool large = __any_sync(0xffffffffu, most * fabsf(cap_in) > kTanhSmall);
+      each([&](float& z, int, int, int) {
+        const float x = z * cap_in, q = x * x;
+        const float t = fmaf(fmaf(fmaf(tanh_over_x(3), q, tanh_over_x(2)), q, tanh_over_x(1)), q, tanh_over_x(0)) * (z * c);
+        z = large && fabsf(x) > kTanhSmall ? cap_out * tanh_from(x * (2.f * kLog2e)) : t;
+      });
+    } else {
+      each([&](float& z, int, int, int) { z *= c; });
+    }
     if (p.map && far) {
       const bool is_above = k0 > info.start;
       const float add[2] = {is_above ? above[0] : below[0], is_above ? above[1] : below[1]};

@@ -116,10 +116,11 @@ __device__ __forceinline__ void write_rows(const unsigned char* stage, int first
 // where REV. CAP_SLOPE: also 1 - tanh^2, the cap's derivative, into slope.
 //
 // tanh: where every score of the warp's rows is small against the cap
-// (|x| <= 0.4, the usual case) tanh(x) / x is a polynomial of degree 3 in x^2,
-// fitted for the least relative error there (1e-7): three multiply-adds
-// instead of two trips to the special-function unit, which the weights' 2^z
-// needs.
+// (kTanhSmall, the usual case) the polynomial alone: four multiply-adds and two
+// products instead of two trips to the special-function unit, which the
+// weights' 2^z needs. Elsewhere each score takes the form that its own size
+// asks for, so that its value does not depend on its neighbours', which may be
+// hidden from it.
 template <int N, int MODE, bool REV, bool CAP_SLOPE>
 __device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SLOPE ? N : 1], const AttnParams& p,
                                             float c, const float* bias, float slope2, int o0) {
@@ -144,21 +145,21 @@ __device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SL
     const float2 g2 = both(REV ? -g : g), base = both(linear ? g * (float)o0 : 0.f);
     if (p.cap > 0.f) {
       const float k = p.scale / p.cap, out = p.cap * kLog2e;
-      const float2 in = both(1.f / out);
+      const float2 in = both(1.f / out), k2 = both(k);
       float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < N; ++j) top[j & 3] = fmaxf(top[j & 3], fabsf(s[j]));
       const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      const bool small = __all_sync(0xffffffffu, most * fabsf(k) <= 0.4f);
-      const float tanh_over_x[4] = {0.999999902f, -0.333313625f, 0.132709768f, -0.0475536036f};
-      const float k2 = k * k;
+      const bool small = __all_sync(0xffffffffu, most * fabsf(k) <= kTanhSmall);
+      // of the polynomial, times what takes a raw product to base 2 (k's powers
+      // in them would leave the range of floats at large and at tiny caps)
       float2 a[4];
-      float power = out * k;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = both(tanh_over_x[i] * power);
-        power *= k2;
-      }
+      for (int i = 0; i < 4; ++i) a[i] = both(tanh_over_x(i) * c);
+      auto polynomial = [&](float2 x) {
+        const float2 y = mul2(x, k2), q = mul2(y, y);
+        return mul2(fma2(fma2(fma2(a[3], q, a[2]), q, a[1]), q, a[0]), x);
+      };
       auto finish = [&](int j, float2 t) {
         if (CAP_SLOPE) {
           const float2 th = mul2(t, in), f = fma2(make_float2(-th.x, -th.y), th, both(1.f));
@@ -173,15 +174,17 @@ __device__ __forceinline__ void tile_scores(float (&s)[N], float (&slope)[CAP_SL
       // chains of multiply-adds from overlapping (four times slower)
       if (small) {
 #pragma unroll
-        for (int j = 0; j < N; j += 2) {
-          const float2 x = make_float2(s[j], s[j + 1]), q = mul2(x, x);
-          finish(j, mul2(fma2(fma2(fma2(a[3], q, a[2]), q, a[1]), q, a[0]), x));
-        }
+        for (int j = 0; j < N; j += 2) finish(j, polynomial(make_float2(s[j], s[j + 1])));
       } else {
         const float c2 = 2.f * kLog2e * k;
 #pragma unroll
-        for (int j = 0; j < N; j += 2)
-          finish(j, make_float2(out * tanh_from(s[j] * c2), out * tanh_from(s[j + 1] * c2)));
+        for (int j = 0; j < N; j += 2) {
+          const float2 x = make_float2(s[j], s[j + 1]);
+          float2 t = polynomial(x);
+          if (fabsf(x.x * k) > kTanhSmall) t.x = out * tanh_from(x.x * c2);
+          if (fabsf(x.y * k) > kTanhSmall) t.y = out * tanh_from(x.y * c2);
+          finish(j, t);
+        }
       }
     } else {
 #pragma unroll

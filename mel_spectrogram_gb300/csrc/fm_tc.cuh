@@ -210,9 +210,18 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh(x) = 1 - 2 / (e^2x + 1); k2 = 2 log2(e), folded into x by the caller:
-// x2 = 2 log2(e) x. Saturates cleanly at both ends.
+// tanh(x) = 1 - 2 / (e^2x + 1) from x2 = 2 log2(e) x. Saturates cleanly at both
+// ends, but its error is absolute (about 2^-22): times a large cap it would
+// swamp the scores far below the cap. So it is for |x| > kTanhSmall only, where
+// tanh(x) is large enough for it.
 __device__ __forceinline__ float tanh_from(float x2) { return fmaf(-2.f, rcp(ex2(x2) + 1.f), 1.f); }
+// Below that, tanh(x) / x is a polynomial of degree 3 in x^2, fitted for the
+// least relative error there (1e-7).
+constexpr float kTanhSmall = 0.4f;
+__device__ __forceinline__ float tanh_over_x(int i) {
+  constexpr float a[4] = {0.999999902f, -0.333313625f, 0.132709768f, -0.0475536036f};
+  return a[i];
+}
 
 // pairs of 32-bit floats in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {

@@ -96,3 +96,26 @@ def test_second_derivatives(ops):
     (d,) = torch.autograd.grad(ops.relative_bias(leaf, 4, 5, max_distance=16).sum(), leaf, create_graph=True)
     (second,) = torch.autograd.grad((d * leaf).sum(), leaf)
     assert torch.equal(second, d)
+
+
+# ---------------------------------------------------------------------------
+# caps far above the scores, and scores on both sides of them
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("softcap", [200.0, 1e4, 1e6, 1e8, 1e30])
+@pytest.mark.parametrize("Tq", [1, 4, 16, 129])
+def test_large_caps(ops, Tq, softcap, dtype):
+    q, k, v, dy, _ = base.make((2, Tq, 150, 4, 2, 64), dtype)
+    base.check_attention(ops, q, k, v, f"cap {softcap}", softcap=softcap, scale=0.5)
+    base.check_attention(ops, q, k, v, f"cap {softcap}", dy=dy, softcap=softcap, scale=0.5)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("softcap", [30.0, 1e4])
+@pytest.mark.parametrize("Tq", [3, 129])
+def test_caps_between_rows(ops, Tq, softcap, dtype):
+    # one query whose scores reach the cap beside others far below it
+    q, k, v, dy, _ = base.make((1, Tq, 150, 2, 2, 64), dtype)
+    q[:, 1] *= softcap / 8
+    base.check_attention(ops, q, k, v, f"cap {softcap}", softcap=softcap)
+    base.check_attention(ops, q, k, v, f"cap {softcap}", dy=dy, softcap=softcap)
