@@ -271,20 +271,23 @@ Tensor relative_bias(Tensor table, int64_t q_len, int64_t k_len, int64_t q_start
 }
 
 // ---- attention ------------------------------------------------------------------
-// What one call's passes share besides q, k, v and the table. The masks stay
-// alive until the backward pass has read them.
+// What one call's passes share besides q, k, v and the table.
 struct Call : torch::CustomClassHolder {
   double scale, softcap;
   bool causal;
   int64_t start_all;
   const fm_buckets* buckets = nullptr;
+};
+// The masks and slopes: like q, k and v saved for the backward pass, which
+// would otherwise answer for what has been written over them since.
+struct Masks {
   Tensor slopes, q_docs, k_docs, k_lens, q_start, prefix;
 };
 
 void set_strides(int64_t (&to)[3], const Tensor& t) { to[0] = t.stride(0), to[1] = t.stride(1), to[2] = t.stride(2); }
 
-fm_attention_args attention_args(const Call& c, const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& out,
-                                 const Tensor& rest, const Tensor& lse, const Tensor& table) {
+fm_attention_args attention_args(const Call& c, const Masks& m, const Tensor& q, const Tensor& k, const Tensor& v,
+                                 const Tensor& out, const Tensor& rest, const Tensor& lse, const Tensor& table) {
   fm_attention_args a{};
   a.batch = q.size(0), a.q_len = q.size(1), a.k_len = k.size(1);
   a.heads = q.size(2), a.kv_heads = k.size(2), a.dim = q.size(3);
@@ -298,13 +301,13 @@ fm_attention_args attention_args(const Call& c, const Tensor& q, const Tensor& k
   set_strides(a.out_s, out);
   a.lse = (float*)mut(lse);
   a.out_rest = mut(rest);
-  a.q_docs = (const int32_t*)ptr(c.q_docs), a.k_docs = (const int32_t*)ptr(c.k_docs);
-  a.k_lens = (const int32_t*)ptr(c.k_lens), a.q_start = (const int32_t*)ptr(c.q_start);
-  a.prefix = (const int32_t*)ptr(c.prefix);
+  a.q_docs = (const int32_t*)ptr(m.q_docs), a.k_docs = (const int32_t*)ptr(m.k_docs);
+  a.k_lens = (const int32_t*)ptr(m.k_lens), a.q_start = (const int32_t*)ptr(m.q_start);
+  a.prefix = (const int32_t*)ptr(m.prefix);
   a.q_start_all = c.start_all;
   a.buckets = c.buckets;
   if (table.defined()) a.table = ptr(table), a.table_dtype = type_of(table, "table");
-  a.slopes = (const float*)ptr(c.slopes);
+  a.slopes = (const float*)ptr(m.slopes);
   return a;
 }
 
@@ -318,14 +321,15 @@ void workspace_for(fm_attention_args& a, int backward, const Tensor& like, Tenso
 
 // rest: what rounding took from the output (16-bit types, where a backward
 // pass will want its exact product with the gradient)
-std::tuple<Tensor, Tensor, Tensor> attention_forward(const Call& c, const Tensor& q, const Tensor& k, const Tensor& v,
-                                                     const Tensor& table, bool want_lse, bool want_rest) {
+std::tuple<Tensor, Tensor, Tensor> attention_forward(const Call& c, const Masks& m, const Tensor& q, const Tensor& k,
+                                                     const Tensor& v, const Tensor& table, bool want_lse,
+                                                     bool want_rest) {
   const auto options = q.options().requires_grad(false);
   Tensor out = at::empty(q.sizes(), options.memory_format(at::MemoryFormat::Contiguous)), rest, lse;
   if (want_rest && q.scalar_type() != at::kFloat)
     rest = at::empty(q.sizes(), options.memory_format(at::MemoryFormat::Contiguous));
   if (want_lse) lse = at::empty({q.size(0), q.size(2), q.size(1)}, options.dtype(at::kFloat));
-  fm_attention_args a = attention_args(c, q, k, v, out, rest, lse, table);
+  fm_attention_args a = attention_args(c, m, q, k, v, out, rest, lse, table);
   OnDevice on(q);
   Tensor work;
   workspace_for(a, 0, q, work);
@@ -344,18 +348,20 @@ Tensor gradient_rows(const Tensor& t) {
 
 struct AttentionNode : torch::autograd::Function<AttentionNode> {
   static variable_list forward(AutogradContext* ctx, const Tensor& q, const Tensor& k, const Tensor& v,
-                               const Maybe& maybe_table, const c10::intrusive_ptr<Call>& c) {
+                               const Maybe& maybe_table, const c10::intrusive_ptr<Call>& c, const Masks& m) {
     const Tensor table = or_none(maybe_table);
-    auto [out, rest, lse] = attention_forward(*c, q, k, v, table, true, true);
-    ctx->save_for_backward({q, k, v, table, out, rest, lse});
+    auto [out, rest, lse] = attention_forward(*c, m, q, k, v, table, true, true);
+    ctx->save_for_backward({q, k, v, table, out, rest, lse, m.slopes, m.q_docs, m.k_docs, m.k_lens, m.q_start,
+                            m.prefix});
     ctx->saved_data["call"] = c10::IValue::make_capsule(c);
     ctx->mark_non_differentiable({lse});
     ctx->set_materialize_grads(false);
     return {out, lse};
   }
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
-    if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
+    if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()};
     const auto saved = ctx->get_saved_variables();
+    const Masks m{saved[7], saved[8], saved[9], saved[10], saved[11], saved[12]};
     const Tensor &q = saved[0], &k = saved[1], &v = saved[2], &table = saved[3];
     const auto capsule = ctx->saved_data["call"].toCapsule();
     const Call& c = *static_cast<Call*>(capsule.get());
@@ -368,7 +374,7 @@ struct AttentionNode : torch::autograd::Function<AttentionNode> {
       dk = at::empty(k.sizes(), dense);
       dv = at::empty(v.sizes(), dense);
       if (table.defined() && ctx->needs_input_grad(3)) dtable = at::empty(table.sizes(), table.options().requires_grad(false));
-      fm_attention_args a = attention_args(c, q, k, v, saved[4], saved[5], saved[6], table);
+      fm_attention_args a = attention_args(c, m, q, k, v, saved[4], saved[5], saved[6], table);
       a.dout = ptr(dout), a.dq = mut(dq), a.dk = mut(dk), a.dv = mut(dv), a.dtable = mut(dtable);
       set_strides(a.dout_s, dout);
       set_strides(a.dq_s, dq);
@@ -379,7 +385,7 @@ struct AttentionNode : torch::autograd::Function<AttentionNode> {
       workspace_for(a, 1, q, work);
       run(fm_attention_backward(&a, on.stream), "fm_attention_backward");
     }
-    return once({dq, dk, dv, dtable, Tensor()}, "attention", grads[0], q, k, v, table);
+    return once({dq, dk, dv, dtable, Tensor(), Tensor()}, "attention", grads[0], q, k, v, table);
   }
 };
 
@@ -392,12 +398,12 @@ Tensor int32_of(const Tensor& t, const char* name, at::IntArrayRef shape, const 
 }
 
 std::tuple<Tensor, Tensor> attention(Tensor q, Tensor k, Tensor v, Tensor table, const c10::intrusive_ptr<Call>& c,
-                                     int64_t far, bool both, bool want_lse) {
+                                     Masks m, int64_t far, bool both, bool want_lse) {
   TORCH_CHECK_VALUE(q.is_cuda(), "q must be a CUDA tensor (the operators run only on the GPU)");
   need_cuda(k, "k", q);
   need_cuda(v, "v", q);
   need_cuda(table, "table", q);
-  need_cuda(c->slopes, "slopes", q);
+  need_cuda(m.slopes, "slopes", q);
   type_of(q, "q");
   TORCH_CHECK_TYPE(k.scalar_type() == q.scalar_type() && v.scalar_type() == q.scalar_type(),
                    "q, k and v need one dtype, got ", q.scalar_type(), ", ", k.scalar_type(), ", ", v.scalar_type());
@@ -411,19 +417,19 @@ std::tuple<Tensor, Tensor> attention(Tensor q, Tensor k, Tensor v, Tensor table,
   if (std::isnan(c->scale)) c->scale = 1.0 / std::sqrt((double)D);
   TORCH_CHECK_VALUE(std::isfinite(c->scale) && c->softcap >= 0 && std::isfinite(c->softcap),
                     "scale must be finite, softcap finite and not negative");
-  TORCH_CHECK_VALUE(!c->prefix.defined() || c->causal, "prefix needs causal=True");
-  TORCH_CHECK_VALUE(c->q_docs.defined() == c->k_docs.defined(), "q_docs and k_docs go together");
-  c->q_docs = int32_of(c->q_docs, "q_docs", {B, Tq}, q);
-  c->k_docs = int32_of(c->k_docs, "k_docs", {B, Tk}, q);
-  c->k_lens = int32_of(c->k_lens, "k_lens", {B}, q);
-  c->prefix = int32_of(c->prefix, "prefix", {B}, q);
-  c->q_start = int32_of(c->q_start, "q_start", {B}, q);
+  TORCH_CHECK_VALUE(!m.prefix.defined() || c->causal, "prefix needs causal=True");
+  TORCH_CHECK_VALUE(m.q_docs.defined() == m.k_docs.defined(), "q_docs and k_docs go together");
+  m.q_docs = int32_of(m.q_docs, "q_docs", {B, Tq}, q);
+  m.k_docs = int32_of(m.k_docs, "k_docs", {B, Tk}, q);
+  m.k_lens = int32_of(m.k_lens, "k_lens", {B}, q);
+  m.prefix = int32_of(m.prefix, "prefix", {B}, q);
+  m.q_start = int32_of(m.q_start, "q_start", {B}, q);
   const bool grad = at::GradMode::is_enabled();
-  if (c->slopes.defined()) {
-    TORCH_CHECK_VALUE(c->slopes.scalar_type() == at::kFloat && c->slopes.dim() == 1 && c->slopes.size(0) == H,
+  if (m.slopes.defined()) {
+    TORCH_CHECK_VALUE(m.slopes.scalar_type() == at::kFloat && m.slopes.dim() == 1 && m.slopes.size(0) == H,
                       "slopes must be float32 of shape (", H, ",)");
-    TORCH_CHECK(!(grad && c->slopes.requires_grad()), "slopes are constants: no gradient is computed for them");
-    c->slopes = c->slopes.contiguous();
+    TORCH_CHECK(!(grad && m.slopes.requires_grad()), "slopes are constants: no gradient is computed for them");
+    m.slopes = m.slopes.contiguous();
   }
   if (table.defined()) {
     check_table(table);
@@ -440,10 +446,10 @@ std::tuple<Tensor, Tensor> attention(Tensor q, Tensor k, Tensor v, Tensor table,
   rows(k);
   rows(v);
   if (grad && (wants_grad(q) || wants_grad(k) || wants_grad(v) || wants_grad(table))) {
-    auto r = AttentionNode::apply(q, k, v, maybe(table), c);
+    auto r = AttentionNode::apply(q, k, v, maybe(table), c, m);
     return {r[0], r[1]};
   }
-  auto [out, rest, lse] = attention_forward(*c, q, k, v, table, want_lse, false);
+  auto [out, rest, lse] = attention_forward(*c, m, q, k, v, table, want_lse, false);
   return {out, lse};
 }
 
@@ -526,26 +532,27 @@ PyObject* py_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     count_args(n, 16);
     const Tensor q = tensor_arg(v[0], "q", false), k = tensor_arg(v[1], "k", false), w = tensor_arg(v[2], "v", false);
     auto c = c10::make_intrusive<Call>();
+    Masks m;
     c->scale = v[3] == Py_None ? NAN : real_arg(v[3]);
     TORCH_CHECK_VALUE(v[3] == Py_None || std::isfinite(c->scale), "scale must be finite");
     c->causal = PyObject_IsTrue(v[4]);
-    c->prefix = tensor_arg(v[5], "prefix", true);
+    m.prefix = tensor_arg(v[5], "prefix", true);
     c->softcap = real_arg(v[6]);
     const Tensor table = tensor_arg(v[7], "table", true);
     const int64_t far = whole_arg(v[8]);
     const bool both = PyObject_IsTrue(v[9]), want_lse = PyObject_IsTrue(v[15]);
-    c->slopes = tensor_arg(v[10], "slopes", true);
-    c->q_docs = tensor_arg(v[11], "q_docs", true);
-    c->k_docs = tensor_arg(v[12], "k_docs", true);
-    c->k_lens = tensor_arg(v[13], "k_lens", true);
+    m.slopes = tensor_arg(v[10], "slopes", true);
+    m.q_docs = tensor_arg(v[11], "q_docs", true);
+    m.k_docs = tensor_arg(v[12], "k_docs", true);
+    m.k_lens = tensor_arg(v[13], "k_lens", true);
     c->start_all = FM_Q_START_END;
-    if (THPVariable_Check(v[14])) c->q_start = THPVariable_Unpack(v[14]);
+    if (THPVariable_Check(v[14])) m.q_start = THPVariable_Unpack(v[14]);
     else if (v[14] != Py_None)
       c->start_all = std::max<int64_t>(-((int64_t)1 << 40), std::min<int64_t>((int64_t)1 << 40, whole_arg(v[14])));
     Tensor out, lse;
     {
       NoGil free;
-      std::tie(out, lse) = attention(q, k, w, table, c, far, both, want_lse);
+      std::tie(out, lse) = attention(q, k, w, table, c, m, far, both, want_lse);
     }
     if (!want_lse) return THPVariable_Wrap(out);
     PyObject *a = THPVariable_Wrap(out), *b = THPVariable_Wrap(lse);

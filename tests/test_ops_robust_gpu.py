@@ -119,3 +119,22 @@ def test_caps_between_rows(ops, Tq, softcap, dtype):
     q[:, 1] *= softcap / 8
     base.check_attention(ops, q, k, v, f"cap {softcap}", softcap=softcap)
     base.check_attention(ops, q, k, v, f"cap {softcap}", dy=dy, softcap=softcap)
+
+
+# ---------------------------------------------------------------------------
+# masks and slopes changed between the passes
+
+def test_changed_masks_are_noticed(ops):
+    q, k, v, dy, g = base.make((2, 20, 20, 2, 2, 64), BF16)
+    ids = base.docs_of(20, [(0, 20)], [(0, 12), (1, 8)])
+    extra = {"q_docs": ids, "k_docs": ids.clone(), "k_lens": base.lengths(20, 15), "q_start": base.lengths(0, 1),
+             "prefix": base.lengths(3, 4), "slopes": torch.rand(2, device="cuda", generator=g)}
+    for name in extra:
+        kw = {n: t.clone() for n, t in extra.items()}
+        leaves = [t.detach().requires_grad_() for t in (q, k, v)]
+        out = ops.attention(*leaves, causal=True, **kw)
+        want = torch.autograd.grad(out, leaves, dy, retain_graph=True)
+        kw[name].add_(1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            torch.autograd.grad(out, leaves, dy)
+        del out, want
