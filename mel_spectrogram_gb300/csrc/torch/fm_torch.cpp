@@ -3,6 +3,7 @@
 // of fm_ops.h. In C++ because the smallest calls take less time on the GPU than
 // Python takes to prepare them; every computation is in libfm_mel.so.
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -73,6 +74,15 @@ using Maybe = std::optional<Tensor>;
 Maybe maybe(const Tensor& t) { return t.defined() ? Maybe(t) : Maybe(); }
 Tensor or_none(const Maybe& t) { return t ? *t : Tensor(); }
 bool wants_grad(const Tensor& t) { return t.defined() && t.requires_grad(); }
+
+// Forward-mode derivatives are refused: a result without a tangent would read as
+// one whose tangent is zero.
+template <typename... Inputs>
+void no_tangents(const char* name, const Inputs&... inputs) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+  auto has = [](const Tensor& t) { return t.defined() && t._fw_grad(0).defined(); };
+  TORCH_CHECK_NOT_IMPLEMENTED(!(has(inputs) || ...), name, " has no forward-mode derivative");
+}
 
 // What a backward pass returns where the caller asked for a graph of it: the
 // gradients, whose own history is an error that leads to everything they were
@@ -170,6 +180,7 @@ struct NormNode : torch::autograd::Function<NormNode> {
 };
 
 Tensor layer_norm(const Tensor& x, Tensor weight, Tensor bias, double eps) {
+  no_tangents("layer_norm", x, weight, bias);
   TORCH_CHECK_VALUE(x.is_cuda(), "x must be a CUDA tensor (the operators run only on the GPU)");
   need_cuda(weight, "weight", x);
   need_cuda(bias, "bias", x);
@@ -260,6 +271,7 @@ struct BiasNode : torch::autograd::Function<BiasNode> {
 };
 
 Tensor relative_bias(Tensor table, int64_t q_len, int64_t k_len, int64_t q_start, int64_t far, bool both) {
+  no_tangents("relative_bias", table);
   TORCH_CHECK_VALUE(table.is_cuda(), "table must be a CUDA tensor (the operators run only on the GPU)");
   check_table(table);
   TORCH_CHECK_VALUE(q_len >= 0 && k_len >= 0, "q_len and k_len must not be negative");
@@ -399,6 +411,7 @@ Tensor int32_of(const Tensor& t, const char* name, at::IntArrayRef shape, const 
 
 std::tuple<Tensor, Tensor> attention(Tensor q, Tensor k, Tensor v, Tensor table, const c10::intrusive_ptr<Call>& c,
                                      Masks m, int64_t far, bool both, bool want_lse) {
+  no_tangents("attention", q, k, v, table, m.slopes);
   TORCH_CHECK_VALUE(q.is_cuda(), "q must be a CUDA tensor (the operators run only on the GPU)");
   need_cuda(k, "k", q);
   need_cuda(v, "v", q);

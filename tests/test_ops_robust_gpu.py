@@ -138,3 +138,27 @@ def test_changed_masks_are_noticed(ops):
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             torch.autograd.grad(out, leaves, dy)
         del out, want
+
+
+# ---------------------------------------------------------------------------
+# forward-mode derivatives are refused, not dropped
+
+def test_forward_mode(ops):
+    import torch.autograd.forward_ad as fw
+
+    q, k, v, _, g = base.make((1, 6, 6, 2, 1, 16), F32)
+    x, w, table = base.randn(g, 5, 16), base.randn(g, 16), base.randn(g, 8, 2)
+    calls = [(lambda x, w: ops.layer_norm(x, w), (x, w)),
+             (lambda x, b: ops.layer_norm(x, None, b), (x, w)),
+             (lambda t: ops.relative_bias(t, 4, 5, max_distance=16), (table,)),
+             (lambda q, k, v, t: ops.attention(q, k, v, table=t, max_distance=16), (q, k, v, table)),
+             (lambda q, k, v, s: ops.attention(q, k, v, slopes=s), (q, k, v, torch.ones(2, device="cuda")))]
+    for call, inputs in calls:
+        for n in range(len(inputs)):
+            for grad in (True, False):
+                with fw.dual_level(), torch.set_grad_enabled(grad):
+                    args = list(inputs)
+                    args[n] = fw.make_dual(args[n], torch.ones_like(args[n]))
+                    with pytest.raises(NotImplementedError, match="forward-mode"):
+                        call(*args)
+                    call(*inputs)  # no tangent: as ever
