@@ -4,6 +4,7 @@
 // Python takes to prepare them; every computation is in libfm_mel.so.
 #include <ATen/ATen.h>
 #include <c10/core/AutogradState.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -12,6 +13,7 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 
 #include <cmath>
 #include <map>
@@ -74,6 +76,14 @@ using Maybe = std::optional<Tensor>;
 Maybe maybe(const Tensor& t) { return t.defined() ? Maybe(t) : Maybe(); }
 Tensor or_none(const Maybe& t) { return t ? *t : Tensor(); }
 bool wants_grad(const Tensor& t) { return t.defined() && t.requires_grad(); }
+
+// Traces are refused: the calls are no operators of torch's own registry, so that
+// a trace would hold their outputs' allocations, or one call's results, alone.
+void no_trace(const char* name) {
+  using c10::impl::TorchDispatchModeKey, c10::impl::TorchDispatchModeTLS;
+  const bool traced = torch::jit::tracer::isTracing() || TorchDispatchModeTLS::get_mode(TorchDispatchModeKey::PROXY);
+  TORCH_CHECK_NOT_IMPLEMENTED(!traced, name, " cannot be traced");
+}
 
 // Forward-mode derivatives are refused: a result without a tangent would read as
 // one whose tangent is zero.
@@ -180,6 +190,7 @@ struct NormNode : torch::autograd::Function<NormNode> {
 };
 
 Tensor layer_norm(const Tensor& x, Tensor weight, Tensor bias, double eps) {
+  no_trace("layer_norm");
   no_tangents("layer_norm", x, weight, bias);
   TORCH_CHECK_VALUE(x.is_cuda(), "x must be a CUDA tensor (the operators run only on the GPU)");
   need_cuda(weight, "weight", x);
@@ -271,6 +282,7 @@ struct BiasNode : torch::autograd::Function<BiasNode> {
 };
 
 Tensor relative_bias(Tensor table, int64_t q_len, int64_t k_len, int64_t q_start, int64_t far, bool both) {
+  no_trace("relative_bias");
   no_tangents("relative_bias", table);
   TORCH_CHECK_VALUE(table.is_cuda(), "table must be a CUDA tensor (the operators run only on the GPU)");
   check_table(table);
@@ -411,6 +423,7 @@ Tensor int32_of(const Tensor& t, const char* name, at::IntArrayRef shape, const 
 
 std::tuple<Tensor, Tensor> attention(Tensor q, Tensor k, Tensor v, Tensor table, const c10::intrusive_ptr<Call>& c,
                                      Masks m, int64_t far, bool both, bool want_lse) {
+  no_trace("attention");
   no_tangents("attention", q, k, v, table, m.slopes);
   TORCH_CHECK_VALUE(q.is_cuda(), "q must be a CUDA tensor (the operators run only on the GPU)");
   need_cuda(k, "k", q);

@@ -162,3 +162,20 @@ def test_forward_mode(ops):
                     with pytest.raises(NotImplementedError, match="forward-mode"):
                         call(*args)
                     call(*inputs)  # no tangent: as ever
+
+
+# ---------------------------------------------------------------------------
+# traces, which would hold the allocations alone, are refused
+
+@pytest.mark.filterwarnings("ignore")
+def test_traces(ops):
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    q, k, v, _, g = base.make((1, 6, 6, 2, 1, 16), F32)
+    table = base.randn(g, 8, 2)
+    for call, inputs in [(lambda x: ops.layer_norm(x), (q,)), (lambda t: ops.relative_bias(t, 4, 5, max_distance=16), (table,)),
+                         (lambda q, k, v: ops.attention(q, k, v), (q, k, v))]:
+        with pytest.raises(NotImplementedError, match="trac"):
+            torch.jit.trace(call, inputs)
+        with pytest.raises(NotImplementedError, match="trac"):
+            make_fx(call)(*inputs)
