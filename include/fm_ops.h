@@ -70,7 +70,8 @@ int64_t fm_layer_norm_workspace(const fm_layer_norm_args* args);
  *
  * fm_buckets_create builds the map for the offsets -max_distance ..
  * max_distance (beyond them it is constant) in whole numbers on the host and
- * copies it to the current device; the handle is read-only afterwards, usable
+ * copies it to the current device (it waits for that copy alone; allowed while a
+ * graph is being recorded); the handle is read-only afterwards, usable
  * from several threads and streams on that device, and owned by the caller
  * until fm_buckets_destroy.
  *   num_buckets  : 4 .. 4096 bidirectional (even), 2 .. 4096 one-sided.

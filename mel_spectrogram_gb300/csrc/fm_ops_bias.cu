@@ -253,6 +253,27 @@ __global__ void __launch_bounds__(256) bucket_sums(const int32_t* ranges, int ma
   }
 }
 
+// Host memory to the device, there before this returns, whichever stream reads
+// it next: on a stream of its own, which waits for none and none for it. (A plain
+// copy from pageable memory may return before the device has it, and torch's
+// side streams do not wait for the default one.) Allocation and copy are allowed
+// while this or another thread records a graph.
+cudaError_t upload(int32_t** to, const int32_t* from, size_t bytes) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t err = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (err != cudaSuccess) return err;
+  cudaStream_t st = nullptr;
+  *to = nullptr;
+  err = cudaMalloc(to, bytes);
+  if (err == cudaSuccess) err = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+  if (err == cudaSuccess) err = cudaMemcpyAsync(*to, from, bytes, cudaMemcpyHostToDevice, st);
+  if (err == cudaSuccess) err = cudaStreamSynchronize(st);
+  if (st) cudaStreamDestroy(st);
+  if (err != cudaSuccess && *to) cudaFree(*to);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return err;
+}
+
 constexpr int kMaxLen = (1 << 29) - 1;
 
 fm_status check(const fm_relative_bias_args* a) {
@@ -347,12 +368,8 @@ extern "C" fm_status fm_buckets_create(fm_buckets** out, int num_buckets, int ma
   }
   fm_status st = FM_ERR_CUDA;
   if (cudaGetDevice(&b->device) == cudaSuccess) {
-    const cudaError_t err = cudaMalloc(&b->map, sizeof(int32_t) * n_all);
-    if (err == cudaErrorMemoryAllocation) st = FM_ERR_OOM;
-    if (err == cudaSuccess) {
-      if (cudaMemcpy(b->map, host, sizeof(int32_t) * n_all, cudaMemcpyHostToDevice) == cudaSuccess) st = FM_OK;
-      else cudaFree(b->map);
-    }
+    const cudaError_t err = upload(&b->map, host, sizeof(int32_t) * n_all);
+    st = err == cudaSuccess ? FM_OK : err == cudaErrorMemoryAllocation ? FM_ERR_OOM : FM_ERR_CUDA;
   }
   if (st != FM_OK) {
     cudaGetLastError();  // an allocation failure stays out of later calls' status

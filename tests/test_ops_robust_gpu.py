@@ -179,3 +179,34 @@ def test_traces(ops):
             torch.jit.trace(call, inputs)
         with pytest.raises(NotImplementedError, match="trac"):
             make_fx(call)(*inputs)
+
+
+# ---------------------------------------------------------------------------
+# bucket maps first used where nothing has made them yet
+
+def test_first_use_inside_a_recording(ops):
+    q, k, v, dy, g = base.make((1, 40, 40, 2, 2, 64), BF16)
+    table = base.randn(g, 38, 2, dtype=BF16)
+    ops.attention(q, k, v)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ops.attention(q, k, v, table=table, max_distance=77)
+        bias = ops.relative_bias(table, 5, 6, max_distance=78)
+    graph.replay()
+    ref.close(out, *ref.attention(q, k, v, table=table, max_distance=77)["out"], "replayed")
+    ref.close(bias, *ref.dense_bias(table, 5, 6, 1, 78, True)["out"], "replayed")
+
+
+def test_first_use_on_another_stream(ops):
+    g = base.gen(3)
+    table = base.randn(g, 40, 2)
+    torch.cuda.synchronize()
+    side, got = torch.cuda.Stream(), []
+    torch.cuda._sleep(10 ** 8)  # the default stream is busy: nothing of the other may wait for or pass it
+    with torch.cuda.stream(side):
+        for far in range(100, 160):
+            got.append(ops.relative_bias(table, 30, 200, max_distance=far))
+    side.synchronize()
+    for far, out in zip(range(100, 160), got):
+        ref.close(out, *ref.dense_bias(table, 30, 200, 170, far, True)["out"], f"max_distance {far}")
