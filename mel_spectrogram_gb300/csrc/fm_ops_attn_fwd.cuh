@@ -270,8 +270,10 @@ __device__ __forceinline__ bool block(const TcParams& t, const dim3 at, const in
       // both warps have their scores in registers now: P may replace them
       mx = fmaxf(mx, row_stat[j & 1][w][half ^ 1][lane_row]);
       if (raw) mx *= c;  // scale > 0 here
-      if (__any_sync(0xffffffffu, mx > m + kRise || (m == -INFINITY && mx > m))) {
-        const float top_m = fmaxf(m, mx), f = top_m == -INFINITY ? 1.f : ex2(m - top_m);
+      // each row by its own scores: what its warp's other rows see may be hidden from it
+      const bool risen = mx > m + kRise || (m == -INFINITY && mx > m);
+      if (__any_sync(0xffffffffu, risen)) {
+        const float top_m = risen ? mx : m, f = risen ? ex2(m - mx) : 1.f;
         m = top_m;
         l *= f;
         if (j > 0) {

@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
         for (int e = 0; e < 4; ++e)
           if (s[x][e] != -INFINITY && (bad >> (2 * (8 * x + pair + (e & 1))) & 3)) s[x][e] = NAN;
     }
-    // the running maximum follows only rises by 2^8, as in the tiled kernel
+    // the running maximum follows only rises by 2^8, as in the tiled kernel, of
+    // the row itself
     float top[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -263,9 +264,8 @@ __global__ void __launch_bounds__(kWarps * 32) step(const __grid_constant__ Step
       float f[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float next = fmaxf(m[r], top[r]);
-        f[r] = next == -INFINITY ? 1.f : ex2(m[r] - next);
-        m[r] = next;
+        f[r] = risen(r) ? ex2(m[r] - top[r]) : 1.f;
+        m[r] = risen(r) ? top[r] : m[r];
         l[r] *= f[r];
       }
 #pragma unroll

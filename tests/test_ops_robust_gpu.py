@@ -210,3 +210,32 @@ def test_first_use_on_another_stream(ops):
     side.synchronize()
     for far, out in zip(range(100, 160), got):
         ref.close(out, *ref.dense_bias(table, 30, 200, 170, far, True)["out"], f"max_distance {far}")
+
+
+# ---------------------------------------------------------------------------
+# what a mask hides changes no bit of the others, however large it is
+
+def interleaved(dtype, dim):
+    """Two recordings frame by frame in turn, so that every tile and warp holds
+    both: inputs, the same with the second one loud, and the ids."""
+    T = 300
+    ids = (torch.arange(T, dtype=torch.int32, device="cuda") % 2)[None]
+    q, k, v, dy, _ = base.make((1, T, T, 2, 1, dim), dtype)
+    k = k * torch.linspace(0.5, 4, T, device="cuda").to(dtype)[None, :, None, None]  # maxima that rise from tile to tile
+    loud = [t.clone() for t in (q, k, v, dy)]
+    for t, f in zip(loud, (4, 8, 30, 300)):
+        t[:, 1::2] *= f
+    return (q, k, v, dy), loud, ids
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_hidden_rows_change_no_output(ops, dtype, dim, softcap):
+    plain, loud, ids = interleaved(dtype, dim)
+    for causal in (False, True):
+        for rows in (slice(0, 300), slice(150, 153)):  # in tiles, and few
+            want, got = (ops.attention(q[:, rows], k, v, q_docs=ids[:, rows], k_docs=ids, causal=causal,
+                                       q_start=rows.start, softcap=softcap) for q, k, v, _ in (plain, loud))
+            assert torch.equal(got[:, ::2], want[:, ::2])
+            assert not torch.equal(got[:, 1::2], want[:, 1::2])
