@@ -55,6 +55,7 @@ AttnParams params(const fm_attention_args* a) {
     p.table_f32 = a->table_dtype == FM_F32;
   }
   p.slopes = a->slopes;
+  p.f16 = a->dtype == FM_F16;
   return p;
 }
 

@@ -30,6 +30,7 @@ struct AttnParams {
   float* delta;  // [batch][heads][q_len]: sum of dout * out
   float* part;   // partial bias gradients: [batch * q tiles][heads][2 * max_distance + 1]
   int q_tiles;
+  int f16;  // the inputs' type: the backward pass on the tensor cores scales dS
 };
 
 // Rows of one batch entry: how many keys count, where the queries stand.

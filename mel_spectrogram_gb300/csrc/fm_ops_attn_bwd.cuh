@@ -41,10 +41,12 @@ constexpr int kCols = 64;      // rows of a streamed tile
 constexpr int kColumns = kCols / 2;  // a thread's share
 constexpr int kDiagPad = 192;  // room beside the bias gradient for a tile's diagonals
 constexpr int kChains = 4, kChainEntries = 48;
-// f16 operands: P is kept 2^15 larger (weights are at most 1), and dS times a
-// power of two that brings its bound 2 |dout| |v| to 2^14, so that small
-// weights and small gradients stay normal numbers and large ones in range.
-// The products' results are scaled back in 32 bits. bf16 has the range.
+// f16 operands: P is kept 2^15 larger (weights are at most 1), and each row of dS
+// (a query's, or a key's in the keys' kernel) times a power of two that brings
+// its bound 2 |dout| |v| to 2^14, so that small weights and small gradients stay
+// normal numbers and large ones in range. The bound takes what the row sees and
+// no more (bwd_scales): what is hidden from it changes none of its bits. The
+// products' results are scaled back in 32 bits. bf16 has the range.
 template <bool BF16>
 constexpr float kLift = BF16 ? 0.f : 15.f;
 
@@ -112,17 +114,10 @@ struct Extra {
   const float* lse2;   // [batch * heads][q_pad]: base-2 lse, +inf for rows that see nothing or are not there
   const float* delta;  // [batch * heads][q_pad]
   int q_pad;           // q_len rounded up to 64
-  // [batch * kv_heads] largest squared norms of a row of dout, then of v (f16)
-  const float* peak;
+  // f16: powers of two for the rows of dS, [batch][kv_heads][tiles of 128 queries or keys]
+  const float *q_scale, *k_scale;
   int slots;  // tiles of the ring
 };
-// the power of two for dS
-__device__ __forceinline__ float ds_scale(const Extra& x, int at, int count) {
-  const float bound = 0.5f * log2f(x.peak[at]) + 0.5f * log2f(x.peak[count + at]) + 1.f;
-  const float e = floorf(14.f - bound);
-  return fabsf(e) < 120.f ? exp2f(e) : 1.f;  // nothing, infinite or NaN: as it is
-}
-
 // One block's work; SCAN: of the second launch, on tensor memory that its block
 // holds (held), as in the forward pass. False: a wait gave up.
 template <int DP, bool BF16, int MODE, bool KEYS, bool SCAN>
@@ -223,7 +218,9 @@ __device__ __forceinline__ bool block(const TcParams& t, const Extra& x, const d
     const int row = r0 + lane_row;  // the key or the query
     const float c = p.scale * kLog2e;
     const bool raw = MODE == 0 || (SCAN && t.raw);
-    const float sigma = BF16 ? 1.f : ds_scale(x, b * p.kv_heads + hk, p.batch * p.kv_heads);
+    const int row_tiles = KEYS ? t.k_tiles : t.q_tiles;
+    const float sigma =
+        BF16 ? 1.f : (KEYS ? x.k_scale : x.q_scale)[((long long)b * p.kv_heads + hk) * row_tiles * kTile + row];
     const float tau = BF16 ? 1.f : sigma * exp2f(-kLift<BF16>);
     const int32_t* kdocs = p.k_docs ? p.k_docs + (long long)b * p.k_len : nullptr;
     const int32_t* qdocs = p.q_docs ? p.q_docs + (long long)b * p.q_len : nullptr;

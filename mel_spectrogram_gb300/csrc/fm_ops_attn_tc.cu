@@ -151,30 +151,17 @@ __global__ void __launch_bounds__(32 * WARPS) join(const AttnParams p, int split
   }
 }
 
-// the largest of a block's values (not negative), into *to
-__device__ __forceinline__ void block_peak(float v, float* to) {
-  __shared__ float tops[8];
-  v = warp_max(v);
-  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = v;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) v = fmaxf(v, tops[w]);
-    atomicMax((int*)to, __float_as_int(v));  // bits of such floats are ordered as ints; a maximum has no order
-  }
-}
-
 // Statistics of the backward pass by query, padded to whole tiles of 64:
 // base-2 lse (+inf where a query sees nothing or is padding: every weight
 // 2^(z - inf) is 0) less `lift`, and delta = dout . out. LANES threads a row, 8
-// elements each, kStatsParts rows in turn; block (x, head, batch entry). peak: the largest squared norm
-// of a row of dout, by key head.
+// elements each, kStatsParts rows in turn; block (x, head, batch entry). norms
+// (f16, zeros before): a query's largest squared norm of dout over the heads that
+// share keys; what is not finite counts as 0.
 constexpr int kStatsParts = 4;
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) bwd_stats(const AttnParams p, int q_pad, float lift, float* lse2, float* delta,
-                                                 float* peak) {
+                                                 float* norms, int norm_pad) {
   const int lane = threadIdx.x % LANES, h = blockIdx.y, b = blockIdx.z;
-  float top = 0.f;
 #pragma unroll 2
   for (int part = 0; part < kStatsParts; ++part) {
     const int i = (blockIdx.x * kStatsParts + part) * (256 / LANES) + threadIdx.x / LANES;
@@ -202,35 +189,135 @@ __global__ void __launch_bounds__(256) bwd_stats(const AttnParams p, int q_pad, 
       s += __shfl_xor_sync(0xffffffffu, s, o, LANES);
       norm += __shfl_xor_sync(0xffffffffu, norm, o, LANES);
     }
-    top = norm <= 3.402823466e38f ? fmaxf(top, norm) : top;  // what is not finite sets no scale
     if (lane == 0 && i < q_pad) {
       lse2[row * q_pad + i] = l == -INFINITY ? INFINITY : l * kLog2e - lift;
       delta[row * q_pad + i] = s;
+      // bits of floats that are not negative are ordered as ints; a maximum has no order
+      if (norms && norm <= 3.402823466e38f)
+        atomicMax((int*)norms + ((long long)b * p.kv_heads + h / p.group) * norm_pad + i, __float_as_int(norm));
     }
   }
-  if (peak) block_peak(top, peak + b * p.kv_heads + h / p.group);
 }
 
-// The largest squared norm of a row of v that counts, by batch entry and key
-// head; 16 rows at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) bwd_v_peak(const AttnParams p, float* peak) {
-  const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 15;
-  const int len = row_info(p, b).len;
-  float top = 0.f;
-  for (int j0 = blockIdx.x * 16; j0 < len; j0 += gridDim.x * 16) {
-    const int j = j0 + (threadIdx.x >> 4);
-    float norm = 0.f;
-    if (j < len && lane * 8 < p.dim && (p.k_docs == nullptr || p.k_docs[(long long)b * p.k_len + j] >= 0)) {
-      const Pack<T, 8> v = *(const Pack<T, 8>*)((const T*)p.v + b * p.vs.b + j * p.vs.t + h * p.vs.h + lane * 8);
+// Squared norms of v by key, whole tiles of 128; 0 for what does not count or is
+// not finite. 16 threads a key, 16 keys a block.
+__global__ void __launch_bounds__(256) bwd_v_norms(const AttnParams p, float* norms, int pad) {
+  const int h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 15, j = blockIdx.x * 16 + (threadIdx.x >> 4);
+  float norm = 0.f;
+  if (j < row_info(p, b).len && lane * 8 < p.dim && (p.k_docs == nullptr || p.k_docs[(long long)b * p.k_len + j] >= 0)) {
+    const Pack<__half, 8> v =
+        *(const Pack<__half, 8>*)((const __half*)p.v + b * p.vs.b + j * p.vs.t + h * p.vs.h + lane * 8);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) norm = fmaf(to_f(v.v[k]), to_f(v.v[k]), norm);
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, o, 16);
-    top = norm <= 3.402823466e38f ? fmaxf(top, norm) : top;  // what is not finite sets no scale
+    for (int k = 0; k < 8; ++k) norm = fmaf(to_f(v.v[k]), to_f(v.v[k]), norm);
   }
-  block_peak(top, peak + b * p.kv_heads + h);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, o, 16);
+  if (lane == 0) norms[((long long)b * p.kv_heads + h) * pad + j] = norm <= 3.402823466e38f ? norm : 0.f;
+}
+
+// The power of two for each row of dS: 2^14 over the bound 2 |dout| |v| of the
+// row's own norm and the largest one that it sees. A block takes the 128 queries
+// or keys of a tile, a thread a row. Of a tile that all of them see a thread reads
+// one norm; of one cut by lengths or causality a row needs the largest norm up to,
+// or from, one column, which the block makes once for all; only where documents
+// meet each thread goes through the tile's norms and ids. 6 us for causal
+// training's 8 x 4 x 1292 rows (17 with each thread going through every cut tile).
+__global__ void __launch_bounds__(kTile) bwd_scales(const __grid_constant__ TcParams t, const float* q_norms,
+                                                    const float* k_norms, float* q_scale, float* k_scale) {
+  __shared__ float norm[kTile], tops[kTile / 32];
+  __shared__ int id[kTile];
+  const AttnParams& p = t.p;
+  const bool keys = (int)blockIdx.x >= t.q_tiles;
+  const int b = blockIdx.z, tile = keys ? blockIdx.x - t.q_tiles : blockIdx.x, r0 = tile * kTile, tid = threadIdx.x;
+  const RowInfo info = row_info(p, b);
+  const long long head = (long long)b * p.kv_heads + blockIdx.y;
+  const long long q_at = head * t.q_tiles * kTile, k_at = head * t.k_tiles * kTile;
+  const float *own = keys ? k_norms + k_at : q_norms + q_at, *other = keys ? q_norms + q_at : k_norms + k_at;
+  const int row = r0 + tid, s_len = keys ? p.q_len : p.k_len, own_len = keys ? p.k_len : p.q_len;
+  // columns [lo, hi) are seen by length and causality; tiles [begin, end) hold some of any row's
+  int lo = 0, hi = keys ? p.q_len : info.len, begin = 0, end = keys ? t.q_tiles : 0;
+  int all_lo = 0, all_hi = hi;  // of all rows
+  if (keys) {
+    if (p.causal) {
+      if (row >= info.prefix) lo = row - info.start;
+      if (r0 + kTile > info.prefix) all_lo = r0 + kTile - 1 - info.start;
+      if (r0 >= info.prefix) begin = min(end, max(0, r0 - info.start) / kTile);
+    }
+  } else {
+    if (p.causal) {
+      hi = min(hi, max(info.start + row + 1, info.prefix));
+      all_hi = min(all_hi, max(info.start + r0 + 1, info.prefix));
+    }
+    end = (key_end(p, info, r0, min(kTile, p.q_len - r0)) + kTile - 1) / kTile;
+  }
+  const int32_t* docs = nullptr;
+  int4 own_range = make_int4(0, 0, 1, 0);
+  int doc = -2;  // matches none
+  if (t.k_ranges) {
+    docs = keys ? p.q_docs + (long long)b * p.q_len : p.k_docs + (long long)b * p.k_len;
+    own_range = keys ? t.k_ranges[b * t.k_tiles + tile] : t.q_ranges[b * t.q_tiles + tile];
+    if (row < own_len) doc = (keys ? p.k_docs + (long long)b * p.k_len : p.q_docs + (long long)b * p.q_len)[row];
+    if (doc < 0) doc = -2;
+  }
+  float all = 0.f, mine = 0.f;  // of this thread's column of tiles that all see; of this row's
+  // without documents those tiles follow one another
+  const int whole_begin = docs ? begin : max(begin, (all_lo + kTile - 1) / kTile);
+  const int whole_end = docs ? begin : min(end, all_hi / kTile);
+#pragma unroll 8
+  for (int i = whole_begin; i < whole_end; ++i) all = fmaxf(all, other[i * kTile + tid]);
+  for (int i = begin; i < end; ++i) {
+    const int c0 = i * kTile, c = c0 + tid;
+    bool same = true;
+    if (docs) {
+      const int4 o = keys ? t.q_ranges[b * t.q_tiles + i] : t.k_ranges[b * t.k_tiles + i];
+      if (o.x > own_range.y || o.y < own_range.x) continue;
+      same = o.z && own_range.z && o.x == own_range.x;
+      if (same && c0 >= all_lo && c0 + kTile <= all_hi) {
+        all = fmaxf(all, other[c]);
+        continue;
+      }
+    } else if (i >= whole_begin && i < whole_end) {
+      i = whole_end - 1;
+      continue;
+    }
+    float v = other[c];
+    __syncthreads();
+    if (same) {
+      // a query sees the tile's keys before its `hi`, a key the queries from its
+      // `lo` on: the largest of a warp's columns up to, or from, each one
+      const int lane = tid & 31;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const float o = keys ? __shfl_down_sync(0xffffffffu, v, d) : __shfl_up_sync(0xffffffffu, v, d);
+        if (keys ? lane + d < 32 : lane >= d) v = fmaxf(v, o);
+      }
+      norm[tid] = v;
+      __syncthreads();
+      const int first = max(lo - c0, 0), last = min(hi - c0, kTile) - 1;
+      if (first <= last) {
+        const int at = keys ? first : last;
+        mine = fmaxf(mine, norm[at]);
+        for (int w = keys ? (at | 31) + 1 : (at & ~31) - 1; w >= 0 && w < kTile; w += keys ? 32 : -32)
+          mine = fmaxf(mine, norm[w]);
+      }
+      continue;
+    }
+    norm[tid] = v;
+    id[tid] = c < s_len ? docs[c] : -1;
+    __syncthreads();
+    float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+    for (int k = 0; k < kTile; ++k)
+      m[k & 3] = fmaxf(m[k & 3], c0 + k >= lo && c0 + k < hi && id[k] == doc ? norm[k] : 0.f);
+    mine = fmaxf(mine, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+  }
+  all = warp_max(all);
+  if ((tid & 31) == 0) tops[tid >> 5] = all;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kTile / 32; ++w) mine = fmaxf(mine, tops[w]);
+  const float e = floorf(13.f - 0.5f * log2f(own[row]) - 0.5f * log2f(mine));
+  (keys ? k_scale + k_at : q_scale + q_at)[row] = fabsf(e) < 120.f ? exp2f(e) : 1.f;  // of nothing: as it is
 }
 
 // Whether the few-query kernel runs. It takes time with its rows (queries x
@@ -316,8 +403,9 @@ TcPlan tc_plan(const AttnParams& p, bool backward) {
   if (w.splits > 1) at += align256(rows * w.splits * (int64_t)sizeof(float));
   w.stats = at;
   if (backward) at += align256((int64_t)sizeof(float) * 2 * p.batch * p.heads * ((p.q_len + 63) / 64 * 64));
-  w.peak = at;
-  if (backward) at += align256((int64_t)sizeof(float) * 2 * p.batch * p.kv_heads);
+  w.scales = at;  // norms of queries and keys, then the powers of two
+  if (backward && p.f16)
+    at += align256((int64_t)sizeof(float) * 2 * p.batch * p.kv_heads * kTile * ((int64_t)w.q_tiles + w.k_tiles));
   w.bias = at;
   if (p.map && w.step.splits == 0) at += align256((int64_t)sizeof(float) * p.heads * (2 * (int64_t)p.max_distance + 1));
   w.flags = at;
@@ -402,20 +490,24 @@ fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cu
   const bool narrow = p.dim <= 64;
   const int per_block = kStatsParts * (narrow ? 32 : 16);
   const dim3 grid((x.q_pad + per_block - 1) / per_block, p.heads, p.batch);
-  float* peak = nullptr;
-  const int count = p.batch * p.kv_heads;
+  float *delta = lse2 + rows, *q_norms = nullptr;
+  const int q_rows = w.q_tiles * kTile, k_rows = w.k_tiles * kTile;
+  const long long heads = (long long)p.batch * p.kv_heads;
   if (!bf16) {
-    peak = (float*)(ws + w.peak);
-    if (cudaMemsetAsync(peak, 0, sizeof(float) * 2 * count, st) != cudaSuccess) return FM_ERR_CUDA;
-    const int rows16 = (p.k_len + 15) / 16;
-    bwd_v_peak<__half><<<dim3(rows16 < 16 ? rows16 : 16, p.kv_heads, p.batch), 256, 0, st>>>(p, peak + count);
-    x.peak = peak;
+    q_norms = (float*)(ws + w.scales);
+    if (cudaMemsetAsync(q_norms, 0, sizeof(float) * heads * q_rows, st) != cudaSuccess) return FM_ERR_CUDA;
   }
-  float* delta = lse2 + rows;
-  if (bf16 && narrow) bwd_stats<__nv_bfloat16, 8><<<grid, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, delta, peak);
-  else if (bf16) bwd_stats<__nv_bfloat16, 16><<<grid, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, delta, peak);
-  else if (narrow) bwd_stats<__half, 8><<<grid, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, delta, peak);
-  else bwd_stats<__half, 16><<<grid, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, delta, peak);
+  if (bf16 && narrow) bwd_stats<__nv_bfloat16, 8><<<grid, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, delta, nullptr, 0);
+  else if (bf16) bwd_stats<__nv_bfloat16, 16><<<grid, 256, 0, st>>>(p, x.q_pad, 0.f, lse2, delta, nullptr, 0);
+  else if (narrow) bwd_stats<__half, 8><<<grid, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, delta, q_norms, q_rows);
+  else bwd_stats<__half, 16><<<grid, 256, 0, st>>>(p, x.q_pad, bwd::kLift<false>, lse2, delta, q_norms, q_rows);
+  if (!bf16) {
+    float *k_norms = q_norms + heads * q_rows, *q_scale = k_norms + heads * k_rows, *k_scale = q_scale + heads * q_rows;
+    bwd_v_norms<<<dim3(k_rows / 16, p.kv_heads, p.batch), 256, 0, st>>>(p, k_norms, k_rows);
+    bwd_scales<<<dim3(w.q_tiles + w.k_tiles, p.kv_heads, p.batch), kTile, 0, st>>>(t, q_norms, k_norms, q_scale, k_scale);
+    x.q_scale = q_scale;
+    x.k_scale = k_scale;
+  }
   const int mode = mode_of(p);
   using Fn = fm_status (*)(const TcParams&, const bwd::Extra&, int, cudaStream_t);
   const bool small = p.dim <= 64;

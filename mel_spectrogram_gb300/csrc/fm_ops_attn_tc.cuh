@@ -63,7 +63,7 @@ fm_status attn_step(const AttnParams& p, int64_t dtype, const StepPlan& w, float
 struct TcPlan {
   StepPlan step;  // step.splits > 0: the forward pass takes the few-query kernel
   int splits, split_tiles, q_tiles, k_tiles;
-  int64_t ranges, part_o, part_lse, stats, peak, bias, flags, flags_keys, total;
+  int64_t ranges, part_o, part_lse, stats, scales, bias, flags, flags_keys, total;
 };
 bool tc_layout_ok(const AttnParams& p, int64_t dtype, bool backward);
 TcPlan tc_plan(const AttnParams& p, bool backward);  // backward needs heads, q_len, map and grad only

@@ -239,3 +239,50 @@ def test_hidden_rows_change_no_output(ops, dtype, dim, softcap):
                                        q_start=rows.start, softcap=softcap) for q, k, v, _ in (plain, loud))
             assert torch.equal(got[:, ::2], want[:, ::2])
             assert not torch.equal(got[:, 1::2], want[:, 1::2])
+
+
+# ---------------------------------------------------------------------------
+# nor of their gradients
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_hidden_rows_change_no_gradient(ops, dtype, dim, softcap):
+    plain, loud, ids = interleaved(dtype, dim)
+    for causal in (False, True):
+        want, got = (passes(ops, *inputs, q_docs=ids, k_docs=ids, causal=causal, softcap=softcap)
+                     for inputs in (plain, loud))
+        for name, a, b in zip(("out", "dq", "dk", "dv"), got, want):
+            assert torch.equal(a[:, ::2], b[:, ::2]), (name, causal)
+            assert not torch.equal(a[:, 1::2], b[:, 1::2])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_later_rows_change_no_gradient(ops, dtype, dim):
+    T, n = 300, 150
+    q, k, v, dy, _ = base.make((1, T, T, 2, 1, dim), dtype)
+    want = passes(ops, q, k, v, dy, causal=True)
+    loud = [t.clone() for t in (q, k, v, dy)]
+    for t, f in zip(loud, (4, 4, 30, 300)):
+        t[:, n:] *= f
+    got = passes(ops, *loud, causal=True)
+    for a, b in zip(got[:2], want[:2]):  # earlier queries' output and gradient
+        assert torch.equal(a[:, :n], b[:, :n])
+    loud = [q.clone(), k, v, dy.clone()]
+    loud[0][:, :n] *= 4
+    loud[3][:, :n] *= 300
+    got = passes(ops, *loud, causal=True)
+    for a, b in zip(got[2:], want[2:]):  # later keys' gradients
+        assert torch.equal(a[:, n:], b[:, n:])
+
+
+def test_loud_and_quiet_gradients(ops):
+    # f16 rows whose gradients are 10^5 times apart, each within its own bound
+    q, k, v, dy, _ = base.make((1, 200, 200, 2, 1, 64), F16)
+    ids = base.docs_of(200, [(0, 100), (1, 100)])
+    dy[:, :100] *= 2 ** -5
+    v[:, :100] *= 2 ** -2
+    dy[:, 100:] *= 300
+    v[:, 100:] *= 30
+    base.check_attention(ops, q, k, v, "loud and quiet", dy=dy, q_docs=ids, k_docs=ids)
