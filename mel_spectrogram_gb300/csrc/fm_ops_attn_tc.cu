@@ -531,7 +531,8 @@ fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cu
 
 extern "C" fm_status fm_ops_poll_error(void) {
   unsigned* word = fm::ops_error_word();
-  if (word == nullptr) return FM_ERR_CUDA;
+  // the whole device: a copy would not wait for streams that do not wait for the default one
+  if (word == nullptr || cudaDeviceSynchronize() != cudaSuccess) return FM_ERR_CUDA;
   unsigned v = 0;
   if (cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return FM_ERR_CUDA;
   if (v != 0 && cudaMemset(word, 0, sizeof v) != cudaSuccess) return FM_ERR_CUDA;

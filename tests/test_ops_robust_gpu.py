@@ -286,3 +286,15 @@ def test_loud_and_quiet_gradients(ops):
     dy[:, 100:] *= 300
     v[:, 100:] *= 30
     base.check_attention(ops, q, k, v, "loud and quiet", dy=dy, q_docs=ids, k_docs=ids)
+
+
+# ---------------------------------------------------------------------------
+# the error word
+
+def test_poll_waits_for_every_stream(ops):
+    side, event = torch.cuda.Stream(), torch.cuda.Event()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(5 * 10 ** 8)
+        event.record()
+    assert ops.library().fm_ops_poll_error() == 0
+    assert event.query()
