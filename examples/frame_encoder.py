@@ -19,7 +19,7 @@ import torch
 from torch import nn
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from mel_spectrogram_gb300 import MelSpectrogram, attention, layer_norm  # noqa: E402
+from mel_spectrogram_gb300 import FM_OK, MelSpectrogram, attention, layer_norm, ops  # noqa: E402
 
 
 class Norm(nn.Module):
@@ -149,6 +149,8 @@ def run(steps=20, dtype=torch.bfloat16, seconds=2.0, seed=0):
             lens = torch.full((1,), n + 1, dtype=torch.int32, device="cuda")
             got.append(model.step(first[:, n:n + 1], cache, lens))
         far = float((torch.cat(got, 1) - whole).float().norm() / whole.float().norm())
+    if ops.poll_error() != FM_OK:
+        raise RuntimeError("a wait in a kernel gave up: the results are not valid")
     return losses, far
 
 

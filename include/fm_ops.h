@@ -185,12 +185,20 @@ fm_status fm_attention_backward(const fm_attention_args* args, fm_stream_t strea
  * slopes, dtable). */
 int64_t fm_attention_workspace(const fm_attention_args* args, int backward);
 
-/* Takes and clears the current device's error word of these operators, after
- * waiting for the work queued on it: FM_ERR_KERNEL_TIMEOUT if a bounded wait
- * inside an attention kernel gave up (its results are then not valid, and until
- * the word is taken later calls may give up early too), FM_OK otherwise. Not
- * allowed while a graph is being recorded. */
+/* Where a bounded wait inside an attention kernel gives up (after two seconds;
+ * never in ordinary running), the results of its call are not valid. From when
+ * the host can see it the attention calls on that device start nothing and
+ * return FM_ERR_KERNEL_TIMEOUT, until the error is taken; calls under way by
+ * then, and replays of recorded ones, may give up early too.
+ *
+ * fm_ops_poll_error waits for all work queued on the current device, on any
+ * stream, then takes and clears that error: FM_ERR_KERNEL_TIMEOUT or FM_OK. Not
+ * allowed while a graph is being recorded.
+ *
+ * fm_ops_selftest_wait -- diagnostic: queues a kernel of one warp whose wait
+ * runs out, so that the two ways of learning of it can be tested. */
 fm_status fm_ops_poll_error(void);
+fm_status fm_ops_selftest_wait(fm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -109,6 +109,7 @@ extern "C" fm_status fm_attention_forward(const fm_attention_args* a, fm_stream_
   if (a->q == nullptr || a->out == nullptr || (a->k_len > 0 && (a->k == nullptr || a->v == nullptr)))
     return FM_ERR_INVALID_ARG;
   if ((a->buckets && a->table == nullptr) || !same_device(a->buckets)) return FM_ERR_INVALID_ARG;
+  if (fm_status s = ops_error_seen()) return s;
   AttnParams p = params(a);
   p.out = a->out;
   if (tc_layout_ok(p, a->dtype, false)) {
@@ -137,6 +138,7 @@ extern "C" fm_status fm_attention_backward(const fm_attention_args* a, fm_stream
   if ((a->buckets && a->table == nullptr) || !same_device(a->buckets)) return FM_ERR_INVALID_ARG;
   if (a->workspace == nullptr || a->workspace_bytes < backward_bytes(a) || ((uintptr_t)a->workspace & 15))
     return FM_ERR_INVALID_ARG;
+  if (fm_status s = ops_error_seen()) return s;
   AttnParams p = params(a);
   p.out_in = a->out;
   p.dout = a->dout;

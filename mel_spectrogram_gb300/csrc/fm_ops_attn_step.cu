@@ -69,7 +69,7 @@ struct StepParams {
   AttnParams p;
   CUtensorMap km, vm;  // {dim, token, head, batch}, boxes of 64 x 16
   int k_mh, k_mb, v_mh, v_mb;
-  unsigned* err;
+  ErrorWords err;
   int splits, split_keys;  // keys of one split, a multiple of kWarps * kKeys
   int row_tiles;
   float *part_o, *part_lse;
@@ -408,8 +408,7 @@ fm_status attn_step(const AttnParams& p, int64_t dtype, const StepPlan& w, float
   t.row_tiles = w.row_tiles;
   t.part_o = part_o;
   t.part_lse = part_lse;
-  t.err = ops_error_word();
-  if (t.err == nullptr ||
+  if (!ops_error_words(&t.err) ||
       !tc_encode(&t.km, p.k, p.ks, p.batch, p.k_len, p.kv_heads, p.dim, kKeys, bf16, &t.k_mh, &t.k_mb) ||
       !tc_encode(&t.vm, p.v, p.vs, p.batch, p.k_len, p.kv_heads, p.dim, kKeys, bf16, &t.v_mh, &t.v_mb))
     return FM_ERR_CUDA;

@@ -4,20 +4,38 @@
 
 #include <cudaTypedefs.h>
 
+#include <mutex>
+
 namespace fm {
 
 __device__ unsigned g_ops_error;
 
-unsigned* ops_error_word() {
-  static unsigned* known[64] = {};
+bool ops_error_words(tc::ErrorWords* words) {
+  static std::mutex mu;
+  static tc::ErrorWords known[64] = {};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  if (known[dev] == nullptr) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_ops_error) != cudaSuccess) return nullptr;
-    known[dev] = (unsigned*)p;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev].host == nullptr) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return false;
+    void *d = nullptr, *h = nullptr;
+    // addressed the same from the device: a 64-bit process has one address space
+    const bool ok = cudaGetSymbolAddress(&d, g_ops_error) == cudaSuccess &&
+                    cudaHostAlloc(&h, sizeof(unsigned), cudaHostAllocPortable | cudaHostAllocMapped) == cudaSuccess;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!ok) return false;
+    *(volatile unsigned*)h = 0;
+    known[dev] = tc::ErrorWords{(unsigned*)d, (unsigned*)h};
   }
-  return known[dev];
+  *words = known[dev];
+  return true;
+}
+
+fm_status ops_error_seen() {
+  tc::ErrorWords w;
+  if (!ops_error_words(&w)) return FM_ERR_CUDA;
+  return *(volatile unsigned*)w.host ? FM_ERR_KERNEL_TIMEOUT : FM_OK;
 }
 
 fm_status attn_fwd_bf16_64(const TcParams& t, int mode, cudaStream_t st);
@@ -422,8 +440,7 @@ fm_status tc_setup(TcParams& t, const AttnParams& p, int64_t dtype, const TcPlan
                    cudaStream_t st) {
   const bool bf16 = dtype == FM_BF16;
   t.p = p;
-  t.err = ops_error_word();
-  if (t.err == nullptr) return FM_ERR_CUDA;
+  if (!ops_error_words(&t.err)) return FM_ERR_CUDA;
   t.raw = mode_of(p) == 0;
   t.q_tiles = w.q_tiles;
   t.k_tiles = w.k_tiles;
@@ -529,12 +546,35 @@ fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cu
 }
 }  // namespace fm
 
+namespace {
+// a wait for an arrival that never comes
+__global__ void wait_for_nothing(fm::tc::ErrorWords err) {
+  __shared__ uint64_t bar;
+  __shared__ volatile int dead;
+  if (threadIdx.x == 0) {
+    fm::tc::bar_init(fm::tc::smem_u32(&bar), 1);
+    fm::tc::fence_bar_init();
+    dead = 0;
+  }
+  __syncthreads();
+  fm::tc::bar_wait(fm::tc::smem_u32(&bar), 0, &dead, err);
+}
+}  // namespace
+
+extern "C" fm_status fm_ops_selftest_wait(fm_stream_t stream) {
+  fm::tc::ErrorWords w;
+  if (!fm::ops_error_words(&w)) return FM_ERR_CUDA;
+  wait_for_nothing<<<1, 32, 0, (cudaStream_t)stream>>>(w);
+  return fm::launch_status();
+}
+
 extern "C" fm_status fm_ops_poll_error(void) {
-  unsigned* word = fm::ops_error_word();
+  fm::tc::ErrorWords w;
   // the whole device: a copy would not wait for streams that do not wait for the default one
-  if (word == nullptr || cudaDeviceSynchronize() != cudaSuccess) return FM_ERR_CUDA;
+  if (!fm::ops_error_words(&w) || cudaDeviceSynchronize() != cudaSuccess) return FM_ERR_CUDA;
   unsigned v = 0;
-  if (cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return FM_ERR_CUDA;
-  if (v != 0 && cudaMemset(word, 0, sizeof v) != cudaSuccess) return FM_ERR_CUDA;
+  if (cudaMemcpy(&v, w.device, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return FM_ERR_CUDA;
+  if (v != 0 && cudaMemset(w.device, 0, sizeof v) != cudaSuccess) return FM_ERR_CUDA;
+  *(volatile unsigned*)w.host = 0;
   return (fm_status)v;
 }

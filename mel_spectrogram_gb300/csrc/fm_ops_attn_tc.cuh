@@ -30,7 +30,7 @@ struct TcParams {
   const float* bias;     // [heads][2 * max_distance + 1]: the bias by offset, base 2
   float* part_o;         // [splits][batch][heads][q_len][dim]
   float* part_lse;       // [splits][batch][heads][q_len], base 2
-  unsigned* err;
+  tc::ErrorWords err;
   // Where masks may hide a key from one query of a tile and not from another, a
   // block notes here whether its results were all finite, and a second launch
   // runs the others again, looking at every streamed row (clean_row): nearly
@@ -44,8 +44,9 @@ struct TcParams {
 
 constexpr int kScan = 3;  // in place of a mode: the second launch
 
-// the device's error word for the operators, NULL if there is none
-unsigned* ops_error_word();
+// The current device's error words, NULL if there are none: made by the first
+// call, also while a graph is being recorded.
+bool ops_error_words(tc::ErrorWords* words);
 
 // Bytes of workspace of the tensor-core passes, and whether they take this
 // call: 16-bit types, dim a multiple of 8 up to 128, and tensors whose rows
@@ -67,6 +68,9 @@ struct TcPlan {
 };
 bool tc_layout_ok(const AttnParams& p, int64_t dtype, bool backward);
 TcPlan tc_plan(const AttnParams& p, bool backward);  // backward needs heads, q_len, map and grad only
+// FM_ERR_KERNEL_TIMEOUT where a wait gave up since the words were last taken: its
+// call's results are not valid, and nothing more is started on top of them
+fm_status ops_error_seen();
 fm_status attn_tc_forward(const AttnParams& p, int64_t dtype, char* ws, cudaStream_t st);
 // grad: the bias gradient is wanted (p.part is set here; its rows are p.batch * q_tiles of tile kTile)
 fm_status attn_tc_backward(AttnParams& p, int64_t dtype, bool grad, char* ws, cudaStream_t st);

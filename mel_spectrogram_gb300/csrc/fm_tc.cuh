@@ -35,6 +35,11 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
+// Where a wait that gave up is noted: in a word on the device, which other waits
+// look at while they poll, and in one in host memory, which the next call looks at.
+struct ErrorWords {
+  unsigned *device, *host;
+};
 // A wait that ends: after two seconds or 2^26 polls it gives up, records the
 // error and returns false, and so does every wait that finds the error (its
 // own block's flag, or the device's word) while it polls. A role that got
@@ -44,7 +49,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
-__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead, unsigned* err) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead, const ErrorWords& err) {
   const unsigned long long begin = now_ns();
 #pragma unroll 1
   for (int i = 0; i < (1 << 20); ++i) {
@@ -52,13 +57,15 @@ __device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, vol
     for (int k = 0; k < 64; ++k)
       if (bar_try(bar, parity)) return true;
     if (*dead) return false;
-    if (*(volatile unsigned*)err != 0 || now_ns() - begin > 2000000000ull) break;
+    if (*(volatile unsigned*)err.device != 0 || now_ns() - begin > 2000000000ull) break;
   }
   *dead = 1;
-  atomicExch(err, 5u /* FM_ERR_KERNEL_TIMEOUT */);
+  atomicExch(err.device, 5u /* FM_ERR_KERNEL_TIMEOUT */);
+  *(volatile unsigned*)err.host = 5u;
+  __threadfence_system();
   return false;
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead, unsigned* err) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead, const ErrorWords& err) {
 #pragma unroll 1
   for (int k = 0; k < 32; ++k)
     if (bar_try(bar, parity)) return true;

@@ -42,6 +42,7 @@ EXPORTS = [
     "fm_attention_backward",
     "fm_attention_workspace",
     "fm_ops_poll_error",
+    "fm_ops_selftest_wait",
 ]
 
 
@@ -60,6 +61,7 @@ def library() -> C.CDLL:
     L.fm_buckets_map.argtypes, L.fm_buckets_map.restype = [vp, vp], ci
     L.fm_buckets_destroy.argtypes, L.fm_buckets_destroy.restype = [vp], ci
     L.fm_ops_poll_error.argtypes, L.fm_ops_poll_error.restype = [], ci
+    L.fm_ops_selftest_wait.argtypes, L.fm_ops_selftest_wait.restype = [vp], ci
     return L
 
 
@@ -139,6 +141,10 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: float
     (batch,)). A query that sees nothing returns zeros and passes no gradient.
     Keys past k_lens and padding frames are never read into a result.
 
+    Where a wait inside a kernel gave up (after two seconds; never in ordinary
+    running) that call's results are not valid, and the next calls raise FmError
+    until poll_error() has taken the error.
+
     Differentiable in q, k, v and table (once). return_lse: also the log of
     the softmax's sum, (batch, heads, q_len) float32 (no gradient).
     """
@@ -148,7 +154,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: float
 
 def poll_error(device: torch.device | str = "cuda") -> int:
     """Wait for the device, then take and clear the operators' error status:
-    FM_OK, or FM_ERR_KERNEL_TIMEOUT where a bounded wait in a kernel gave up."""
+    FM_OK, or FM_ERR_KERNEL_TIMEOUT where a bounded wait in an attention kernel
+    gave up. Until it is taken attention() and its backward pass raise it; after
+    replays of a recorded graph, which make no call, ask here."""
     with torch.cuda.device(_cuda_device(device)):
-        torch.cuda.synchronize()
         return int(library().fm_ops_poll_error())

@@ -298,3 +298,25 @@ def test_poll_waits_for_every_stream(ops):
         event.record()
     assert ops.library().fm_ops_poll_error() == 0
     assert event.query()
+
+
+def test_a_wait_that_gave_up_is_raised(ops):
+    from mel_spectrogram_gb300 import FM_ERR_KERNEL_TIMEOUT, FM_OK, FmError
+
+    for dtype in TYPES:
+        q, k, v, dy, _ = base.make((1, 140, 140, 2, 2, 64), dtype)
+        want = passes(ops, q, k, v, dy)
+        leaf = q.detach().requires_grad_()
+        out = ops.attention(leaf, k, v)
+        side = torch.cuda.Stream()
+        assert ops.library().fm_ops_selftest_wait(side.cuda_stream) == FM_OK
+        side.synchronize()
+        for _ in range(2):
+            with pytest.raises(FmError) as e:
+                ops.attention(q, k, v)
+            assert e.value.status == FM_ERR_KERNEL_TIMEOUT
+        with pytest.raises(RuntimeError, match="KERNEL_TIMEOUT"):
+            torch.autograd.grad(out, leaf, dy)
+        assert ops.poll_error() == FM_ERR_KERNEL_TIMEOUT
+        assert ops.poll_error() == FM_OK
+        assert all(torch.equal(a, b) for a, b in zip(want, passes(ops, q, k, v, dy)))
