@@ -495,6 +495,11 @@ int64_t whole_arg(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw python_error();
   return v;
 }
+bool flag_arg(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();  // it has no truth value
+  return v != 0;
+}
 void count_args(Py_ssize_t got, Py_ssize_t want) {
   TORCH_CHECK_TYPE(got == want, "expected ", want, " arguments, got ", got);
 }
@@ -537,7 +542,7 @@ PyObject* py_relative_bias(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Tensor table = tensor_arg(v[0], "table", false);
     const int64_t q = whole_arg(v[1]), k = whole_arg(v[2]);
     const int64_t start = v[3] == Py_None ? k - q : whole_arg(v[3]), far = whole_arg(v[4]);
-    const bool both = PyObject_IsTrue(v[5]);
+    const bool both = flag_arg(v[5]);
     Tensor y;
     {
       NoGil free;
@@ -561,12 +566,12 @@ PyObject* py_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     Masks m;
     c->scale = v[3] == Py_None ? NAN : real_arg(v[3]);
     TORCH_CHECK_VALUE(v[3] == Py_None || std::isfinite(c->scale), "scale must be finite");
-    c->causal = PyObject_IsTrue(v[4]);
+    c->causal = flag_arg(v[4]);
     m.prefix = tensor_arg(v[5], "prefix", true);
     c->softcap = real_arg(v[6]);
     const Tensor table = tensor_arg(v[7], "table", true);
     const int64_t far = whole_arg(v[8]);
-    const bool both = PyObject_IsTrue(v[9]), want_lse = PyObject_IsTrue(v[15]);
+    const bool both = flag_arg(v[9]), want_lse = flag_arg(v[15]);
     m.slopes = tensor_arg(v[10], "slopes", true);
     m.q_docs = tensor_arg(v[11], "q_docs", true);
     m.k_docs = tensor_arg(v[12], "k_docs", true);
@@ -599,7 +604,7 @@ PyObject* py_buckets(PyObject*, PyObject* const* v, Py_ssize_t n) {
     count_args(n, 4);
     const c10::Device device(c10::kCUDA, (c10::DeviceIndex)whole_arg(v[0]));
     const int64_t num = whole_arg(v[1]), far = whole_arg(v[2]);
-    return PyLong_FromVoidPtr(buckets_for(device, num, far, PyObject_IsTrue(v[3])));
+    return PyLong_FromVoidPtr(buckets_for(device, num, far, flag_arg(v[3])));
   } catch (const Failure& e) {
     return raise(e);
   }

@@ -320,3 +320,18 @@ def test_a_wait_that_gave_up_is_raised(ops):
         assert ops.poll_error() == FM_ERR_KERNEL_TIMEOUT
         assert ops.poll_error() == FM_OK
         assert all(torch.equal(a, b) for a, b in zip(want, passes(ops, q, k, v, dy)))
+
+
+# ---------------------------------------------------------------------------
+# arguments whose truth value is an error
+
+def test_flags_without_a_truth_value(ops):
+    q = torch.randn(1, 3, 2, 8, device="cuda")
+    t = torch.randn(8, 2, device="cuda")
+    many = torch.ones(2)
+    for call in (lambda: ops.attention(q, q, q, causal=many), lambda: ops.attention(q, q, q, bidirectional=many),
+                 lambda: ops.attention(q, q, q, return_lse=many),
+                 lambda: ops.relative_bias(t, 3, 3, max_distance=9, bidirectional=many),
+                 lambda: ops.bucket_map(8, 9, many)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
