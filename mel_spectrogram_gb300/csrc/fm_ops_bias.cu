@@ -233,12 +233,18 @@ __global__ void __launch_bounds__(256) bucket_sums(const int32_t* ranges, int ma
     if (hi == max_distance || hi > first + count - 1) hi = first + count - 1;
     const int n = hi - lo + 1;
     if (n > 0) {
-      const float* base = part + h * head_stride + (lo - first);
-      const long long total = rows * n;
+      // element t of the bucket: row t / n, column t % n, both followed without a
+      // division (their product may pass 2^32)
+      const int r = threadIdx.x / n, dr = 256 / n, dc = 256 - dr * n;
+      int col = threadIdx.x - r * n;
+      const float* at = part + h * head_stride + (lo - first) + r * row_stride + col;
+      const long long total = rows * n, step = dr * row_stride + dc, next = row_stride - n;
 #pragma unroll 8
       for (long long t = threadIdx.x; t < total; t += 256) {
-        const unsigned r = (unsigned)t / (unsigned)n;
-        s += base[r * row_stride + ((unsigned)t - r * (unsigned)n)];
+        s += *at;
+        at += step;
+        col += dc;
+        if (col >= n) col -= n, at += next;
       }
     }
   }

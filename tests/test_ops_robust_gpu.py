@@ -335,3 +335,23 @@ def test_flags_without_a_truth_value(ops):
                  lambda: ops.bucket_map(8, 9, many)):
         with pytest.raises(RuntimeError, match="ambiguous"):
             call()
+
+
+# ---------------------------------------------------------------------------
+# partial bias gradients beyond 2^32 of a bucket's elements
+
+def test_bias_gradient_of_many_rows(ops):
+    # 65535 batch entries x 33 tiles of queries x 2048 offsets of one bucket; 35 GB of partial sums
+    B, Tq = 65535, 2100
+    q = torch.zeros(B, Tq, 1, 1, device="cuda")
+    k = torch.zeros(1, 2, 1, 1, device="cuda").expand(B, 2, 1, 1)
+    v = torch.tensor([1.0, 0.0], device="cuda").view(1, 2, 1, 1).expand(B, 2, 1, 1)
+    dy = torch.zeros(B, Tq, 1, 1, device="cuda")
+    dy[-1000:] = 1.0
+    table = torch.zeros(4, 1, device="cuda", requires_grad=True)
+    out = ops.attention(q, k, v, table=table, max_distance=2048, q_start=0)
+    (d,) = torch.autograd.grad(out, table, dy)
+    # weights of 1/2: dS is 1/4 and -1/4; bucket 1 gets all pairs but (0, 0), (1, 1) and (0, 1), bucket 3 the last
+    assert d.flatten().tolist() == [0.0, 250.0, 0.0, -250.0]
+    del q, k, v, dy, out
+    torch.cuda.empty_cache()
