@@ -81,22 +81,47 @@ def _compile(src: str, extra: list[str], build_dir: str = BUILD) -> str:
     return r.stderr
 
 
-def _compile_torch() -> str:
-    """The object of fm_torch.cpp; "" where torch is not installed."""
+def _torch_identity() -> str:
+    """What the binding is built against: torch's place and version (without
+    importing it) and Python's; "" where torch is not installed."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.origin:
         return ""
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        return "\n".join([spec.origin, sys.version, f.read()])
+
+
+def _torch_stale(out: str, identity: str) -> bool:
+    """Whether the binding's object is missing, older than its sources or built
+    against another torch."""
+    try:
+        with open(out + ".torch") as f:
+            built = f.read()
+    except OSError:
+        return True
+    return built != identity or _stale(out, [TORCH_SRC, *_headers(), __file__])
+
+
+def _compile_torch() -> str:
+    """The object of fm_torch.cpp; "" where torch is not installed."""
+    identity = _torch_identity()
+    if not identity:
+        return ""
     out = os.path.join(BUILD, "fm_torch.cpp.o")
-    if not _stale(out, [TORCH_SRC, *_headers(), __file__]):
+    if not _torch_stale(out, identity):
         return out
-    inc = os.path.join(os.path.dirname(spec.origin), "include")
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}", f"-isystem{inc}",
-           f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-isystem{cuda}",
-           f"-isystem{sysconfig.get_paths()['include']}", "-c", TORCH_SRC, "-o", out]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-I{INCLUDE}", f"-isystem{inc}", f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+           f"-isystem{cuda}", f"-isystem{sysconfig.get_paths()['include']}", "-c", TORCH_SRC, "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for fm_torch.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    with open(out + ".torch", "w") as f:
+        f.write(identity)
     return out
 
 

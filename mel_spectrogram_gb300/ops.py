@@ -23,7 +23,11 @@ from . import _binding as fb
 if not os.path.exists(fb.LIB_PATH):
     fb.lib()  # raises with the build command
 
-from . import _fm_torch as _C  # noqa: E402
+try:
+    from . import _fm_torch as _C  # noqa: E402
+except ImportError as e:
+    raise ImportError(f"the operators' binding to torch does not load ({e}): build it with "
+                      "`python -m mel_spectrogram_gb300.build` where torch is installed") from e
 
 _C.set_error(fb.FmError)
 
