@@ -338,15 +338,30 @@ __global__ void __launch_bounds__(kTile) bwd_scales(const __grid_constant__ TcPa
   (keys ? k_scale + k_at : q_scale + q_at)[row] = fabsf(e) < 120.f ? exp2f(e) : 1.f;  // of nothing: as it is
 }
 
-// Whether the few-query kernel runs. It takes time with its rows (queries x
-// heads that share a key head, 16 an operand), the tiled kernel with its heads,
-// each a tile of 256 however few queries fill it. Measured, bf16, 32 rows of 3001
-// keys, 4 key heads of 8 heads each: head size 128, 16 queries 136 us against
-// 285, 32 queries 231 against 285; head size 64, 75 and 143 against 234. Where
-// no heads share keys, more than one operand reads the keys again, and either
-// kernel may win: 32 rows, 4 heads, 24 queries, 66 us against 46 at head size 128
-// and 43 against 37 at 64; 16 heads, 156 against 167 and 81 against 136.
-bool takes_step(const AttnParams& p) { return p.q_len <= (p.group >= 4 ? 32 : 16); }
+// Whether the few-query kernel runs. It takes time with its operands of 16 rows
+// (queries x heads that share a key head), the tiled kernel with its heads, each a
+// tile of 256 rows however few queries fill it; a row costs the first less at head
+// size 64 than at 128. Measured, bf16, few-query / tiled in us (batch x key heads x
+// heads that share one, keys):
+//  16 queries: 35 / 38 and 52 / 46 (32x4x1, 3001; size 64 and 128), 63 / 137 and
+//   153 / 167 (32x16x1), 74 / 236 and 138 / 286 (32x4x8), 19 / 17 and 23 / 19
+//   (64x1x2, 800), 14 / 19 and 17 / 21 (1x1x1, 30001).
+//  17 to 32, size 64: 43 / 72 (64x4x1, 3001), 81 / 137 (32x16x1), 41 to 52 / 70
+//   (32x4x2), 29 to 43 / 37 (8x2x8), 28 to 31 / 37 (24x4x1), 41 to 45 / 38
+//   (32x4x1), 21 to 25 / 17 (64x1x2, 800).
+//  17 to 32, size 128: where four or more heads share keys, 98 to 138 / 165 (32x4x4),
+//   17 to 25 / 27 (3x8x8, 600), 55 to 71 / 86 (1x2x32, 12001), but 52 to 66 / 45
+//   (8x2x8) and 45 to 66 / 43 (2x1x64), where the tiled kernel's blocks are one full
+//   wave of the SMs and split no keys; where fewer share, 156 / 167 (32x16x1), but
+//   101 to 114 / 87 (64x4x1), 52 to 64 / 37 (64x4x1, 800), 52 to 105 / 86 (32x4x2).
+//  40 and more: 92 / 71 and 98 / 87 (64x4x1), 51 / 40 and 70 / 49 (40x4x1, 1500),
+//   174 / 235 and 282 / 285 (32x4x8), at 64 queries 253 / 235 and 431 / 286.
+bool takes_step(const AttnParams& p) {
+  if (p.q_len <= 16 || p.q_len > 32) return p.q_len <= 16;
+  const long long blocks = (long long)p.batch * p.heads;
+  const bool one_wave = 2 * blocks > num_sms() && blocks <= num_sms();
+  return p.dim <= 64 || (p.group >= 4 && !one_wave);
+}
 
 int mode_of(const AttnParams& p) {
   if (p.cap > 0.f || p.slopes || !(p.scale > 0.f)) return 2;

@@ -172,3 +172,17 @@ def test_relative_bias_offsets(ops):
     ref.close(out[:, :3], *first["out"], "first rows")
     del out, dy
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# both sides of every limit between the kernels for few queries and in tiles
+
+@pytest.mark.parametrize("dim", [64, 72, 128])
+@pytest.mark.parametrize("Tq", [16, 17, 32, 33])
+def test_choice_of_kernel(ops, Tq, dim):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    # batch entries of heads 4 (2 and 4 of them sharing keys) around half and all of the SMs' blocks
+    for kv_heads in (2, 1):
+        for batch in {sms // 8, sms // 8 + 1, sms // 4, sms // 4 + 1}:
+            q, k, v, _, _ = base.make((batch, Tq, 150, 4, kv_heads, dim), BF16)
+            base.check_attention(ops, q, k, v, f"{batch} {Tq} {kv_heads} {dim}", causal=True)
