@@ -39,7 +39,9 @@ AttnParams params(const fm_attention_args* a) {
   p.dim = (int)a->dim;
   p.causal = a->causal != 0;
   p.scale = (float)a->scale;
-  p.cap = (float)a->softcap;
+  // smaller caps make all scores equal to 32 bits as this one does, but could
+  // round to 0, which means no cap, or leave the range of floats as scale / cap
+  p.cap = a->softcap > 0 ? (float)(a->softcap > 1e-30 ? a->softcap : 1e-30) : 0.f;
   p.q = a->q, p.k = a->k, p.v = a->v;
   p.qs = strides(a->q_s), p.ks = strides(a->k_s), p.vs = strides(a->v_s), p.os = strides(a->out_s);
   p.lse = a->lse;

@@ -111,6 +111,16 @@ def test_large_caps(ops, Tq, softcap, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("softcap", [1e-46, 1e-39, 1e-20, 1e-3])
+@pytest.mark.parametrize("Tq", [4, 129])
+def test_small_caps(ops, Tq, softcap, dtype):
+    q, k, v, dy, _ = base.make((1, Tq, 150, 2, 2, 64), dtype)
+    q[:, 1] = 0  # scores of 0 beside others far beyond the cap
+    base.check_attention(ops, q, k, v, f"cap {softcap}", softcap=softcap)
+    base.check_attention(ops, q, k, v, f"cap {softcap}", dy=dy, softcap=softcap)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("softcap", [30.0, 1e4])
 @pytest.mark.parametrize("Tq", [3, 129])
 def test_caps_between_rows(ops, Tq, softcap, dtype):
