@@ -6,8 +6,8 @@
 // the bias), each recomputing the scores, so that every sum has one owner and
 // one order. Bound by the FP32 pipes' shared-memory operands: 4 x 4 products
 // per thread and step. Small problems are bound by latency: 2 rows of 129
-// frames, 4 heads of 40, train in about 100 us of kernels, five tiles one after
-// another in each.
+// frames, 4 heads of 40, train in 115 us of kernels (forward 27, backward 4, 42
+// and 37, the bias's sums 4), five tiles one after another in each.
 #include "fm_ops_attn.cuh"
 
 #include <cmath>

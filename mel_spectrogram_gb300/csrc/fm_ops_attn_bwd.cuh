@@ -24,8 +24,8 @@
 // products count as well: their 128 x 64 x 16 steps read 6 KB of shared memory
 // for 32 cycles of arithmetic (the tensor unit takes 128 bytes a cycle).
 // Measured: 8 packed rows of 3001 frames, 8 heads of 64, bf16, bias of 320
-// buckets up to 800: 204 us for the queries, 183 for the keys; 8 rows of 1292,
-// 16 heads of 128 on 4 key heads, f16, causal, capped: 170 and 235.
+// buckets up to 800: 205 us for the queries, 186 for the keys; 8 rows of 1292,
+// 16 heads of 128 on 4 key heads, f16, causal, capped: 177 and 237.
 #pragma once
 
 #include "fm_ops_attn_tc.cuh"

@@ -13,7 +13,7 @@
 // tensor unit at dim 128) for 2 x 16384 exponentials, and takes about 3200: a
 // tile's own chain (scores, 1500 cycles of softmax, products) is longer than
 // its share of the tensor unit, and tensor memory has no room for a third score
-// buffer beside two outputs of 128 columns. Measured: 372 us for 8 rows of up
+// buffer beside two outputs of 128 columns. Measured: 374 us for 8 rows of up
 // to 3001 frames, 16 heads of 128, bf16 (447 GFLOP: 1200 TFLOP/s, 0.61 of the
 // measured matrix rate). With a bias by distance at head size 64 the shared
 // reads of the bias, the exponentials and the products want about 1000 cycles

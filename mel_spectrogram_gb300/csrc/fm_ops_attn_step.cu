@@ -11,7 +11,7 @@
 // (with cp.async they took a third of 633 instructions a tile, which is what
 // bound the kernel, at 38 % of the bandwidth). Warps join through shared
 // memory, blocks through the join kernel. Measured, with the join: 293 MB of 64
-// caches of up to 3001 frames in 62 us (0.71 of the measured bandwidth), 184 MB
+// caches of up to 3001 frames in 63 us (0.70 of the measured bandwidth), 184 MB
 // of an hour's 360001 frames in 43 (0.64), in 297 splits. What is left is the
 // chain from a tile's arrival over its two products to the next: twelve warps an
 // SM, as many as the registers hold, issue in 0.32 of the cycles.

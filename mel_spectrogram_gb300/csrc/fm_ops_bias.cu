@@ -77,7 +77,7 @@ __host__ __device__ inline int fill_pitch(int max_distance) {
 // stores. A pack far from the diagonal is one value, one near it one shared
 // read; an element at a time (an index, two clamps and a 2-byte read each) the
 // kernel took 86 us for 16 x 3001 x 3001 in 16 bits, bound by instructions; so
-// it takes 54 (288 MB, 5.3 TB/s).
+// it takes 56 (288 MB, 5.1 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(kFillThreads) bias_fill(const BiasParams p) {
   extern __shared__ __align__(16) unsigned char raw[];
@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(kFillThreads) bias_fill(const BiasParams p) {
 // offset and walks down its diagonal over the rows of a chunk, 16 reads under
 // way, so neighbouring threads read neighbouring elements and a sum stays in
 // one register; beyond, where one bucket holds all, the last block sums whole
-// stretches of rows with 16-byte reads. No atomics, one fixed order. 95 us for
-// 16 x 3001 x 3001 in 16 bits with 800 places either way (288 MB, 3.0 TB/s); by
+// stretches of rows with 16-byte reads. No atomics, one fixed order. 86 us for
+// 16 x 3001 x 3001 in 16 bits with 800 places either way (288 MB, 3.3 TB/s); by
 // themselves the walk takes 46 of a cold cache and the stretches 57. (The band
 // staged in shared memory instead took 62 us where the walk takes 35.)
 template <typename T>

@@ -6,7 +6,7 @@
 // forward pass and x and dy once each in the backward pass. The variance is
 // the mean of squared deviations from the finished mean (two passes over
 // registers), never a difference of sums. Measured for 82688 rows of 1024 in
-// bf16: forward 62 us (5.4 TB/s), backward 113 (4.5 TB/s) and 4 for its columns.
+// bf16: forward 60 us (5.6 TB/s), backward 113 (4.5 TB/s) and 6 for its columns.
 #include "fm_ops.cuh"
 
 namespace fm {
@@ -160,10 +160,11 @@ __global__ void __launch_bounds__(kBlock) norm_fwd_wide(const NormParams p) {
 //
 // A warp keeps a row's 64 sums per lane of 32 elements, so registers leave
 // twelve warps an SM; their reads and the arithmetic between them take turns.
-// Measured for 82688 rows of 1024 in bf16 (508 MB): 100 us in blocks of four
-// warps, three to an SM; 127 in blocks of eight (one and a half fit); 103 with
-// the next row's reads ahead (254 registers, eight warps); 106 to 123 with two
-// or four warps a row, whose sums then need barriers.
+// Compared for 82688 rows of 1024 in bf16 (508 MB), by itself over and over on the
+// same inputs, which leaves some of them in L2 (113 us from a cold one): 100 us in
+// blocks of four warps, three to an SM; 127 in blocks of eight (one and a half
+// fit); 103 with the next row's reads ahead (254 registers, eight warps); 106 to
+// 123 with two or four warps a row, whose sums then need barriers.
 constexpr int kBwdWarps = 4;
 template <int TPR, int E>  // threads of a block, and blocks meant to fit an SM
 constexpr int kBwdThreads = TPR == 32 ? 32 * kBwdWarps : TPR;

@@ -5,7 +5,9 @@ Functions on CUDA tensors with autograd support. Every computation runs in the
 library's own kernels, on the current stream of the tensors' device;
 ``_fm_torch`` (csrc/torch/fm_torch.cpp) checks arguments, allocates outputs and
 workspaces and builds the autograd nodes. Bad arguments raise ValueError or
-TypeError, a failing library call FmError.
+TypeError, a failing library call FmError; second derivatives raise RuntimeError,
+forward-mode derivatives and traces NotImplementedError. Inputs, masks included,
+that are changed in place before the backward pass raise there.
 
     y = layer_norm(x, weight, bias)                      # (..., width)
     b = relative_bias(table, q_len, k_len)               # (heads, q_len, k_len)
