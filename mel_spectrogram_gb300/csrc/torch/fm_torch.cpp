@@ -46,8 +46,17 @@ int type_of(const Tensor& t, const char* name) {
   }
   TORCH_CHECK_TYPE(false, name, ": dtype ", t.scalar_type(), " not supported (float32, float16, bfloat16)");
 }
-const void* ptr(const Tensor& t) { return t.defined() ? t.const_data_ptr() : nullptr; }
-void* mut(const Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; }
+// A tensor's memory, NULL for an absent tensor. One without memory of its own (a
+// fake tensor, a wrapper around others) is refused: the library would take it for
+// absent.
+template <typename P>
+P* its_memory(P* p, const Tensor& t) {
+  TORCH_CHECK_VALUE(p != nullptr || t.numel() == 0, "a tensor of ", t.numel(),
+                    " elements has no memory of its own (a fake or wrapper tensor): the operators need the data");
+  return p;
+}
+const void* ptr(const Tensor& t) { return t.defined() ? its_memory(t.const_data_ptr(), t) : nullptr; }
+void* mut(const Tensor& t) { return t.defined() ? its_memory(t.mutable_data_ptr(), t) : nullptr; }
 
 void need_cuda(const Tensor& t, const char* name, const Tensor& like) {
   if (!t.defined()) return;
@@ -174,7 +183,7 @@ struct NormNode : torch::autograd::Function<NormNode> {
       a.x_stride = xs, a.dy_stride = dys, a.dx_stride = width;
       a.eps = ctx->saved_data["eps"].toDouble();
       a.x = ptr(x2), a.weight = ptr(weight), a.dy = ptr(dy2);
-      a.mean = (float*)st.const_data_ptr(), a.rstd = a.mean + rows;
+      a.mean = (float*)ptr(st), a.rstd = a.mean + rows;
       a.dx = mut(dx), a.dweight = mut(dw), a.dbias = mut(db);
       OnDevice on(x);
       Tensor work;

@@ -365,3 +365,44 @@ def test_bias_gradient_of_many_rows(ops):
     assert d.flatten().tolist() == [0.0, 250.0, 0.0, -250.0]
     del q, k, v, dy, out
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# tensors without memory of their own: an absent pointer must not read as an
+# absent argument
+
+class Wrapper(torch.Tensor):
+    """A subclass around another tensor, as distributed and fake tensors are."""
+
+    @staticmethod
+    def __new__(cls, t):
+        return torch.Tensor._make_wrapper_subclass(cls, t.shape, dtype=t.dtype, device=t.device)
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise NotImplementedError(func)
+
+
+def test_tensors_without_memory(ops):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    x, w = torch.randn(5, 16, device="cuda"), torch.randn(16, device="cuda")
+    q, k, v, _, g = base.make((2, 6, 6, 2, 1, 16), F32)
+    ids = torch.zeros(2, 6, dtype=torch.int32, device="cuda")
+    table = base.randn(g, 8, 2)
+    extra = {"q_docs": ids, "k_docs": ids, "k_lens": base.lengths(3, 4), "q_start": base.lengths(0, 1),
+             "prefix": base.lengths(3, 4), "slopes": torch.rand(2, device="cuda"), "table": table}
+    calls = [lambda: ops.layer_norm(x, Wrapper(w)), lambda: ops.layer_norm(x, w, Wrapper(w)),
+             lambda: ops.layer_norm(Wrapper(x), w), lambda: ops.relative_bias(Wrapper(table), 4, 5, max_distance=16),
+             lambda: ops.attention(Wrapper(q), k, v)]
+    for name in extra:
+        kw = dict(extra, **{name: Wrapper(extra[name])})
+        calls.append(lambda kw=kw: ops.attention(q, k, v, causal=True, max_distance=16, **kw))
+    for call in calls:
+        with pytest.raises(ValueError, match="memory"):
+            call()
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        for call in (lambda: ops.layer_norm(x, w), lambda: ops.relative_bias(table, 4, 5, max_distance=16),
+                     lambda: ops.attention(q, k, v)):
+            with pytest.raises(ValueError, match="memory"):
+                call()
