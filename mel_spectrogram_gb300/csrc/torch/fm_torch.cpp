@@ -86,6 +86,10 @@ Maybe maybe(const Tensor& t) { return t.defined() ? Maybe(t) : Maybe(); }
 Tensor or_none(const Maybe& t) { return t ? *t : Tensor(); }
 bool wants_grad(const Tensor& t) { return t.defined() && t.requires_grad(); }
 
+// t with the signs that its values have: a view of a conjugate's imaginary part
+// may hold them as a flag, which its memory does not show.
+Tensor signed_as_is(const Tensor& t) { return t.defined() && t.is_neg() ? t.resolve_neg() : t; }
+
 // Traces are refused: the calls are no operators of torch's own registry, so that
 // a trace would hold their outputs' allocations, or one call's results, alone.
 void no_trace(const char* name) {
@@ -168,7 +172,7 @@ struct NormNode : torch::autograd::Function<NormNode> {
       at::NoGradGuard no_grad;
       const int64_t width = x.size(-1), rows = x.numel() / width;
       auto [x2, xs] = rows_of(x, width);
-      auto [dy2, dys] = rows_of(grads[0], width);
+      auto [dy2, dys] = rows_of(signed_as_is(grads[0]), width);
       const auto options = x.options().requires_grad(false);
       const bool f32 = weight.defined() ? weight.scalar_type() == at::kFloat : ctx->saved_data["bias_f32"].toBool();
       const auto ptype = f32 ? options.dtype(at::kFloat) : options;
@@ -198,9 +202,10 @@ struct NormNode : torch::autograd::Function<NormNode> {
   }
 };
 
-Tensor layer_norm(const Tensor& x, Tensor weight, Tensor bias, double eps) {
+Tensor layer_norm(Tensor x, Tensor weight, Tensor bias, double eps) {
   no_trace("layer_norm");
   no_tangents("layer_norm", x, weight, bias);
+  x = signed_as_is(x), weight = signed_as_is(weight), bias = signed_as_is(bias);
   TORCH_CHECK_VALUE(x.is_cuda(), "x must be a CUDA tensor (the operators run only on the GPU)");
   need_cuda(weight, "weight", x);
   need_cuda(bias, "bias", x);
@@ -272,7 +277,7 @@ struct BiasNode : torch::autograd::Function<BiasNode> {
     Tensor dtable;
     {
       at::NoGradGuard no_grad;
-      const Tensor dout = grads[0].contiguous();
+      const Tensor dout = signed_as_is(grads[0]).contiguous();
       dtable = at::empty({v[4], v[5]}, dout.options().requires_grad(false));
       fm_relative_bias_args a{};
       a.heads = v[5], a.q_len = v[1], a.k_len = v[2], a.q_start = v[3];
@@ -293,6 +298,7 @@ struct BiasNode : torch::autograd::Function<BiasNode> {
 Tensor relative_bias(Tensor table, int64_t q_len, int64_t k_len, int64_t q_start, int64_t far, bool both) {
   no_trace("relative_bias");
   no_tangents("relative_bias", table);
+  table = signed_as_is(table);
   TORCH_CHECK_VALUE(table.is_cuda(), "table must be a CUDA tensor (the operators run only on the GPU)");
   check_table(table);
   TORCH_CHECK_VALUE(q_len >= 0 && k_len >= 0, "q_len and k_len must not be negative");
@@ -401,7 +407,7 @@ struct AttentionNode : torch::autograd::Function<AttentionNode> {
     Tensor dq, dk, dv, dtable;
     {
       at::NoGradGuard no_grad;
-      const Tensor dout = gradient_rows(grads[0]);
+      const Tensor dout = gradient_rows(signed_as_is(grads[0]));
       const auto dense = q.options().requires_grad(false).memory_format(at::MemoryFormat::Contiguous);
       dq = at::empty(q.sizes(), dense);
       dk = at::empty(k.sizes(), dense);
@@ -427,13 +433,15 @@ Tensor int32_of(const Tensor& t, const char* name, at::IntArrayRef shape, const 
   need_cuda(t, name, q);
   TORCH_CHECK_TYPE(t.scalar_type() == at::kInt, name, ": dtype ", t.scalar_type(), ", expected int32");
   TORCH_CHECK_VALUE(t.sizes() == shape, name, " has shape ", t.sizes(), ", expected ", shape);
-  return t.contiguous();
+  return signed_as_is(t).contiguous();
 }
 
 std::tuple<Tensor, Tensor> attention(Tensor q, Tensor k, Tensor v, Tensor table, const c10::intrusive_ptr<Call>& c,
                                      Masks m, int64_t far, bool both, bool want_lse) {
   no_trace("attention");
   no_tangents("attention", q, k, v, table, m.slopes);
+  q = signed_as_is(q), k = signed_as_is(k), v = signed_as_is(v), table = signed_as_is(table);
+  m.slopes = signed_as_is(m.slopes);
   TORCH_CHECK_VALUE(q.is_cuda(), "q must be a CUDA tensor (the operators run only on the GPU)");
   need_cuda(k, "k", q);
   need_cuda(v, "v", q);

@@ -406,3 +406,29 @@ def test_tensors_without_memory(ops):
                      lambda: ops.attention(q, k, v)):
             with pytest.raises(ValueError, match="memory"):
                 call()
+
+
+# ---------------------------------------------------------------------------
+# views whose sign is a flag
+
+def test_negated_views(ops):
+    def same(call, inputs, dy):
+        for n in range(len(inputs) + 1):
+            got = []
+            for flip in (lambda t: torch._neg_view(t), lambda t: -t):
+                args = [flip(t) if m == n else t.clone() for m, t in enumerate(inputs)]
+                leaves = [t.detach().requires_grad_() for t in args]
+                out = call(*leaves)
+                got.append([out.detach(), *torch.autograd.grad(out, leaves, flip(dy) if n == len(inputs) else dy),
+                            call(*args)])
+            for a, b in zip(*got):
+                assert torch.equal(a, b), n
+
+    q, k, v, dy, g = base.make((1, 40, 40, 2, 2, 64), BF16)
+    table = base.randn(g, 8, 2, dtype=BF16)
+    same(lambda x, w, b: ops.layer_norm(x, w, b), [base.randn(g, 7, 64), base.randn(g, 64), base.randn(g, 64)],
+         base.randn(g, 7, 64))
+    same(lambda t: ops.relative_bias(t, 4, 5, max_distance=16), [table], base.randn(g, 2, 4, 5, dtype=BF16))
+    same(lambda q, k, v, t: ops.attention(q, k, v, table=t, max_distance=16), [q, k, v, table], dy)
+    slopes = torch.rand(2, device="cuda")
+    assert torch.equal(ops.attention(q, k, v, slopes=torch._neg_view(slopes)), ops.attention(q, k, v, slopes=-slopes))
