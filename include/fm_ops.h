@@ -330,7 +330,8 @@ int64_t fm_gated_workspace(const fm_gated_args* args, int backward);
  *             forward leaves (NULL: not wanted) and the backward reads.
  *   workspace : fm_scan_workspace() bytes, 16-byte aligned, the same for both
  *             directions; without it, or with fewer bytes, few channels of long rows
- *             take longer (and sums are joined in another order).
+ *             take longer (and sums are joined in another order). Not touched where
+ *             fm_scan_workspace() is 0.
  */
 typedef struct {
   int64_t batch, frames, channels;

@@ -29,7 +29,9 @@ ScanParams params(const fm_scan_args* a) {
   p.x = a->x, p.g = a->gate;
   p.lens = a->lens, p.docs = a->docs;
   p.marks = a->marks;
-  if (a->workspace_bytes > 0 && a->workspace_bytes >= fm_scan_workspace(a)) p.sums = (float2*)a->workspace;
+  // calls that need none take none: what they were handed may hold less than they would write
+  const int64_t need = fm_scan_workspace(a);
+  if (need > 0 && a->workspace_bytes >= need) p.sums = (float2*)a->workspace;
   return p;
 }
 }  // namespace
