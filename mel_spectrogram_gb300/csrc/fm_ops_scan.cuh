@@ -948,7 +948,8 @@ struct Kernels {
   }
   static long long groups(const ScanParams& p) { return p.batch * ((p.channels + S::CB - 1) / S::CB); }
   // Clusters of n blocks that the device runs at once, 0 where it takes none of this
-  // size: asked for once.
+  // size: asked for once. A question that fails is none of its answers: the next call asks
+  // again.
   static int at_once(int n) {
     static std::atomic<int> known[64][kMaxCluster + 1];  // 1 more than the answer
     int dev = 0;
@@ -960,7 +961,7 @@ struct Kernels {
     const cudaLaunchConfig_t cfg = config(n, n, &attr, nullptr);
     if (!ready(k, n) || cudaOccupancyMaxActiveClusters(&v, k, &cfg) != cudaSuccess || v < 0) {
       cudaGetLastError();
-      v = 0;
+      return 0;
     }
     known[dev][n].store(v + 1, std::memory_order_relaxed);
     return v;
@@ -979,7 +980,7 @@ struct Kernels {
   // us with stretches, 538 without.
   static Split split(const ScanParams& p) {
     const long long tiles = (p.frames + S::kTile - 1) / S::kTile;
-    Split best{1, 1LL << 62};
+    Split best{1, 1LL << 58};  // consider() takes six times this
     for (int n = 1; n <= kMaxCluster && n <= tiles; ++n) {
       const int slots = at_once(n);
       if (slots == 0) continue;

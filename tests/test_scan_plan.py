@@ -86,3 +86,29 @@ def run(tmp_path, program, *args):
 def test_stretches_stay_within_the_workspace(tmp_path):
     for r in run(tmp_path, WORKSPACES, "16", "8", "2"):
         assert r.returncode == 0, r.stdout + r.stderr
+
+
+# a question that failed once is asked again; one that was answered is not
+FAILURES = r"""
+int main(int, char**) {
+  const fm_scan_args a = args_of(1, 360001, 8, 1 << 20);
+  const scan::ScanParams p = params(&a);
+  fails = true;
+  const scan::Split none = split_of<false>(p);
+  if (none.ranks != 1 || none.stretches != 1 || none.rounds <= 0) return 1;
+  int before = asked;
+  fails = false;
+  const scan::Split some = split_of<false>(p);
+  if (asked == before) return 2;
+  before = asked;
+  const scan::Split again = split_of<false>(p);
+  if (asked != before) return 3;
+  printf("%d blocks, %d stretches\n", some.ranks, some.stretches);
+  return some.stretches > 1 && again.stretches == some.stretches && again.ranks == some.ranks ? 0 : 4;
+}
+"""
+
+
+def test_failed_questions_are_asked_again(tmp_path):
+    (r,) = run(tmp_path, FAILURES, "")
+    assert r.returncode == 0, (r.returncode, r.stdout, r.stderr)
