@@ -27,10 +27,13 @@ struct GatedParams {
 };
 
 __device__ __forceinline__ float sigmoid_of(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// The normal distribution's integral up to g, by erfc: 1 + erf of a g far below zero would
+// leave none of its digits (g = -5.5: half of it, -6: nothing).
+__device__ __forceinline__ float normal_integral(float g) { return 0.5f * erfcf(g * -0.70710678118654752f); }
 template <int ACT>
 __device__ __forceinline__ float act_of(float g) {
   if (ACT == FM_ACT_SILU) return g * sigmoid_of(g);
-  if (ACT == FM_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+  if (ACT == FM_ACT_GELU) return g * normal_integral(g);
   if (ACT == FM_ACT_SIGMOID) return sigmoid_of(g);
   return g > 0.f || g != g ? g : 0.f;
 }
@@ -42,7 +45,7 @@ __device__ __forceinline__ void act_and_slope(float g, float& a, float& slope) {
     a = g * s;
     slope = s * (1.f + g * (1.f - s));
   } else if (ACT == FM_ACT_GELU) {
-    const float c = 0.5f * (1.f + erff(g * 0.70710678118654752f));
+    const float c = normal_integral(g);
     a = g * c;
     slope = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), c);
   } else if (ACT == FM_ACT_SIGMOID) {

@@ -1,0 +1,89 @@
+"""The gated linear layer where its activation, or what it is multiplied with, is far from
+one: bounds relative to what comes out, not to the largest that could."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from tests import recurrent_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+TYPES = [F32, F16, BF16]
+E = ref.E
+# f32: the FP32 pipes; 16 bits: up to 32 rows by the few rows' kernel, above by the matrix unit's
+ROWS = [1, 20, 40]
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from mel_spectrogram_gb300 import ops
+
+    return ops
+
+
+def one_unit_each(g, u, rows, dtype):
+    """x and weights of width 8 whose projections are g and u themselves, one value a unit."""
+    x = torch.zeros(rows, 8, device="cuda", dtype=dtype)
+    x[:, 0] = 1
+    wg, wu = (torch.zeros(len(g), 8, device="cuda", dtype=dtype) for _ in range(2))
+    wg[:, 0], wu[:, 0] = g.to(dtype), u.to(dtype)
+    return x, wg, wu
+
+
+def largest_of(dtype):
+    return {F32: 2.0 ** 100, F16: 2.0 ** 14, BF16: 2.0 ** 100}[dtype]
+
+
+def lift(v, dtype):
+    """Powers of two that bring the magnitudes v to about one, as far as the type has them."""
+    return torch.exp2(-torch.log2(v.abs()).round()).clamp(max=largest_of(dtype))
+
+
+def act(g, kind):
+    """The activation, its slope, and the magnitude of the slope's terms."""
+    if kind == "gelu":
+        c, pdf = 0.5 * torch.erfc(-g * math.sqrt(0.5)), torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+        return g * c, c + g * pdf, c + (g * pdf).abs()
+    p, q = torch.sigmoid(g), torch.sigmoid(-g)
+    if kind == "sigmoid":
+        return p, p * q, p * q
+    return g * p, p + g * p * q, p + (g * p * q).abs()
+
+
+def check_act(ops, kind, g, rows, dtype, rel, train=True):
+    """act(g) u and, by dh of one row, dg and du themselves; rel(g): the relative error in 32 bits."""
+    g = g.to(dtype).double()
+    a, slope, terms = act(g, kind)
+    unit, tiny = ref.U[dtype], ref.TINY[dtype]
+    u = lift(a, dtype)
+    x, wg, wu = one_unit_each(g, u, rows, dtype)
+    h = ops.gated_linear(x, wg, wu, kind)
+    want = a * u
+    ref.close(h, want.expand(rows, -1), ((unit + rel(g)) * want.abs() + tiny).expand(rows, -1), f"{kind}: h")
+    if not train:
+        return
+    # dw_gate's first column is dg of that row, dw_up's is du
+    u = lift(slope, dtype)
+    x, wg, wu = one_unit_each(g, u, rows, dtype)
+    leaves = [t.requires_grad_() for t in (x, wg, wu)]
+    dh = torch.zeros(rows, len(g), device="cuda", dtype=dtype)
+    dh[0] = 1
+    dg, du = (t[:, 0] for t in torch.autograd.grad(ops.gated_linear(*leaves, kind), leaves[1:], dh))
+    # rounded to the type before the product and after it
+    ref.close(dg, u * slope, 2 * unit * (u * slope).abs() + rel(g) * u * terms + 2 * tiny, f"{kind}: dg")
+    ref.close(du, a, (2 * unit + rel(g)) * a.abs() + 2 * tiny, f"{kind}: du")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", ROWS)
+def test_gelu_of_what_is_far_below_zero(ops, rows, dtype):
+    # erfc's relative slope is x^2 2 + 1 = g^2 + 1 times its argument's two roundings, its own
+    # error 4 of its last places; on the matrix unit's side exp(-g^2 / 2) with three
+    # roundings of its exponent, a polynomial and two approximate instructions
+    g = -torch.linspace(0.25, 8, 256, device="cuda")
+    check_act(ops, "gelu", g, rows, dtype, lambda g: (2 * g * g + 32) * E)
+    check_act(ops, "gelu", -g, rows, dtype, lambda g: 32 * E)
