@@ -26,7 +26,18 @@ struct GatedParams {
   void *h, *dx, *dwg, *dwu;
 };
 
-__device__ __forceinline__ float sigmoid_of(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// 1 / (1 + e^-g) and what it lacks of one, each to a few of its last places on both sides:
+// by e^-|g|, which does not overflow, and an exponential that rounds its argument once
+// (the fast one is off by 50 last places at g = -40).
+__device__ __forceinline__ float sigmoid_of(float g) {
+  const float e = expf(-fabsf(g));
+  return (g < 0.f ? e : 1.f) / (1.f + e);
+}
+__device__ __forceinline__ float sigmoid_of(float g, float& rest) {
+  const float e = expf(-fabsf(g)), one = 1.f / (1.f + e);
+  rest = g < 0.f ? one : e * one;
+  return g < 0.f ? e * one : one;
+}
 // The normal distribution's integral up to g, by erfc: 1 + erf of a g far below zero would
 // leave none of its digits (g = -5.5: half of it, -6: nothing).
 __device__ __forceinline__ float normal_integral(float g) { return 0.5f * erfcf(g * -0.70710678118654752f); }
@@ -41,16 +52,18 @@ __device__ __forceinline__ float act_of(float g) {
 template <int ACT>
 __device__ __forceinline__ void act_and_slope(float g, float& a, float& slope) {
   if (ACT == FM_ACT_SILU) {
-    const float s = sigmoid_of(g);
+    float rest;
+    const float s = sigmoid_of(g, rest);
     a = g * s;
-    slope = s * (1.f + g * (1.f - s));
+    slope = s * (1.f + g * rest);
   } else if (ACT == FM_ACT_GELU) {
     const float c = normal_integral(g);
     a = g * c;
-    slope = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), c);
+    slope = fmaf(g * 0.39894228040143268f, expf(-0.5f * g * g), c);
   } else if (ACT == FM_ACT_SIGMOID) {
-    a = sigmoid_of(g);
-    slope = a * sigmoid_of(-g);
+    float rest;
+    a = sigmoid_of(g, rest);
+    slope = a * rest;
   } else {
     a = g > 0.f || g != g ? g : 0.f;
     slope = g > 0.f ? 1.f : 0.f;

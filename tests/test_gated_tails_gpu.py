@@ -87,3 +87,11 @@ def test_gelu_of_what_is_far_below_zero(ops, rows, dtype):
     g = -torch.linspace(0.25, 8, 256, device="cuda")
     check_act(ops, "gelu", g, rows, dtype, lambda g: (2 * g * g + 32) * E)
     check_act(ops, "gelu", -g, rows, dtype, lambda g: 32 * E)
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("kind", ["silu", "sigmoid"])
+def test_exponentials_in_32_bits(ops, kind, rows):
+    # exp is off by two of its last places, then a sum, a division and two products
+    g = torch.linspace(-80, 80, 321, device="cuda")
+    check_act(ops, kind, g, rows, F32, lambda g: 16 * E)
