@@ -250,10 +250,16 @@ __device__ __forceinline__ void tie(uint32_t* r) {
 // ---- activations of pairs -----------------------------------------------------
 __device__ __forceinline__ float2 pair_of(const uint32_t* v) { return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])); }
 __device__ __forceinline__ void set_pair(uint32_t* v, float2 x) { v[0] = __float_as_uint(x.x), v[1] = __float_as_uint(x.y); }
-__device__ __forceinline__ float2 sigmoids(float2 g) {
+// and e = exp(-g)
+__device__ __forceinline__ float2 sigmoids(float2 g, float2& e) {
   g = mul2(g, both(-kLog2e));
-  const float2 d = add2(make_float2(ex2(g.x), ex2(g.y)), both(1.f));
+  e = make_float2(ex2(g.x), ex2(g.y));
+  const float2 d = add2(e, both(1.f));
   return make_float2(rcp(d.x), rcp(d.y));
+}
+__device__ __forceinline__ float2 sigmoids(float2 g) {
+  float2 e;
+  return sigmoids(g, e);
 }
 // The normal distribution's integral up to g, and e = exp(-g^2 / 2): of |g| from 1, or of
 // g itself, erfc(|g| / sqrt 2) / 2 = e t P(t) with t = 1 / (1 + 0.304 |g|); P of degree 7
@@ -289,11 +295,17 @@ __device__ __forceinline__ float2 acts(float2 g) {
 }
 template <int ACT>
 __device__ __forceinline__ void acts_and_slopes(float2 g, float2& a, float2& slope) {
-  if (ACT == FM_ACT_SILU || ACT == FM_ACT_SIGMOID) {
+  if (ACT == FM_ACT_SILU) {
     const float2 s = sigmoids(g), r = fma2(s, both(-1.f), both(1.f));
-    a = ACT == FM_ACT_SILU ? mul2(g, s) : s;
-    // s + g s (1 - s), or s (1 - s)
-    slope = ACT == FM_ACT_SILU ? fma2(a, r, s) : mul2(s, r);
+    a = mul2(g, s);
+    slope = fma2(a, r, s);  // s + g s (1 - s)
+  } else if (ACT == FM_ACT_SIGMOID) {
+    // s (1 - s). Above zero 1 - s is e^-g s: taken from one, it would be 1 % off at g = 12
+    // and nothing from 17 on.
+    float2 e;
+    a = sigmoids(g, e);
+    const float2 r = fma2(a, both(-1.f), both(1.f)), q = mul2(e, a);
+    slope = mul2(a, make_float2(g.x > 0.f ? q.x : r.x, g.y > 0.f ? q.y : r.y));
   } else if (ACT == FM_ACT_RELU) {
     a = positive(g);
     slope = make_float2(g.x > 0.f ? 1.f : 0.f, g.y > 0.f ? 1.f : 0.f);

@@ -95,3 +95,12 @@ def test_exponentials_in_32_bits(ops, kind, rows):
     # exp is off by two of its last places, then a sum, a division and two products
     g = torch.linspace(-80, 80, 321, device="cuda")
     check_act(ops, kind, g, rows, F32, lambda g: 16 * E)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", ROWS)
+def test_slopes_of_saturated_sigmoids(ops, rows, dtype):
+    # the exponent g log2(e) with two roundings, two approximate instructions, two products
+    g = torch.linspace(-11 if dtype is F16 else -40, 11 if dtype is F16 else 40, 161, device="cuda")
+    check_act(ops, "sigmoid", g, rows, dtype, lambda g: (2 * g.abs() + 24) * E)
+    check_act(ops, "silu", g, rows, dtype, lambda g: (2 * g.abs() + 24) * E)
