@@ -113,10 +113,10 @@ __global__ void __launch_bounds__(32 * kWarps) gated_step(const GatedParams p) {
       const long long r = j * 8 + l % 4 * 2 + k;
       if (r >= p.rows) continue;
       float g = g2[k], u = u2[k];
-      if (sizeof(T) == 1) {
+      if (sizeof(T) == 1) {  // one after the other: their product may be out of range where g is not
         const float xs = p.x_scales[r];
-        g *= xs * p.g_scales[f];
-        u *= xs * p.u_scales[f];
+        g = g * xs * p.g_scales[f];
+        u = u * xs * p.u_scales[f];
       }
       float h = 0.f;
       if (p.act == FM_ACT_SILU) h = act_of<FM_ACT_SILU>(g);

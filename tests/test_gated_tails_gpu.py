@@ -104,3 +104,25 @@ def test_slopes_of_saturated_sigmoids(ops, rows, dtype):
     g = torch.linspace(-11 if dtype is F16 else -40, 11 if dtype is F16 else 40, 161, device="cuda")
     check_act(ops, "sigmoid", g, rows, dtype, lambda g: (2 * g.abs() + 24) * E)
     check_act(ops, "silu", g, rows, dtype, lambda g: (2 * g.abs() + 24) * E)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [3, 20, 40])
+def test_scales_far_apart(ops, rows, dtype):
+    # scales of rows and of weights whose product passes the range of floats at either end
+    # while the projections do not: a sum that is 0 stays 0, a small one keeps its digits
+    K, F = 32, 24
+    eight = torch.float8_e4m3fn
+    x, wg, wu = torch.zeros(rows, K, device="cuda"), torch.zeros(F, K, device="cuda"), torch.zeros(F, K, device="cuda")
+    x[:, ::2], wg[1, 1::2], wu[1] = 448, 448, 1    # unit 1: a sum of nothing but zeros
+    wg[2], wu[2] = 448, 448
+    sx, sg, su = (torch.ones(n, device="cuda") for n in (rows, F, F))
+    sx[0], sg[1], su[1] = 1e30, 1e10, 1e-30        # 1e40 times 0
+    sx[1], sg[2], su[2] = 1e-10, 1e-30, 1e37       # 1e-40 times 3e6: g = 3.2e-34, u = 3.2e33
+    h = ops.gated_linear_8bit(x.to(eight), sx, wg.to(eight), sg, wu.to(eight), su, "silu", dtype)
+    assert (h[0, 1] == 0).all()
+    total = 448.0 * 448.0 * (K // 2)
+    g, u = (total * float(sx[1].double()) * float(s[2].double()) for s in (sg, su))
+    want = torch.tensor(g / 2 * u, dtype=torch.float64)
+    # four products, the sum (exact), the activation's few roundings, one to the type
+    ref.close(h[1, 2], want, (24 * E + ref.U[dtype]) * want, "far apart")
