@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 
 #include "fm_ops_rows.cuh"
+#include "fm_tc.cuh"
 
 namespace fm {
 namespace {
@@ -66,6 +67,23 @@ __device__ __forceinline__ float scale_of(unsigned largest) {
   return largest >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
                                 : fmaxf(__uint_as_float(largest) / kLargest, 1.17549435e-38f);
 }
+
+// v / scale by the reciprocal's two halves: it is known to 46 bits (29 for scales beyond
+// 2^120), so that the one rounding of the sum gives the rounded quotient but for borders
+// closer than that. The first half is rounded down, which keeps both of one sign and a -0
+// one. 82688 rows of 1024 in bf16 with the norm (without): 104 us (45), by the rounded reciprocal
+// alone, whose quotients are off by one and a half last places, 104 (43), by divisions 125 (55).
+struct Inverse {
+  float first, rest;
+  __device__ explicit Inverse(float scale) {
+    first = __frcp_rd(scale);
+    rest = fmaf(-first, scale, 1.f) * first;
+  }
+  __device__ float2 times(float2 v) const {
+    return tc::fma2(v, tc::both(first), tc::mul2(v, tc::both(rest)));
+  }
+  __device__ float times(float v) const { return fmaf(v, first, v * rest); }
+};
 
 // total = x + residual as it is held
 template <typename T>
@@ -146,18 +164,21 @@ __global__ void __launch_bounds__(kBlock) rms_fwd(const RmsParams p) {
       for (int k = 0; k < VEC; ++k) m = max(m, abs_bits(v[n][k]));
     const float scale = scale_of(row_max<TPR>(m, (unsigned*)red));
     if (lane == 0) p.scales[row] = scale;
-    const float inv = 1.f / scale;
+    const Inverse inv(scale);
     E4M3* y = (E4M3*)p.y + row * p.ys;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int at = n * TPR + lane;
       if (at < nvec) {
         if (VEC == 1) {
-          y[at] = e4m3(v[n][0] * inv);
+          y[at] = e4m3(inv.times(v[n][0]));
         } else {
           Pack<uint16_t, (VEC + 1) / 2> q;
 #pragma unroll
-          for (int k = 0; k < VEC / 2; ++k) q.v[k] = e4m3x2(v[n][2 * k] * inv, v[n][(2 * k + 1) % VEC] * inv);
+          for (int k = 0; k < VEC / 2; ++k) {
+            const float2 two = inv.times(make_float2(v[n][2 * k], v[n][(2 * k + 1) % VEC]));
+            q.v[k] = e4m3x2(two.x, two.y);
+          }
           *(Pack<uint16_t, (VEC + 1) / 2>*)(y + (long long)at * VEC) = q;
         }
       }
@@ -217,9 +238,9 @@ __global__ void __launch_bounds__(kBlock) rms_fwd_wide(const RmsParams p) {
     scale = scale_of(row_max<kBlock>(m, (unsigned*)red));
     if (threadIdx.x == 0) p.scales[row] = scale;
   }
-  const float inv = 1.f / scale;
+  const Inverse inv(scale);
   for (int i = threadIdx.x; i < p.width; i += kBlock) {
-    if (EIGHT) ((E4M3*)p.y)[row * p.ys + i] = e4m3(value(i) * inv);
+    if (EIGHT) ((E4M3*)p.y)[row * p.ys + i] = e4m3(inv.times(value(i)));
     else ((T*)p.y)[row * p.ys + i] = from_f<T>(value(i));
   }
 }
