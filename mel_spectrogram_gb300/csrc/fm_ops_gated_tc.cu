@@ -3,6 +3,8 @@
 // gradients of FM_F16 are scaled by powers of two.
 #include <cudaTypedefs.h>
 
+#include <climits>
+
 #include "fm_ops_gated_tc.cuh"
 
 namespace fm {
@@ -55,46 +57,119 @@ __global__ void __launch_bounds__(256) copy_rows(const T* from, long long stride
     for (int c = blockIdx.x * 256 + threadIdx.x; c < cols; c += gridDim.x * 256) to[r * to_stride + c] = from[r * stride + c];
 }
 
-// FM_F16: each row of dh is scaled so that its largest finite magnitude lies in [1, 2):
-// dg and du then keep their precision whatever the gradient's size, unless u itself
-// is far from it. scale[r] = 2^-e; *top = the largest e. A warp a row.
+// FM_F16: dg and du of a row are scaled by a power of two, so that what they can reach at
+// most is just below what f16 holds: no product is lost to infinity that its sum is not,
+// and digits are lost below 2^-24 of that alone. With |dh| < 2^(e + 1) in the row,
+// |u| <= |x| max |w_up| in 2-norms, |act(g)| <= |g| (1: sigmoid) and slopes up to 1.13, both
+// stay below 1.13 * 2^(e + 1 + reach), where the two norms' product is below 2^reach.
+// What is not finite, in dh, x or the weights, does not count: it ends in its own row.
+struct RowSize {
+  short dh;    // the largest |dh| is in 2^dh .. 2^(dh + 1); kLeast for a row of zeros
+  short norm;  // |x| < 2^norm
+};
+struct Loudest {
+  int up, gate;        // bits of the largest squared norm of w_up's and w_gate's rows
+  int by_norm, by_dh;  // largest dh + norm, and dh, of the rows that have a gradient
+  int top;             // largest exponent that any row was scaled down by (see scale_rows)
+};
+constexpr int kNone = -30;  // exponent of a norm of zero: below that of any other
+// the least power of two above the norm, whose square may be off by a thousandth and more for
+// long rows
+__device__ __forceinline__ int norm_exponent(float square) {
+  int e = kNone;
+  if (square > 0.f) frexpf(sqrtf(square) * 1.05f, &e);
+  return e;
+}
+__device__ __forceinline__ int reach(int norm, const Loudest& all, int act, int width) {
+  const int up = norm_exponent(__int_as_float(max(all.up, 0))), gate = norm_exponent(__int_as_float(max(all.gate, 0)));
+  const int most = act == FM_ACT_SIGMOID ? max(norm + up, 0) : norm + max(up, gate);
+  return most + (width >> 20 != 0);  // sums of so many terms may be off by as much as they are
+}
+
+// The largest finite magnitude of a lane's part of a row, and its squares' sum.
 template <int VEC>
-__global__ void __launch_bounds__(256) row_scales(const __half* dh, long long stride, long long rows, int cols,
-                                                  float* scale, int* top) {
-  const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  if (r >= rows) return;
-  const int lane = threadIdx.x % 32;
-  unsigned most = 0;
+__device__ __forceinline__ void measure(const __half* row, int cols, int lane, unsigned& most, float& square) {
+  most = 0, square = 0.f;
 #pragma unroll 4
   for (int c = lane * VEC; c < cols; c += 32 * VEC) {
-    const Pack<__half, VEC> q = *(const Pack<__half, VEC>*)(dh + r * stride + c);
+    const Pack<__half, VEC> q = *(const Pack<__half, VEC>*)(row + c);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       const unsigned v = __half_as_ushort(q.v[k]) & 0x7fffu;
-      if (v < 0x7c00u) most = max(most, v);
+      if (v < 0x7c00u) {
+        const float f = __half2float(q.v[k]);
+        most = max(most, v), square = fmaf(f, f, square);
+      }
     }
   }
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane != 0) return;
-  int e = kLeast;  // also of a row of zeros
-  if (most) frexpf(__half2float(__ushort_as_half((unsigned short)most)), &e), --e;
-  scale[r] = power_of_two(-e);
-  atomicMax(top, e);
 }
-// x times each row's 2^e over the largest, for the product that sums over rows: what
-// falls below FM_F16's range there is 2^-24 of the largest row's terms. A warp a row.
-template <int VEC>
-__global__ void __launch_bounds__(256) scale_rows(const __half* x, long long stride, long long rows, int cols,
-                                                  const float* scale, const int* top, __half* to, long long to_stride) {
-  const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-  if (r >= rows) return;
-  const float f = 1.f / (scale[r] * power_of_two(max(*top, kLeast)));
-#pragma unroll 4
-  for (int c = threadIdx.x % 32 * VEC; c < cols; c += 32 * VEC) {
-    Pack<__half, VEC> q = *(const Pack<__half, VEC>*)(x + r * stride + c);
+// A warp a row of dh and x, and then a warp a row of either weight.
+__global__ void __launch_bounds__(256) row_sizes(const GatedParams p, int vec_dh, int vec_x, RowSize* sizes, Loudest* all) {
+  __shared__ int red[4][8];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const long long n = (long long)blockIdx.x * 8 + warp;
+  int found[4] = {INT_MIN, INT_MIN, INT_MIN, INT_MIN};  // as in Loudest
+  unsigned most;
+  float square;
+  if (n < p.rows) {
+    const __half *dh = (const __half*)p.dh + n * p.dhs, *x = (const __half*)p.x + n * p.xs;
+    if (vec_dh) measure<8>(dh, p.hidden, lane, most, square);
+    else measure<1>(dh, p.hidden, lane, most, square);
+    const unsigned largest = __reduce_max_sync(0xffffffffu, most);
+    if (vec_x) measure<8>(x, p.width, lane, most, square);
+    else measure<1>(x, p.width, lane, most, square);
+    square = warp_sum(square);
+    int e = kLeast;
+    if (largest) frexpf(__half2float(__ushort_as_half((unsigned short)largest)), &e), --e;
+    const int norm = norm_exponent(square);
+    if (lane == 0) sizes[n] = RowSize{(short)e, (short)norm};
+    if (largest) found[2] = e + norm, found[3] = e;
+  } else if (n < p.rows + 2LL * p.hidden) {
+    const long long f = n - p.rows;
+    const bool up = f >= p.hidden;
+    const __half* w = up ? (const __half*)p.wu + (f - p.hidden) * p.us : (const __half*)p.wg + f * p.gs;
+    if (vec_x) measure<8>(w, p.width, lane, most, square);
+    else measure<1>(w, p.width, lane, most, square);
+    found[up ? 0 : 1] = __float_as_int(warp_sum(square));
+  }
+  if (lane == 0)
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) q.v[k] = __float2half_rn(__half2float(q.v[k]) * f);
-    *(Pack<__half, VEC>*)(to + r * to_stride + c) = q;
+    for (int i = 0; i < 4; ++i) red[i][warp] = found[i];
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    int v = INT_MIN;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v = max(v, red[threadIdx.x][w]);
+    if (v != INT_MIN) atomicMax((int*)all + threadIdx.x, v);
+  }
+}
+// What each row of dh is multiplied by. X: and x times each row's 2^-s over the largest, for
+// the product that sums over rows, so that all rows' terms have one scale: what falls below
+// FM_F16's range there is 2^-24 of the largest row's terms. A warp a row.
+template <int VEC, bool X>
+__global__ void __launch_bounds__(256) scale_rows(const GatedParams p, const RowSize* sizes, Loudest* all, float* scale,
+                                                  __half* to, long long to_stride) {
+  const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  if (r >= p.rows) return;
+  const RowSize size = sizes[r];
+  const int s = size.dh + reach(size.norm, *all, p.act, p.width) - 14;
+  if (threadIdx.x % 32 == 0) scale[r] = power_of_two(-s);
+  if constexpr (X) {
+    const int up = norm_exponent(__int_as_float(max(all->up, 0))), gate = norm_exponent(__int_as_float(max(all->gate, 0)));
+    int top = all->by_norm + (p.act == FM_ACT_SIGMOID ? up : max(up, gate));
+    if (p.act == FM_ACT_SIGMOID) top = max(top, all->by_dh);
+    top += (p.width >> 20 != 0) - 14;
+    if (all->by_dh < kLeast) top = 0;  // no row has a gradient
+    if (r == 0 && threadIdx.x == 0) all->top = top;
+    const float f = power_of_two(max(min(s - top, 0), -126));
+    const __half* x = (const __half*)p.x + r * p.xs;
+#pragma unroll 4
+    for (int c = threadIdx.x % 32 * VEC; c < p.width; c += 32 * VEC) {
+      Pack<__half, VEC> q = *(const Pack<__half, VEC>*)(x + c);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) q.v[k] = __float2half_rn(__half2float(q.v[k]) * f);
+      *(Pack<__half, VEC>*)(to + r * to_stride + c) = q;
+    }
   }
 }
 
@@ -180,7 +255,7 @@ fm_status add(const TcArgs& t, int cuts, long long rows, long long split, long l
 
 struct Plan {
   int64_t x, g, u;  // copies of rows, -1 for none
-  int64_t d, scales, top, scaled, parts, total;
+  int64_t d, scales, sizes, all, scaled, parts, total;
   long long stride;  // of copied rows
   int fpad;
 };
@@ -208,7 +283,9 @@ Plan plan_of(const fm_gated_args* a, bool backward) {
     if (a->dtype == FM_F16) {
       w.scales = at;
       at += align256(a->rows * (int64_t)sizeof(float));
-      w.top = at;
+      w.sizes = at;
+      at += align256(a->rows * (int64_t)sizeof(RowSize));
+      w.all = at;
       at += 256;
       w.scaled = at;
       if (a->dw_gate || a->dw_up) at += align256(a->rows * w.stride * 2);
@@ -292,17 +369,16 @@ fm_status gated_tc_backward(const fm_gated_args* a, GatedParams p, cudaStream_t 
   t.d = ws + w.d;
   if (f16) {
     float* scales = (float*)(ws + w.scales);
-    int* top = (int*)(ws + w.top);
-    if (cudaMemsetAsync(top, 0x80, sizeof(int), st) != cudaSuccess) return FM_ERR_CUDA;
-    const unsigned blocks = (unsigned)((p.rows + 7) / 8);
-    auto k = lines(p.dh, p.dhs, p.rows, 2) && p.hidden % 8 == 0 ? row_scales<8> : row_scales<1>;
-    k<<<blocks, 256, 0, st>>>((const __half*)p.dh, p.dhs, p.rows, p.hidden, scales, top);
+    RowSize* sizes = (RowSize*)(ws + w.sizes);
+    Loudest* all = (Loudest*)(ws + w.all);
+    if (cudaMemsetAsync(all, 0x80, sizeof(Loudest), st) != cudaSuccess) return FM_ERR_CUDA;  // below all that is found
+    const bool dw = p.dwg || p.dwu, vec_x = p.width % 8 == 0;  // x and the weights are on the 16-byte grid by now
+    const bool vec_dh = lines(p.dh, p.dhs, p.rows, 2) && p.hidden % 8 == 0;
+    row_sizes<<<(unsigned)((p.rows + 2LL * p.hidden + 7) / 8), 256, 0, st>>>(p, vec_dh, vec_x, sizes, all);
+    auto k = !dw ? scale_rows<1, false> : vec_x ? scale_rows<8, true> : scale_rows<1, true>;
+    k<<<(unsigned)((p.rows + 7) / 8), 256, 0, st>>>(p, sizes, all, scales, (__half*)(ws + w.scaled), w.stride);
     t.row_scale = scales;
-    t.top = top;
-    if (p.dwg || p.dwu) {
-      auto k = p.width % 8 == 0 ? scale_rows<8> : scale_rows<1>;  // x is on the 16-byte grid by now
-      k<<<blocks, 256, 0, st>>>((const __half*)p.x, p.xs, p.rows, p.width, scales, top, (__half*)(ws + w.scaled), w.stride);
-    }
+    t.top = &all->top;
     if (fm_status s = launch_status()) return s;
   }
   int bn = 0;

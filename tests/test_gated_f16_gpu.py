@@ -1,0 +1,89 @@
+"""Gradients of the gated linear layer in f16 where its projections, or its rows, are far from
+one another in size: bounds relative to the terms that each result is the sum of."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import recurrent_reference as ref
+from tests.test_gated_gpu import gen, randn
+
+pytestmark = pytest.mark.gpu
+
+F16 = torch.float16
+U, TINY, E = ref.U[F16], ref.TINY[F16], ref.E
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from mel_spectrogram_gb300 import ops
+
+    return ops
+
+
+def check(ops, x, wg, wu, dh, kind, what):
+    """dx and the weights' gradients: dg and du are rounded to f16 relative to themselves whatever
+    their size, results once more; sums are off by 2 E a term, the activation's slope by the
+    error that this gives g and by its own few roundings (128 E of the terms it is made of)."""
+    leaves = [t.detach().requires_grad_() for t in (x, wg, wu)]
+    got = torch.autograd.grad(ops.gated_linear(*leaves, kind), leaves, dh)
+    X, G, P, D = (t.double() for t in (x, wg, wu, dh))
+    g, p = X @ G.T, X @ P.T
+    K = x.shape[1]
+    eg, ep = (2 * (K + 16) * E * (X.abs() @ W.abs().T) for W in (G, P))
+    a, slope, most, bend = ref.act(g, kind)
+    dg, du = D * p * slope, D * a
+    # a and its slope are no larger than the terms 1 and |g| in any of them
+    es = bend * eg + 128 * E * (1 + g.abs())
+    ea = most * eg + 128 * E * g.abs().clamp(min=float(kind == "sigmoid"))
+    ed = U * dg.abs() + D.abs() * (p.abs() * es + slope.abs() * ep + es * ep)
+    eu = U * du.abs() + D.abs() * ea
+    sums = lambda n: 2 * (n + 16) * E  # noqa: E731
+    F, M = wg.shape[0], x.shape[0]
+    want = dg @ G + du @ P
+    size = dg.abs() @ G.abs() + du.abs() @ P.abs()
+    ref.close(got[0], want, U * want.abs() + ed @ G.abs() + eu @ P.abs() + sums(2 * F) * size + TINY, what + ": dx")
+    for name, t, d, e in (("dw_gate", got[1], dg, ed), ("dw_up", got[2], du, eu)):
+        want = d.T @ X
+        ref.close(t, want, U * want.abs() + e.T @ X.abs() + sums(M) * (d.abs().T @ X.abs()) + TINY, f"{what}: {name}")
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "sigmoid", "relu"])
+@pytest.mark.parametrize("M,K,F", [(40, 64, 72), (300, 63, 130)])
+def test_projections_of_any_size(ops, M, K, F, kind):
+    g = gen(M)
+    x, wg, dh = randn(g, M, K, dtype=F16), randn(g, F, K, scale=K ** -0.5), randn(g, M, F)
+    unit = randn(g, F, K, scale=K ** -0.5)
+    # what w_up gives is beyond what f16 holds, dh and w_gate are small enough for all results
+    check(ops, x, (wg * 2 ** -6).to(F16), (unit * 3e4).to(F16), (dh * 2 ** -10).to(F16), kind, "loud up")
+    check(ops, x, (wg * 2 ** -2).to(F16), (unit * 2 ** -12).to(F16), dh.to(F16), kind, "quiet up")
+    check(ops, (x * 2 ** -4), (wg * 2 ** -6).to(F16), (unit * 2 ** -6).to(F16), dh.to(F16), kind, "quiet all")
+    check(ops, x, wg.to(F16), unit.to(F16), (dh * 2 ** -14).to(F16), kind, "quiet gradients")
+    check(ops, x * 2 ** 8, (wg * 2 ** -8).to(F16), (unit * 2 ** -8).to(F16), (dh * 2 ** -6).to(F16), kind, "loud rows")
+
+
+def test_a_quiet_projection_of_many_rows(ops):
+    # dg of about 2^-21 each, of which the weights' gradient sums 4096 of one sign
+    M, F, g = 4096, 40, gen(1)
+    x, wg, wu = torch.zeros(M, 16), torch.zeros(F, 16), torch.zeros(F, 16)
+    r = lambda *s: torch.rand(*s, generator=torch.Generator().manual_seed(2)) + 1  # noqa: E731
+    x[:, 0], x[:, 1] = 1, r(M) * 2 ** -8
+    wg[:, 0], wu[:, 1] = r(F) - 1.5, r(F) * 2 ** -13
+    dh = r(M, F) / 2
+    x, wg, wu, dh = (t.cuda().to(F16) for t in (x, wg, wu, dh))
+    for kind in ("silu", "sigmoid"):
+        check(ops, x, wg, wu, dh, kind, kind)
+
+
+def test_gradients_that_are_nothing(ops):
+    # rows without a gradient, without inputs, weights of nothing: zeros, and the others as they are
+    g = gen(4)
+    x, wg, wu, dh = (randn(g, *s, dtype=F16, scale=0.3) for s in ((50, 40), (24, 40), (24, 40), (50, 24)))
+    dh[3:20], x[10:30] = 0, 0
+    x[5] *= 2 ** 12
+    for kind in ("silu", "sigmoid"):
+        check(ops, x, wg, wu, dh, kind, "rows")
+        check(ops, x, wg, wu * 0, dh, kind, "no up")
+        check(ops, x, wg * 0, wu, dh, kind, "no gate")
+        check(ops, x, wg, wu, dh * 0, kind, "no gradient")
+        check(ops, x * 0, wg, wu, dh, kind, "no input")
