@@ -259,9 +259,9 @@ fm_status fm_rows_8bit(const fm_rows_8bit_args* args, fm_stream_t stream);
  *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
  * Products of 16-bit inputs are summed in 32 bits; dg and du are rounded to dtype
  * for the second products (FM_F16: each row's scaled by a power of two before, so that
- * what they can reach at most is just below what the type holds, which is taken out of
- * the results again: neither becomes infinite where dx, dw_gate or dw_up would not, and
- * both keep their digits where they are small).
+ * what they can reach at most is just below what the type holds, and for the weights'
+ * gradients x alike, which is taken out of the results again: nothing becomes infinite
+ * where dx, dw_gate or dw_up would not, and small rows and projections keep their digits).
  *
  * In 8 bits (in_dtype FM_E4M3, forward only) x, w_gate and w_up are FM_E4M3 values with
  * a scale a row, as fm_rms_norm_forward and fm_rows_8bit write them:

@@ -64,13 +64,13 @@ __global__ void __launch_bounds__(256) copy_rows(const T* from, long long stride
 // stay below 1.13 * 2^(e + 1 + reach), where the two norms' product is below 2^reach.
 // What is not finite, in dh, x or the weights, does not count: it ends in its own row.
 struct RowSize {
-  short dh;    // the largest |dh| is in 2^dh .. 2^(dh + 1); kLeast for a row of zeros
-  short norm;  // |x| < 2^norm
+  short dh, x;  // the largest |dh| is in 2^dh .. 2^(dh + 1), |x| alike; kLeast for a row of zeros
+  short norm;   // |x| in the 2-norm is below 2^norm
 };
 struct Loudest {
   int up, gate;        // bits of the largest squared norm of w_up's and w_gate's rows
-  int by_norm, by_dh;  // largest dh + norm, and dh, of the rows that have a gradient
-  int top;             // largest exponent that any row was scaled down by (see scale_rows)
+  int by_norm, by_x;   // largest dh + x + norm, and dh + x, of the rows that have both
+  int scaled;          // exponent that the weights' gradients are multiplied by (see scale_rows)
 };
 constexpr int kNone = -30;  // exponent of a norm of zero: below that of any other
 // the least power of two above the norm, whose square may be off by a thousandth and more for
@@ -115,15 +115,18 @@ __global__ void __launch_bounds__(256) row_sizes(const GatedParams p, int vec_dh
     const __half *dh = (const __half*)p.dh + n * p.dhs, *x = (const __half*)p.x + n * p.xs;
     if (vec_dh) measure<8>(dh, p.hidden, lane, most, square);
     else measure<1>(dh, p.hidden, lane, most, square);
-    const unsigned largest = __reduce_max_sync(0xffffffffu, most);
+    const unsigned of_dh = __reduce_max_sync(0xffffffffu, most);
     if (vec_x) measure<8>(x, p.width, lane, most, square);
     else measure<1>(x, p.width, lane, most, square);
-    square = warp_sum(square);
-    int e = kLeast;
-    if (largest) frexpf(__half2float(__ushort_as_half((unsigned short)largest)), &e), --e;
-    const int norm = norm_exponent(square);
-    if (lane == 0) sizes[n] = RowSize{(short)e, (short)norm};
-    if (largest) found[2] = e + norm, found[3] = e;
+    const unsigned of_x = __reduce_max_sync(0xffffffffu, most);
+    auto exponent = [](unsigned largest) {
+      int e = kLeast + 1;
+      if (largest) frexpf(__half2float(__ushort_as_half((unsigned short)largest)), &e);
+      return e - 1;
+    };
+    const int e = exponent(of_dh), ex = exponent(of_x), norm = norm_exponent(warp_sum(square));
+    if (lane == 0) sizes[n] = RowSize{(short)e, (short)ex, (short)norm};
+    if (of_dh && of_x) found[2] = e + ex + norm, found[3] = e + ex;
   } else if (n < p.rows + 2LL * p.hidden) {
     const long long f = n - p.rows;
     const bool up = f >= p.hidden;
@@ -143,25 +146,30 @@ __global__ void __launch_bounds__(256) row_sizes(const GatedParams p, int vec_dh
     if (v != INT_MIN) atomicMax((int*)all + threadIdx.x, v);
   }
 }
-// What each row of dh is multiplied by. X: and x times each row's 2^-s over the largest, for
-// the product that sums over rows, so that all rows' terms have one scale: what falls below
-// FM_F16's range there is 2^-24 of the largest row's terms. A warp a row.
+// What each row of dh is multiplied by. X: and x, for the product that sums over rows, so that
+// all rows' terms have one scale. The rows with the largest terms have both factors' largest
+// at 2^14; what another's terms are smaller by, the two share (x takes the first 2^6): terms
+// keep their digits, relative to their own row's largest, to 2^-(36 - n / 2) where that is
+// 2^-n of the largest of all. On x alone, from 1 on, 2^-24 below the largest row
+// nothing would be left, also in columns to which only the small ones add. A warp a row.
 template <int VEC, bool X>
 __global__ void __launch_bounds__(256) scale_rows(const GatedParams p, const RowSize* sizes, Loudest* all, float* scale,
                                                   __half* to, long long to_stride) {
   const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   if (r >= p.rows) return;
   const RowSize size = sizes[r];
-  const int s = size.dh + reach(size.norm, *all, p.act, p.width) - 14;
-  if (threadIdx.x % 32 == 0) scale[r] = power_of_two(-s);
+  int s = size.dh + reach(size.norm, *all, p.act, p.width) - 14;
   if constexpr (X) {
+    // the largest of s + x over the rows that have terms: reach() by parts
     const int up = norm_exponent(__int_as_float(max(all->up, 0))), gate = norm_exponent(__int_as_float(max(all->gate, 0)));
     int top = all->by_norm + (p.act == FM_ACT_SIGMOID ? up : max(up, gate));
-    if (p.act == FM_ACT_SIGMOID) top = max(top, all->by_dh);
+    if (p.act == FM_ACT_SIGMOID) top = max(top, all->by_x);
     top += (p.width >> 20 != 0) - 14;
-    if (all->by_dh < kLeast) top = 0;  // no row has a gradient
-    if (r == 0 && threadIdx.x == 0) all->top = top;
-    const float f = power_of_two(max(min(s - top, 0), -126));
+    if (all->by_x < 2 * kLeast) top = 0;  // there are none
+    if (r == 0 && threadIdx.x == 0) all->scaled = top - 14;
+    const int below = max(top - s - size.x, 0), down = max(below - 6, 0) / 2;
+    s += down;
+    const float f = power_of_two(max(14 - size.x - (below - down), -126));
     const __half* x = (const __half*)p.x + r * p.xs;
 #pragma unroll 4
     for (int c = threadIdx.x % 32 * VEC; c < p.width; c += 32 * VEC) {
@@ -171,6 +179,7 @@ __global__ void __launch_bounds__(256) scale_rows(const GatedParams p, const Row
       *(Pack<__half, VEC>*)(to + r * to_stride + c) = q;
     }
   }
+  if (threadIdx.x % 32 == 0) scale[r] = power_of_two(max(-s, -126));
 }
 
 dim3 copy_grid(long long rows, int cols) {
@@ -378,7 +387,7 @@ fm_status gated_tc_backward(const fm_gated_args* a, GatedParams p, cudaStream_t 
     auto k = !dw ? scale_rows<1, false> : vec_x ? scale_rows<8, true> : scale_rows<1, true>;
     k<<<(unsigned)((p.rows + 7) / 8), 256, 0, st>>>(p, sizes, all, scales, (__half*)(ws + w.scaled), w.stride);
     t.row_scale = scales;
-    t.top = &all->top;
+    t.scaled = &all->scaled;
     if (fm_status s = launch_status()) return s;
   }
   int bn = 0;

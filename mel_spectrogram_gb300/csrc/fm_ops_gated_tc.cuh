@@ -52,7 +52,7 @@ struct TcArgs {
   int fpad;         // hidden units rounded up to whole steps of 64: du's place in a row of D
   void* d;          // [rows][2 * fpad]
   const float* row_scale;  // FM_F16: what each row of dh is multiplied by
-  const int* top;          // FM_F16: exponent that the weights' gradients are multiplied by
+  const int* scaled;       // FM_F16: exponent that the weights' gradients are multiplied by
   int vec_out, vec_dh;     // whether rows of the result (of dh) allow 16-byte accesses
 };
 
@@ -588,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<OP, BN>, 1)
         constexpr int kLd = kOnce < 32 ? kOnce : 32;
         float scale = 1.f;
         if (OP == kDx && t.row_scale && r < p.rows) scale = 1.f / t.row_scale[r];
-        if (OP == kDw && t.top) scale = power_of_two(min(max(*t.top, -126), 126));
+        if (OP == kDw && t.scaled) scale = power_of_two(min(max(*t.scaled, -126), 126));
         ok = bar_wait(sums_full(buffer), turn, &dead, t.err);
         if (!ok) break;
         fence_after();

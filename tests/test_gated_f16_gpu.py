@@ -87,3 +87,21 @@ def test_gradients_that_are_nothing(ops):
         check(ops, x, wg * 0, wu, dh, kind, "no gate")
         check(ops, x, wg, wu, dh * 0, kind, "no gradient")
         check(ops, x * 0, wg, wu, dh, kind, "no input")
+
+
+@pytest.mark.parametrize("far", [2.0 ** 8, 2.0 ** 16, 2.0 ** 22])
+def test_what_only_quiet_rows_hold(ops, far):
+    # columns of x that are 0 in the rows with the large gradients: their sums keep their digits
+    M, K, F, g = 200, 72, 64, gen(7)
+    x, wg, wu = randn(g, M, K, dtype=F16), randn(g, F, K, dtype=F16, scale=0.1), randn(g, F, K, dtype=F16, scale=0.1)
+    dh = randn(g, M, F)
+    quiet = torch.arange(M, device="cuda") % 4 != 0
+    dh = (torch.where(quiet[:, None], dh, dh * far) * 2.0 ** -11).to(F16)
+    x[:, ::3] *= torch.where(quiet, 0.05, 0.0).to(F16)[:, None]
+    x[:, 1::3] *= torch.where(quiet, 0.0, 1.0).to(F16)[:, None]
+    for kind in ("silu", "sigmoid"):
+        check(ops, x, wg, wu, dh, kind, kind)
+    # sizes of x that undo those of the gradients, and ones that add to them
+    size = torch.where(quiet, 1.0, far ** -0.5).to(F16)[:, None]
+    check(ops, x * size, wg, wu, dh, "silu", "undone")
+    check(ops, x * size.flip(0), wg, wu, dh, "silu", "other rows")
