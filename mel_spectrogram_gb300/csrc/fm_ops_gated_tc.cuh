@@ -263,8 +263,9 @@ __device__ __forceinline__ float2 sigmoids(float2 g) {
 }
 // The normal distribution's integral up to g, and e = exp(-g^2 / 2): of |g| from 1, or of
 // g itself, erfc(|g| / sqrt 2) / 2 = e t P(t) with t = 1 / (1 + 0.304 |g|); P of degree 7
-// fitted for the least relative error up to |g| = 14 (8e-8), so that the tail that gelu
-// multiplies by a large g keeps its digits.
+// fitted for the least relative error up to |g| = 14 (1.4e-7), so that the tail that gelu
+// multiplies by a large g keeps its digits. The exponent's three roundings add up to
+// 9e-8 g^2, 2e-5 at 14, to e's.
 __device__ __forceinline__ float2 normal_integrals(float2 g, float2& e) {
   constexpr float c[8] = {0.12126036f, 0.122141108f, 0.102763310f, 0.122487135f, -0.0411235951f, 0.189988881f,
                           -0.154114947f, 0.0365977213f};
