@@ -254,7 +254,7 @@ __device__ __forceinline__ float2 after(float2 A, float2 h, float2 B) {
   const float2 r = fma2(A, h, B);
   return CUTS ? make_float2(cut<CUTS>(A.x) ? B.x : r.x, cut<CUTS>(A.y) ? B.y : r.y) : r;
 }
-// the factor of two stretches: a cut in either stays one, also beside a NaN
+// the product of two factors: a cut in either stays one, also beside a NaN
 __device__ __forceinline__ float with_cut(float p, float A, float f) {
   return __uint_as_float((__float_as_uint(p) & 0x7fffffffu) | ((__float_as_uint(A) | __float_as_uint(f)) & 0x80000000u));
 }
@@ -262,6 +262,21 @@ template <bool CUTS>
 __device__ __forceinline__ float2 both(float2 A, float2 f) {
   const float2 p = mul2(A, f);
   return CUTS ? make_float2(with_cut(p.x, A.x, f.x), with_cut(p.y, A.y, f.y)) : p;
+}
+// A stretch's factor is never 0, however long the stretch: it stays at the smallest float, so
+// that what came before and is infinite stays infinite.
+template <bool CUTS>
+__device__ __forceinline__ float2 above_zero(float2 A) {
+  float2 r = A;
+  if (CUTS) r = make_float2(fabsf(A.x), fabsf(A.y));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(r.x) : "f"(1.4e-45f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(r.y) : "f"(1.4e-45f));
+  return CUTS ? make_float2(with_cut(r.x, A.x, 0.f), with_cut(r.y, A.y, 0.f)) : r;
+}
+// the factor of two stretches
+template <bool CUTS>
+__device__ __forceinline__ float2 joined(float2 A, float2 f) {
+  return above_zero<CUTS>(both<CUTS>(A, f));
 }
 __device__ __forceinline__ float2 shfl_up2(float2 v, int d) {
   return make_float2(__shfl_up_sync(0xffffffffu, v.x, d), __shfl_up_sync(0xffffffffu, v.y, d));
@@ -512,13 +527,14 @@ __global__ void __launch_bounds__(kThreads, 4) forward(const ScanParams p) {
         }
       }
     }
+    A = above_zero<CUTS>(A);
     // of the segments up to this one in the warp
 #pragma unroll
     for (int d = 1; d < SEGW; d *= 2) {
       const float2 a0 = shfl_up2(A, d * LS), b0 = shfl_up2(B, d * LS);
       if (lane >= d * LS) {
         B = after<CUTS>(A, b0, B);
-        A = both<CUTS>(A, a0);
+        A = joined<CUTS>(A, a0);
       }
     }
     if (lane >= 32 - LS) m.warps[warp][pair] = quad(A, B);
@@ -540,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 4) forward(const ScanParams p) {
         if (w == warp) a1 = a, s1 = s;
         const float4 q = m.warps[w][pair];
         s = after<CUTS>(first_of(q), s, second_of(q));
-        a = both<CUTS>(first_of(q), a);
+        a = joined<CUTS>(first_of(q), a);
       }
       h = between_blocks<CUTS, false, LS>(m, p, ranks, rank, lane, warp, round, a, s, carry);
       if (warp > 0) h = after<CUTS>(a1, h, s1);
@@ -699,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 4) backward(const ScanParams p) {
         if (CUTS && (fresh >> i & 1)) R = tc::both(0.f);
       }
     }
+    A = above_zero<CUTS>(A);
     m.segs[seg][pair] = quad(A, B);
     // of the segments from this one on in the warp
 #pragma unroll
@@ -706,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 4) backward(const ScanParams p) {
       const float2 a0 = shfl_down2(A, d * LS), r0 = shfl_down2(R, d * LS);
       if (lane + d * LS < 32) {
         R = after<CUTS>(A, r0, R);
-        A = both<CUTS>(A, a0);
+        A = joined<CUTS>(A, a0);
       }
     }
     if (lane < LS) m.warps[warp][pair] = quad(A, R);
@@ -724,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 4) backward(const ScanParams p) {
         if (w == warp) a1 = a, s1 = s;
         const float4 q = m.warps[w][pair];
         s = after<CUTS>(first_of(q), s, second_of(q));
-        a = both<CUTS>(first_of(q), a);
+        a = joined<CUTS>(first_of(q), a);
       }
       float2 from = between_blocks<CUTS, true, LS>(m, p, ranks, rank, lane, warp, round, a, s, carry);
       if (warp < kWarps - 1) from = after<CUTS>(a1, from, s1);
@@ -852,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 4) stretch_sums(const ScanParams p) 
       }
     }
   }
-  segs[seg][pair] = quad(A, B);
+  segs[seg][pair] = quad(above_zero<CUTS>(A), B);
   __syncthreads();
   A = tc::both(1.f), B = tc::both(0.f);
   if (seg == 0) {
@@ -860,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 4) stretch_sums(const ScanParams p) 
     for (int i = 0; i < kSegs; ++i) {
       const float4 q = segs[BACKWARD ? kSegs - 1 - i : i][pair];
       B = after<CUTS>(first_of(q), B, second_of(q));
-      A = both<CUTS>(first_of(q), A);
+      A = joined<CUTS>(first_of(q), A);
     }
     total[pair] = quad(A, B);
   }
@@ -870,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 4) stretch_sums(const ScanParams p) 
     for (int i = 0; i < ranks; ++i) {
       const float4 q = *cluster.map_shared_rank(&total[pair], BACKWARD ? ranks - 1 - i : i);
       B = after<CUTS>(first_of(q), B, second_of(q));
-      A = both<CUTS>(first_of(q), A);
+      A = joined<CUTS>(first_of(q), A);
     }
     float2* to = p.sums + (stretch + 1) * p.batch * p.channels + at;
     if (have > 0) to[0] = make_float2(A.x, B.x);
