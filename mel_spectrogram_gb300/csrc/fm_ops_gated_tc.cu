@@ -63,9 +63,11 @@ __global__ void __launch_bounds__(256) copy_rows(const T* from, long long stride
 // |u| <= |x| max |w_up| in 2-norms, |act(g)| <= |g| (1: sigmoid) and slopes up to 1.13, both
 // stay below 1.13 * 2^(e + 1 + reach), where the two norms' product is below 2^reach.
 // What is not finite, in dh, x or the weights, does not count: it ends in its own row.
+// 24008 rows of 1024 to 4096: 41 us, memory bound (263 MB), and scale_rows 16.
 struct RowSize {
   short dh, x;  // the largest |dh| is in 2^dh .. 2^(dh + 1), |x| alike; kLeast for a row of zeros
   short norm;   // |x| in the 2-norm is below 2^norm
+  short down;   // for the weights' gradients D's row is 2^-down of what it is for dx
 };
 struct Loudest {
   int up, gate;        // bits of the largest squared norm of w_up's and w_gate's rows
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(256) row_sizes(const GatedParams p, int vec_dh
       return e - 1;
     };
     const int e = exponent(of_dh), ex = exponent(of_x), norm = norm_exponent(warp_sum(square));
-    if (lane == 0) sizes[n] = RowSize{(short)e, (short)ex, (short)norm};
+    if (lane == 0) sizes[n] = RowSize{(short)e, (short)ex, (short)norm, 0};
     if (of_dh && of_x) found[2] = e + ex + norm, found[3] = e + ex;
   } else if (n < p.rows + 2LL * p.hidden) {
     const long long f = n - p.rows;
@@ -148,17 +150,17 @@ __global__ void __launch_bounds__(256) row_sizes(const GatedParams p, int vec_dh
 }
 // What each row of dh is multiplied by. X: and x, for the product that sums over rows, so that
 // all rows' terms have one scale. The rows with the largest terms have both factors' largest
-// at 2^14; what another's terms are smaller by, the two share (x takes the first 2^6): terms
-// keep their digits, relative to their own row's largest, to 2^-(36 - n / 2) where that is
-// 2^-n of the largest of all. On x alone, from 1 on, 2^-24 below the largest row
+// at 2^14; what another's terms are smaller by, x takes up to 2^14 of, and the two share the
+// rest: terms keep their digits, relative to their own row's largest, to 2^-(32 - n / 2) where
+// that is 2^-n of the largest of all. On x alone, from 1 on, 2^-24 below the largest row
 // nothing would be left, also in columns to which only the small ones add. A warp a row.
 template <int VEC, bool X>
-__global__ void __launch_bounds__(256) scale_rows(const GatedParams p, const RowSize* sizes, Loudest* all, float* scale,
+__global__ void __launch_bounds__(256) scale_rows(const GatedParams p, RowSize* sizes, Loudest* all, float* scale,
                                                   __half* to, long long to_stride) {
   const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
   if (r >= p.rows) return;
   const RowSize size = sizes[r];
-  int s = size.dh + reach(size.norm, *all, p.act, p.width) - 14;
+  const int s = size.dh + reach(size.norm, *all, p.act, p.width) - 14;
   if constexpr (X) {
     // the largest of s + x over the rows that have terms: reach() by parts
     const int up = norm_exponent(__int_as_float(max(all->up, 0))), gate = norm_exponent(__int_as_float(max(all->gate, 0)));
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(256) scale_rows(const GatedParams p, const Row
     top += (p.width >> 20 != 0) - 14;
     if (all->by_x < 2 * kLeast) top = 0;  // there are none
     if (r == 0 && threadIdx.x == 0) all->scaled = top - 14;
-    const int below = max(top - s - size.x, 0), down = max(below - 6, 0) / 2;
-    s += down;
+    const int below = max(top - s - size.x, 0), down = max(below - 14, 0) / 2;
+    if (threadIdx.x % 32 == 0) sizes[r].down = (short)down;
     const float f = power_of_two(max(14 - size.x - (below - down), -126));
     const __half* x = (const __half*)p.x + r * p.xs;
 #pragma unroll 4
@@ -179,7 +181,21 @@ __global__ void __launch_bounds__(256) scale_rows(const GatedParams p, const Row
       *(Pack<__half, VEC>*)(to + r * to_stride + c) = q;
     }
   }
-  if (threadIdx.x % 32 == 0) scale[r] = power_of_two(max(-s, -126));
+  if (threadIdx.x % 32 == 0) scale[r] = power_of_two(-s);
+}
+// D's rows that are far below the largest, after dx, which asks nothing of other rows. Where
+// none is, this reads the sizes alone. A warp a row.
+__global__ void __launch_bounds__(256) lower_rows(const RowSize* sizes, long long rows, __half* d, long long ld) {
+  const long long r = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+  const int down = r < rows ? sizes[r].down : 0;
+  if (down == 0) return;
+  const float f = power_of_two(max(-down, -126));
+  for (long long c = threadIdx.x % 32 * 8; c < ld; c += 32 * 8) {
+    Pack<__half, 8> q = *(const Pack<__half, 8>*)(d + r * ld + c);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q.v[k] = __float2half_rn(__half2float(q.v[k]) * f);
+    *(Pack<__half, 8>*)(d + r * ld + c) = q;
+  }
 }
 
 dim3 copy_grid(long long rows, int cols) {
@@ -418,6 +434,10 @@ fm_status gated_tc_backward(const fm_gated_args* a, GatedParams p, cudaStream_t 
     }
   }
   if (p.dwg || p.dwu) {
+    if (f16) {
+      lower_rows<<<(unsigned)((p.rows + 7) / 8), 256, 0, st>>>((const RowSize*)(ws + w.sizes), p.rows, (__half*)t.d, ld);
+      if (fm_status s = launch_status()) return s;
+    }
     set(sums.w, (int)((p.rows + 63) / 64));
     t.vec_out = t.parts ? p.width % 4 == 0
                         : (!p.dwg || lines(p.dwg, p.dgs, p.hidden, 2)) && (!p.dwu || lines(p.dwu, p.dus, p.hidden, 2));

@@ -105,3 +105,19 @@ def test_what_only_quiet_rows_hold(ops, far):
     size = torch.where(quiet, 1.0, far ** -0.5).to(F16)[:, None]
     check(ops, x * size, wg, wu, dh, "silu", "undone")
     check(ops, x * size.flip(0), wg, wu, dh, "silu", "other rows")
+
+
+def test_loud_rows_change_no_bit_of_others_dx(ops):
+    M, K, F, g = 150, 72, 130, gen(8)
+    x, wg, wu = randn(g, M, K, dtype=F16), randn(g, F, K, dtype=F16, scale=0.1), randn(g, F, K, dtype=F16, scale=0.1)
+    dh = randn(g, M, F, dtype=F16, scale=2.0 ** -11)
+    dh[5] *= torch.logspace(0, -4, F, device="cuda").to(F16)
+    rest = torch.arange(M, device="cuda") != 3
+    got = []
+    for loud in (1.0, 2.0 ** 13, 2.0 ** 24):
+        a, d = x.clone(), dh.clone()
+        a[3] *= min(loud, 2.0 ** 8)
+        d[3] = (d[3].float() * min(loud, 2.0 ** 22)).to(F16)
+        leaves = [t.requires_grad_() for t in (a, wg.clone(), wu.clone())]
+        got.append(torch.autograd.grad(ops.gated_linear(*leaves), leaves, d)[0][rest])
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
