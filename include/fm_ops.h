@@ -193,7 +193,8 @@ int64_t fm_attention_workspace(const fm_attention_args* args, int backward);
  *   y     = total * rstd * weight,  rstd = 1 / sqrt(mean(total^2) + eps)
  * of each row. In 8 bits (y_dtype FM_E4M3) a row has one scale:
  *   scale = max(max |y| / 448, 2^-126),  values = y / scale rounded to FM_E4M3
- * from the unrounded y; a row with an infinity or NaN gets a scale of NaN.
+ * from the unrounded y; a row with an infinity or NaN gets a scale of NaN. The mean of
+ * squares is 32-bit: magnitudes beyond 1e18 overflow it, those below 1e-18 vanish in it.
  *
  * Backward: with n = total * rstd and h = dy * weight,
  *   dx = dtotal + rstd * (h - n * mean(h n)),  dweight = sum of dy * n

@@ -10,7 +10,7 @@
 // Where those two have fewer tiles than SMs, each tile's sum is cut into stretches, whose
 // results another kernel adds up in order: dx of 258 rows, 256 to 1024, went through 128
 // steps in 20 blocks otherwise, 90 of the 174 us that the whole step took. Bound by the
-// FP32 pipes and what feeds them: 2048 rows, 512 to 2048 forward 230 us, 37 TFLOP/s.
+// FP32 pipes and what feeds them: 2048 rows, 512 to 2048 forward 235 us, 36 TFLOP/s.
 #include <type_traits>
 
 #include "fm_ops_gated.cuh"

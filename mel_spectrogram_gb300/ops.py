@@ -125,7 +125,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torc
     stream that the next addition takes. x, residual: (..., width) float32,
     float16 or bfloat16, both the same, any strides (rows whose elements are not
     adjacent are copied first). weight: (width,), of x's type or float32, or None
-    for ones. The mean of squares is 32-bit (magnitudes beyond 1e18 overflow it).
+    for ones. The mean of squares is 32-bit (magnitudes beyond 1e18
+    overflow it, those below 1e-18 vanish in it: with an eps of 0 their norm is infinite).
     Differentiable in x, weight and residual (once); total's own gradient is added
     in the same pass.
     """
