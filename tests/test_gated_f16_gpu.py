@@ -121,3 +121,18 @@ def test_loud_rows_change_no_bit_of_others_dx(ops):
         leaves = [t.requires_grad_() for t in (a, wg.clone(), wu.clone())]
         got.append(torch.autograd.grad(ops.gated_linear(*leaves), leaves, d)[0][rest])
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("K", [64, 1 << 21])
+def test_projections_that_reach_their_bound(ops, K):
+    # x and w_up along one line, so that u is the product of their norms; the largest gradients
+    # and slopes of a row beside it
+    M, F, g = 40, 8, gen(9)
+    line = torch.where(torch.rand(K, device="cuda", generator=g) < 0.5, -1.0, 1.0)
+    x = (line * torch.exp2(-6 - torch.arange(M, device="cuda") % 3)[:, None]).to(F16)
+    wu = (line * 2.0 ** -4).expand(F, K).to(F16)
+    wg = (line * 2.0 ** 7 / K).expand(F, K).to(F16)
+    dh = torch.full((M, F), 1.998, device="cuda", dtype=F16)
+    dh[:, 1::2] = -1.0
+    for kind in ("silu", "gelu", "relu", "sigmoid"):
+        check(ops, x, wg, wu, dh, kind, kind)
